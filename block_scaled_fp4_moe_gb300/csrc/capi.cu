@@ -16,6 +16,10 @@ std::atomic<int> g_sms[64];
 
 __global__ void set_word_kernel(uint32_t *p, uint32_t v) { *p = v; }
 
+}  // namespace
+
+namespace moe {
+
 // Streaming-multiprocessor count of the current device; rejects devices the
 // library was not built for.
 moe_status_t current_device_sms(int *sms) {
@@ -38,6 +42,10 @@ moe_status_t current_device_sms(int *sms) {
     *sms = n;
     return MOE_OK;
 }
+
+}  // namespace moe
+
+namespace {
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 

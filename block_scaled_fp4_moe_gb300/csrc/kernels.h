@@ -42,6 +42,10 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Streaming-multiprocessor count of the current device; rejects devices the
+// library was not built for (capi.cu).
+moe_status_t current_device_sms(int *sms);
+
 // static shared memory of the grouping code (two int arrays of kMaxExperts)
 constexpr size_t kGroupStaticSmem = 2 * kMaxExperts * sizeof(int) + 64;
 

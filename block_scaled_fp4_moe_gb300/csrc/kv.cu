@@ -1,0 +1,308 @@
+// kv.cu -- the paged E4M3 cache's bookkeeping: block tables and slot maps from
+// request lengths, and the append of new keys and values.
+#include "attn.h"
+
+namespace moe {
+namespace {
+
+constexpr int kTablesThreads = 512;
+
+// Inclusive sum over the block of a pair of 64-bit counts; *total is the
+// block's sum.  red: 2 * 32 words of shared memory.
+__device__ __forceinline__ ulonglong2 block_scan2(ulonglong2 v, ulonglong2 *red, ulonglong2 *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const unsigned long long a = __shfl_up_sync(0xffffffffu, v.x, d), b = __shfl_up_sync(0xffffffffu, v.y, d);
+        if (lane >= d) {
+            v.x += a;
+            v.y += b;
+        }
+    }
+    if (lane == 31)
+        red[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+        ulonglong2 w = lane < nw ? red[lane] : make_ulonglong2(0, 0);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const unsigned long long a = __shfl_up_sync(0xffffffffu, w.x, d), b = __shfl_up_sync(0xffffffffu, w.y, d);
+            if (lane >= d) {
+                w.x += a;
+                w.y += b;
+            }
+        }
+        red[lane] = w;
+    }
+    __syncthreads();
+    if (warp > 0) {
+        v.x += red[warp - 1].x;
+        v.y += red[warp - 1].y;
+    }
+    *total = red[nw - 1];
+    return v;
+}
+
+// Tables of a step.  Every CTA sums the B requests' new tokens and new blocks
+// itself (8 B bytes from L2, one block-wide scan: cheaper than a second
+// launch or a wait between CTAs) and so agrees on the checks; then each
+// thread finds its token's request by bisection in shared memory and derives
+// block, slot and position.  A token at a block boundary writes the block's
+// table entry: every block that a step adds holds one such token.  Bound by
+// latency: one chain of length loads, scan, bisection, free-list load.
+__global__ void __launch_bounds__(kTablesThreads) kv_tables_kernel(TablesProblem p) {
+    extern __shared__ int32_t sm[];
+    __shared__ ulonglong2 red[32];
+    int32_t *s_ctx = sm, *s_off = sm + p.B, *s_blk = s_off + p.B + 1;   // cached tokens, first token, first new block
+    pdl_wait();
+    pdl_trigger();
+    const int tid = threadIdx.x, sh = p.block_shift, bs = 1 << sh;
+    const long long cap = (long long)p.max_blocks << sh;
+    const int per = (p.B + kTablesThreads - 1) / kTablesThreads;
+    const int head = *p.free_head;
+    int bad = head < 0;
+    for (int b = tid; b < p.B; b += kTablesThreads) {
+        const int c = p.ctx[b], n = p.fresh[b];
+        bad |= c < 0 || n < 0 || (long long)c + n > cap;
+        s_ctx[b] = c;
+        s_off[b] = n;
+    }
+    if (__syncthreads_or(bad)) {
+        if (blockIdx.x == 0 && tid == 0)
+            record_status(p.hdr, MOE_ERR_DEVICE_ASSERT);
+        return;
+    }
+    // held and new blocks; lengths are at most max_blocks * block_size < 2^31
+    auto before = [&](int c) { return (int)(((long long)c + bs - 1) >> sh); };
+    auto made = [&](int c, int n) { return (int)(((long long)c + n + bs - 1) >> sh) - before(c); };
+    const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    ulonglong2 mine = make_ulonglong2(0, 0), total;
+    for (int b = b0; b < b1; ++b) {
+        mine.x += s_off[b];
+        mine.y += made(s_ctx[b], s_off[b]);
+    }
+    const ulonglong2 incl = block_scan2(mine, red, &total);
+    if (total.x > (unsigned long long)p.T || (unsigned long long)head + total.y > (unsigned long long)p.num_free) {
+        if (blockIdx.x == 0 && tid == 0)
+            record_status(p.hdr, MOE_ERR_DEVICE_ASSERT);
+        return;
+    }
+    int off = (int)(incl.x - mine.x), blk = (int)(incl.y - mine.y);
+    for (int b = b0; b < b1; ++b) {
+        const int n = s_off[b];
+        s_off[b] = off;
+        s_blk[b] = blk;
+        off += n;
+        blk += made(s_ctx[b], n);
+    }
+    const int n_tok = (int)total.x;
+    if (tid == 0)
+        s_off[p.B] = n_tok;
+    __syncthreads();
+    const int stride = gridDim.x * kTablesThreads;
+    for (int b = blockIdx.x * kTablesThreads + tid; b <= p.B; b += stride) {
+        p.q_offsets[b] = s_off[b];
+        if (b < p.B)
+            p.kv_lens[b] = s_ctx[b] + s_off[b + 1] - s_off[b];
+        else
+            *p.free_head_out = head + (int)total.y;
+    }
+    for (int t = blockIdx.x * kTablesThreads + tid; t < p.T; t += stride) {
+        if (t >= n_tok) {
+            p.slot_map[t] = -1;
+            p.positions[t] = -1;
+            continue;
+        }
+        int lo = 0, hi = p.B;                    // s_off[lo] <= t < s_off[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_off[mid] <= t)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        const int c = s_ctx[lo], pos = c + t - s_off[lo], idx = pos >> sh, held = before(c);
+        int32_t *entry = p.table + (size_t)lo * p.max_blocks + idx;
+        int id;
+        if (idx < held) {
+            id = *entry;
+        } else {
+            id = p.free_blocks[head + s_blk[lo] + idx - held];
+            if ((pos & (bs - 1)) == 0)
+                *entry = id;
+        }
+        p.slot_map[t] = ((int64_t)id << sh) + (pos & (bs - 1));
+        p.positions[t] = pos;
+    }
+}
+
+// ----------------------------------------------------------------- append
+
+constexpr int kAppendThreads = 128;
+
+// One CTA owns a (block, head) of the keys (blockIdx.z = 0) or values (1): it
+// holds the new tokens of the block in registers (at most 128 x 128 bf16 =
+// 16 x 16 bytes a thread), takes their largest magnitude, settles the exponent,
+// re-rounds the codes that the block held where the exponent grew, and
+// writes the new codes: one pass over the input, no atomics.  A CTA looks at
+// `window` consecutive tokens and works for those that begin a run of tokens in one
+// block (a run may reach past the window); the launcher's window is 1 while
+// T tokens x heads x 2 fill the GPU few times over (a CTA then has one
+// short job) and 16 for prompts, where most tokens begin nothing.
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendProblem p, int window) {
+    constexpr int kLanes = D / 8;                       // threads per token (16 bytes each)
+    constexpr int kTok = kAppendThreads / kLanes;       // tokens per step
+    constexpr int kSteps = 128 / kTok;
+    __shared__ __align__(16) uint8_t s_code[128 * D];   // values: codes [token][dim] before the transpose
+    __shared__ uint32_t s_max[kAppendThreads / 32];
+    __shared__ int s_len;
+    pdl_wait();
+    pdl_trigger();
+    const int tid = threadIdx.x, h = blockIdx.y;
+    const bool is_v = blockIdx.z != 0;
+    const int bs = p.cache.block_size, sh = 31 - __clz(bs);
+    const uint16_t *src = (is_v ? p.v + h * p.v_sh : p.k + h * p.k_sh);
+    const int64_t st = is_v ? p.v_st : p.k_st;
+    const int64_t n_slots = (int64_t)p.cache.num_blocks << sh;
+    const int t_end = min(p.T, ((int)blockIdx.x + 1) * window);
+    for (int t = blockIdx.x * window; t < t_end; ++t) {
+        const int64_t slot = p.slots[t];
+        if (slot < 0)
+            continue;
+        if (slot >= n_slots) {
+            if (tid == 0)
+                record_status(p.hdr, MOE_ERR_DEVICE_ASSERT);
+            continue;
+        }
+        const int64_t blk = slot >> sh;
+        if (t > 0 && p.slots[t - 1] >= 0 && (p.slots[t - 1] >> sh) == blk)
+            continue;                                   // not the first of its run
+        // run length: the first of the next block_size tokens that lies elsewhere
+        __syncthreads();
+        if (tid == 0)
+            s_len = bs;
+        __syncthreads();
+        if (tid < bs && (t + tid >= p.T || p.slots[t + tid] < 0 || (p.slots[t + tid] >> sh) != blk))
+            atomicMin(&s_len, tid);
+        __syncthreads();
+        const int off0 = (int)(slot & (bs - 1)), n = min(s_len, bs - off0);
+        // the new tokens, and their largest magnitude
+        const int lane8 = (tid % kLanes) * 8, row = tid / kLanes;
+        uint4 x[kSteps];
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+            if (i * kTok < n) {
+                const int r = i * kTok + row;
+                x[i] = r < n ? __ldg(reinterpret_cast<const uint4 *>(src + (t + r) * st + lane8)) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+            if (i * kTok < n)
+                m = max(m, amax_bf16x8(x[i]));
+        m = __reduce_max_sync(0xffffffffu, m);
+        if ((tid & 31) == 0)
+            s_max[tid >> 5] = m;
+        __syncthreads();
+        m = max(max(s_max[0], s_max[1]), max(s_max[2], s_max[3]));
+        uint8_t *scale = (is_v ? p.cache.v_scale : p.cache.k_scale) + blk * p.cache.kv_heads + h;
+        uint8_t *codes = (is_v ? p.cache.v : p.cache.k) + ((size_t)blk * p.cache.kv_heads + h) * bs * D;
+        int s = fp8_scale_byte(m);
+        const int was = off0 > 0 ? *scale : 0;
+        if (was < s && off0 > 0) {
+            // the block's own exponent grew: its earlier tokens' codes, rounded to it.  16
+            // bytes are a token's 16 dims (keys) or a dim's 16 tokens (values, of
+            // which those before off0 are meant)
+            const float f = exp2i(max(was - s, -126));
+            for (int u = tid; u < bs / 16 * D; u += kAppendThreads) {
+                const int first = is_v ? u / D * 16 : u / D * 16 + u % 16;
+                if (first >= off0)
+                    continue;
+                uint4 c = reinterpret_cast<uint4 *>(codes)[u];
+                uint32_t *w = reinterpret_cast<uint32_t *>(&c);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t o = 0;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t h2 = e4m3x2_to_f16x2((uint16_t)(w[q] >> (16 * e)));
+                        const float2 f2 = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
+                        o |= fp8_pair(f2.x, f2.y, f) << (16 * e);
+                    }
+                    const int held = is_v ? off0 - first - 4 * q : 4;      // of the word's four codes
+                    const uint32_t keep = held >= 4 ? 0xFFFFFFFFu : held <= 0 ? 0u : (1u << (8 * held)) - 1;
+                    w[q] = (o & keep) | (w[q] & ~keep);
+                }
+                reinterpret_cast<uint4 *>(codes)[u] = c;
+            }
+        } else if (off0 > 0) {
+            s = was;
+        }
+        __syncthreads();                                // old scale read, old codes rewritten
+        if (tid == 0)
+            *scale = (uint8_t)s;
+        const float inv = exp2i(max(127 - s, -126));
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int r = i * kTok + row;
+            if (i * kTok < n && r < n) {
+                const uint2 c = fp8_from_bf16x8(x[i], inv);
+                if (is_v) {
+                    *reinterpret_cast<uint2 *>(s_code + r * D + lane8) = c;
+                } else {
+                    const int o = (int)(p.slots[t + r] & (bs - 1));
+                    *reinterpret_cast<uint2 *>(codes + (o >> 4) * 16 * D + (lane8 >> 4) * 256 + (o & 15) * 16 + (lane8 & 15)) = c;
+                }
+            }
+        }
+        if (is_v) {
+            __syncthreads();
+            // transposed: 16 tokens of one dim are 16 bytes
+            const int sub0 = off0 >> 4, subs = ((off0 + n - 1) >> 4) - sub0 + 1;
+            for (int u = tid; u < subs * D; u += kAppendThreads) {
+                const int sub = sub0 + u / D, d = u % D;
+                uint8_t *dst = codes + (size_t)(sub * D + d) * 16;
+                const int r0 = sub * 16 - off0;         // row of the sub-block's first token
+                if (r0 >= 0 && r0 + 16 <= n) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        w[q] = s_code[(r0 + 4 * q) * D + d] | s_code[(r0 + 4 * q + 1) * D + d] << 8 |
+                               s_code[(r0 + 4 * q + 2) * D + d] << 16 | (uint32_t)s_code[(r0 + 4 * q + 3) * D + d] << 24;
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
+                    for (int j = max(0, -r0); j < 16 && r0 + j < n; ++j)
+                        dst[j] = s_code[(r0 + j) * D + d];
+                }
+            }
+        }
+        __syncthreads();                                // s_code, s_max, s_len free for the next run
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_tables(const TablesProblem &p, cudaStream_t stream) {
+    const size_t smem = (size_t)(3 * p.B + 1) * sizeof(int32_t);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kv_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess)
+            return e;
+    }
+    const int items = p.T > p.B + 1 ? p.T : p.B + 1;
+    int grid = (items + kTablesThreads - 1) / kTablesThreads;
+    if (grid > 304)                     // two CTAs per SM; more would repeat the scan without need
+        grid = 304;
+    return launch_pdl(kv_tables_kernel, dim3(grid), dim3(kTablesThreads), smem, stream, p);
+}
+
+cudaError_t launch_kv_append(const AppendProblem &p, cudaStream_t stream) {
+    const int window = p.T <= 512 ? 1 : 16;
+    const dim3 grid((p.T + window - 1) / window, p.cache.kv_heads, 2);
+    if (p.cache.head_dim == 64)
+        return launch_pdl(kv_append_kernel<64>, grid, dim3(kAppendThreads), 0, stream, p, window);
+    return launch_pdl(kv_append_kernel<128>, grid, dim3(kAppendThreads), 0, stream, p, window);
+}
+
+}  // namespace moe
