@@ -14,12 +14,11 @@ A serving step calls, per step, ``moe_kv_build_tables``, and per layer
 from __future__ import annotations
 
 import ctypes as C
-import dataclasses
 
 import torch
 
 from . import moe
-from .moe import _check, _ptr, _stream
+from .moe import _check
 
 
 class _Cache(C.Structure):
@@ -55,42 +54,66 @@ def exported_symbols() -> list[str]:
     return list(_SIG)
 
 
-def _heads(t: torch.Tensor, dtype, name: str):
-    """Pointer and (token, head) strides of a [T, heads, dim] view with contiguous dims."""
+# A call's time on the host is that of its checks: these do one attribute each on the way through, and say what is wrong
+# only when something is.  Addresses and the stream are passed as plain integers.
+
+_bf16, _i32, _i64, _u8, _f32 = torch.bfloat16, torch.int32, torch.int64, torch.uint8, torch.float32
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream) -> int:
+    if stream is None:
+        return _raw_stream(torch._C._cuda_getDevice()) if _raw_stream else torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _ptr(t: torch.Tensor, dtype, name: str) -> int:
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.stride(2) != 1:
-        raise ValueError(f"{name}: expected [tokens, heads, dim] with contiguous dims")
-    return C.c_void_p(t.data_ptr()), t.stride(0), t.stride(1)
+    raise ValueError(f"{name}: expected a contiguous tensor")
 
 
-def _want(t: torch.Tensor, shape, name: str) -> None:
-    if tuple(t.shape) != tuple(shape):
+def _heads(t: torch.Tensor, name: str):
+    """Pointer and (token, head) strides of a bf16 [T, heads, dim] view with contiguous dims."""
+    st = t.stride()
+    if t.dtype is _bf16 and t.is_cuda and len(st) == 3 and st[2] == 1:
+        return t.data_ptr(), st[0], st[1]
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.dtype is not _bf16:
+        raise ValueError(f"{name}: expected {_bf16}, got {t.dtype}")
+    raise ValueError(f"{name}: expected [tokens, heads, dim] with contiguous dims")
+
+
+def _want(t: torch.Tensor, shape: tuple, name: str) -> None:
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-@dataclasses.dataclass
 class KVCache:
     """The paged E4M3 cache (codes and scale bytes as uint8 tensors):
     k [num_blocks, kv_heads, block_size/16, head_dim/16, 16 tokens, 16 dims],
     v [num_blocks, kv_heads, block_size/16, head_dim, 16 tokens],
     k_scale, v_scale [num_blocks, kv_heads]."""
-    k: torch.Tensor
-    v: torch.Tensor
-    k_scale: torch.Tensor
-    v_scale: torch.Tensor
+    __slots__ = ("k", "v", "k_scale", "v_scale", "num_blocks", "kv_heads", "head_dim", "block_size", "_c", "_ref")
 
-    def __post_init__(self):
-        nb, heads, subs, chunks = self.k.shape[:4]
-        _want(self.k, (nb, heads, subs, chunks, 16, 16), "k")
-        _want(self.v, (nb, heads, subs, 16 * chunks, 16), "v")
-        _want(self.k_scale, (nb, heads), "k_scale")
-        _want(self.v_scale, (nb, heads), "v_scale")
-        u8 = torch.uint8
-        self._c = _Cache(_ptr(self.k, u8, "k").value, _ptr(self.v, u8, "v").value, _ptr(self.k_scale, u8, "k_scale").value,
-                         _ptr(self.v_scale, u8, "v_scale").value, nb, heads, 16 * chunks, 16 * subs)
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        if k.dim() != 6:
+            raise ValueError(f"k: expected six axes, got {tuple(k.shape)}")
+        nb, heads, subs, chunks = k.shape[:4]
+        _want(k, (nb, heads, subs, chunks, 16, 16), "k")
+        _want(v, (nb, heads, subs, 16 * chunks, 16), "v")
+        _want(k_scale, (nb, heads), "k_scale")
+        _want(v_scale, (nb, heads), "v_scale")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_blocks, self.kv_heads, self.head_dim, self.block_size = nb, heads, 16 * chunks, 16 * subs
+        self._c = _Cache(_ptr(k, _u8, "k"), _ptr(v, _u8, "v"), _ptr(k_scale, _u8, "k_scale"), _ptr(v_scale, _u8, "v_scale"), nb, heads,
+                         16 * chunks, 16 * subs)
+        self._ref = C.byref(self._c)
 
     @staticmethod
     def empty(num_blocks: int, kv_heads: int, head_dim: int, block_size: int, device="cuda") -> "KVCache":
@@ -101,28 +124,16 @@ class KVCache:
         return KVCache(make(num_blocks, kv_heads, subs, head_dim // 16, 16, 16), make(num_blocks, kv_heads, subs, head_dim, 16),
                        make(num_blocks, kv_heads), make(num_blocks, kv_heads))
 
-    @property
-    def kv_heads(self) -> int:
-        return self.k.shape[1]
 
-    @property
-    def head_dim(self) -> int:
-        return self.v.shape[3]
-
-    @property
-    def block_size(self) -> int:
-        return 16 * self.v.shape[2]
-
-
-@dataclasses.dataclass
 class FP8Weight:
     """codes uint8 [N, K] (E4M3) and scale uint8 [ceil(N/128), ceil(K/128)] (E8M0)."""
-    codes: torch.Tensor
-    scale: torch.Tensor
+    __slots__ = ("codes", "scale", "n", "k", "_codes", "_scale")
 
-    def __post_init__(self):
-        n, k = self.codes.shape
-        _want(self.scale, (-(-n // 128), -(-k // 128)), "scale")
+    def __init__(self, codes: torch.Tensor, scale: torch.Tensor):
+        self.n, self.k = codes.shape
+        _want(scale, (-(-self.n // 128), -(-self.k // 128)), "scale")
+        self.codes, self.scale = codes, scale
+        self._codes, self._scale = _ptr(codes, _u8, "codes"), _ptr(scale, _u8, "scale")
 
     @staticmethod
     def from_dense(w: torch.Tensor, stream=None) -> "FP8Weight":
@@ -147,32 +158,25 @@ def alloc_workspace(max_tokens: int, max_requests: int, q_heads: int, cache: KVC
 
 def moe_kv_build_tables(ctx_lens, new_lens, block_size, free_blocks, free_head, block_table, kv_lens, q_offsets, slot_map,
                         positions, free_head_out, ws, stream=None):
-    i32 = torch.int32
     B, T = ctx_lens.numel(), slot_map.numel()
-    _want(new_lens, (B,), "new_lens")
-    _want(kv_lens, (B,), "kv_lens")
-    _want(q_offsets, (B + 1,), "q_offsets")
-    _want(positions, (T,), "positions")
-    if block_table.shape[0] != B:
-        raise ValueError(f"block_table: expected {B} rows, got {block_table.shape[0]}")
-    _check(lib().moe_kv_build_tables(_ptr(ctx_lens, i32, "ctx_lens"), _ptr(new_lens, i32, "new_lens"), B, T, block_size,
-                                     _ptr(free_blocks, i32, "free_blocks"), free_blocks.numel(),
-                                     _ptr(free_head, i32, "free_head"), _ptr(block_table, i32, "block_table"),
-                                     block_table.shape[1], _ptr(kv_lens, i32, "kv_lens"), _ptr(q_offsets, i32, "q_offsets"),
-                                     _ptr(slot_map, torch.int64, "slot_map"), _ptr(positions, i32, "positions"),
-                                     _ptr(free_head_out, i32, "free_head_out"), _ptr(ws, torch.uint8, "ws"), ws.numel(),
+    if new_lens.numel() != B or kv_lens.numel() != B or q_offsets.numel() != B + 1 or positions.numel() != T or block_table.shape[0] != B:
+        raise ValueError(f"expected {B} new_lens, kv_lens and rows of block_table, {B + 1} q_offsets, {T} positions")
+    _check(lib().moe_kv_build_tables(_ptr(ctx_lens, _i32, "ctx_lens"), _ptr(new_lens, _i32, "new_lens"), B, T, block_size,
+                                     _ptr(free_blocks, _i32, "free_blocks"), free_blocks.numel(),
+                                     _ptr(free_head, _i32, "free_head"), _ptr(block_table, _i32, "block_table"),
+                                     block_table.shape[1], _ptr(kv_lens, _i32, "kv_lens"), _ptr(q_offsets, _i32, "q_offsets"),
+                                     _ptr(slot_map, _i64, "slot_map"), _ptr(positions, _i32, "positions"),
+                                     _ptr(free_head_out, _i32, "free_head_out"), _ptr(ws, _u8, "ws"), ws.numel(),
                                      _stream(stream)), "moe_kv_build_tables")
 
 
 def moe_kv_append(k, v, slot_map, cache: KVCache, ws, stream=None):
     """k, v bf16 [T, kv_heads, head_dim]; views with strides are taken as they are."""
-    T = k.shape[0]
+    T = slot_map.numel()
     _want(k, (T, cache.kv_heads, cache.head_dim), "k")
-    _want(v, k.shape, "v")
-    _want(slot_map, (T,), "slot_map")
-    _check(lib().moe_kv_append(*_heads(k, torch.bfloat16, "k"), *_heads(v, torch.bfloat16, "v"),
-                               _ptr(slot_map, torch.int64, "slot_map"), T, C.byref(cache._c), _ptr(ws, torch.uint8, "ws"),
-                               ws.numel(), _stream(stream)), "moe_kv_append")
+    _want(v, (T, cache.kv_heads, cache.head_dim), "v")
+    _check(lib().moe_kv_append(*_heads(k, "k"), *_heads(v, "v"), _ptr(slot_map, _i64, "slot_map"), T, cache._ref,
+                               _ptr(ws, _u8, "ws"), ws.numel(), _stream(stream)), "moe_kv_append")
 
 
 def moe_kv_attention_workspace_size(T: int, B: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
@@ -183,29 +187,26 @@ def moe_kv_attention(q, cache: KVCache, block_table, q_offsets, kv_lens, softmax
                      stream=None):
     """q bf16 [T, q_heads, head_dim] (strided views are taken as they are), out
     bf16 of the same shape, contiguous; lse fp32 [T, q_heads] or None."""
-    T, q_heads = q.shape[:2]
-    B = kv_lens.numel()
-    _want(q, (T, q_heads, cache.head_dim), "q")
-    _want(out, q.shape, "out")
-    _want(q_offsets, (B + 1,), "q_offsets")
+    shape, B = q.shape, kv_lens.numel()
+    if len(shape) != 3 or shape[2] != cache.head_dim:
+        raise ValueError(f"q: expected [tokens, heads, {cache.head_dim}], got {tuple(shape)}")
+    T, q_heads = shape[0], shape[1]
+    _want(out, shape, "out")
     if lse is not None:
         _want(lse, (T, q_heads), "lse")
-    if block_table.shape[0] != B:
-        raise ValueError(f"block_table: expected {B} rows, got {block_table.shape[0]}")
-    i32 = torch.int32
-    _check(lib().moe_kv_attention(*_heads(q, torch.bfloat16, "q"), T, q_heads, C.byref(cache._c),
-                                  _ptr(block_table, i32, "block_table"), block_table.shape[1],
-                                  _ptr(q_offsets, i32, "q_offsets"), _ptr(kv_lens, i32, "kv_lens"), B, float(softmax_scale),
-                                  int(causal), int(window), _ptr(out, torch.bfloat16, "out"),
-                                  _ptr(lse, torch.float32, "lse"), _ptr(ws, torch.uint8, "ws"), ws.numel(),
+    if q_offsets.numel() != B + 1 or block_table.shape[0] != B:
+        raise ValueError(f"expected {B + 1} q_offsets and {B} rows of block_table")
+    _check(lib().moe_kv_attention(*_heads(q, "q"), T, q_heads, cache._ref, _ptr(block_table, _i32, "block_table"),
+                                  block_table.shape[1], _ptr(q_offsets, _i32, "q_offsets"), _ptr(kv_lens, _i32, "kv_lens"), B,
+                                  softmax_scale, causal, window, _ptr(out, _bf16, "out"),
+                                  None if lse is None else _ptr(lse, _f32, "lse"), _ptr(ws, _u8, "ws"), ws.numel(),
                                   _stream(stream)), "moe_kv_attention")
 
 
 def moe_quantize_fp8_weight(w, out: FP8Weight, stream=None):
-    n, k = w.shape
-    _want(out.codes, (n, k), "codes")
-    _check(lib().moe_quantize_fp8_weight(_ptr(w, torch.bfloat16, "w"), n, k, _ptr(out.codes, torch.uint8, "codes"),
-                                         _ptr(out.scale, torch.uint8, "scale"), _stream(stream)), "moe_quantize_fp8_weight")
+    _want(w, (out.n, out.k), "w")
+    _check(lib().moe_quantize_fp8_weight(_ptr(w, _bf16, "w"), out.n, out.k, out._codes, out._scale, _stream(stream)),
+           "moe_quantize_fp8_weight")
 
 
 def moe_linear_fp8_workspace_size(T: int, N: int, K: int) -> int:
@@ -214,12 +215,10 @@ def moe_linear_fp8_workspace_size(T: int, N: int, K: int) -> int:
 
 def moe_linear_fp8(x, w: FP8Weight, y, ws, stream=None):
     """y bf16 [T, N] = x W^T; x bf16 [T, K], rows may lie further apart than K."""
-    T, K = x.shape
-    N = w.codes.shape[0]
-    if not x.is_cuda or x.dtype != torch.bfloat16 or x.stride(1) != 1:
-        raise ValueError("x: expected a CUDA bf16 tensor with contiguous rows")
-    _want(w.codes, (N, K), "codes")
-    _want(y, (T, N), "y")
-    _check(lib().moe_linear_fp8(C.c_void_p(x.data_ptr()), x.stride(0) if T > 1 else K, T, _ptr(w.codes, torch.uint8, "codes"),
-                                _ptr(w.scale, torch.uint8, "scale"), N, K, _ptr(y, torch.bfloat16, "y"),
-                                _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)), "moe_linear_fp8")
+    st, T = x.stride(), x.shape[0]
+    if not x.is_cuda or x.dtype is not _bf16 or len(st) != 2 or st[1] != 1:
+        raise ValueError("x: expected a CUDA bf16 matrix with contiguous rows")
+    _want(x, (T, w.k), "x")
+    _want(y, (T, w.n), "y")
+    _check(lib().moe_linear_fp8(x.data_ptr(), st[0] if T > 1 else w.k, T, w._codes, w._scale, w.n, w.k, _ptr(y, _bf16, "y"),
+                                _ptr(ws, _u8, "ws"), ws.numel(), _stream(stream)), "moe_linear_fp8")

@@ -17,22 +17,25 @@
 //
 // Work.  A unit is (request, up to 64 rows, key/value head), a row being a
 // (token, query head of the group) pair, so that a key is read once for the
-// whole group.  A plan kernel lists the row tiles with the 128-token tiles of
+// whole group.  A plan lists the row tiles with the 128-token tiles of
 // cache that each sees; the units' tiles, laid end to end, are cut into
 // equal ranges, one for each CTA of a persistent grid (one per SM).  A range that
 // cuts a unit writes its part (sum and log-sum) to the workspace, and the last of
-// the unit's CTAs to arrive joins the parts in the order of the cache.
+// the unit's CTAs to arrive joins the parts in the order of the cache.  Few
+// row tiles (a decode step): every CTA makes the plan itself in shared memory; many:
+// a kernel before this one makes it in the workspace.
 //
-// CTA: a producer warp streams tiles (16-token sub-blocks, 16 * D consecutive
-// bytes of a block, by bulk copies) into a ring of shared-memory stages;
-// eight consumer warps take 16 rows each and share a tile's sub-blocks among
-// the warps of the same rows: 1 x 8, 2 x 4 or 4 x 2 (row groups x token groups),
-// whichever the unit's rows need.  A sub-block's 8 x 16 byte
-// operand tiles come by ldmatrix (32 bits = 4 codes of a thread's row) and
-// are converted in registers: 16 dims of 8 keys are the B operand of one
-// MMA.  Thread (g, c) of a warp holds codes 4c .. 4c+3, as K positions 2c, 2c+1,
-// 2c+8, 2c+9: q's dims (and, for the values, the weights' tokens) are taken in
-// that order.
+// CTA: eight consumer warps, one warp that streams the cache and three that
+// prepare the queries of the next unit.  The cache comes in tiles (16-token
+// sub-blocks, 16 * D consecutive bytes of a block, as bulk copies of all
+// that lies together) through a ring of shared-memory stages; block ids and scales are
+// loaded two batches of four tiles ahead.  A consumer warp takes 16 rows (units
+// of up to 16) or 32, and the warps of the same rows share a tile's sub-blocks.
+// A sub-block's 8 x 16 byte operand tiles come by ldmatrix (32 bits = 4 codes
+// of a thread's row) and are converted in registers: 16 dims of 8 keys are the
+// B operand of one MMA, or of two with 32 rows.  Thread (g, c) of a warp holds codes
+// 4c .. 4c+3, as K positions 2c, 2c+1, 2c+8, 2c+9: q's dims (and, for the
+// values, the weights' tokens) are taken in that order.
 #include "attn.h"
 
 namespace moe {
@@ -42,15 +45,18 @@ constexpr int kTile = 128;             // tokens of a tile
 constexpr int kSubs = kTile / 16;      // sub-blocks of a tile
 constexpr int kRows = 64;              // rows of a unit
 constexpr int kConsumers = 8;          // consumer warps
-constexpr int kThreads = (kConsumers + 1) * 32;
+constexpr int kThreads = 384;          // three warpgroups: two of consumers, one of producers
+constexpr int kQWarps = 3;
 constexpr int kUnitCost = 2;           // a unit's fixed work, in tiles
 constexpr int kMinCost = 4;            // least range of a CTA, in tiles
 constexpr int kPlanThreads = 1024;
+constexpr int kSmallRequests = 256;    // most requests and row tiles of a plan in shared memory
+constexpr int kSmallTiles = 288;
 constexpr unsigned long long kWaitLimitNs = 200ull * 1000 * 1000;
 
 // A row tile of a request.
 struct RowTile {
-    long long before;      // work of the row tiles before it (all heads), in tiles
+    long long before;         // work of the row tiles before it (all heads), in tiles
     int request, q0, n, kv;   // its first row of q, new tokens, tokens
     int row0;                 // first row (of new tokens x group)
     int tile0, tiles;         // cache tiles it sees
@@ -62,26 +68,19 @@ struct Plan {
     int row_tiles, ctas;
 };
 
-// Where a CTA begins.
-struct Start {
-    long long pos;
-    int row_tile, head;
-};
-
 struct AttnArgs {
     AttnProblem p;
     int group, shift;                    // query heads of a key/value head; log2(block_size)
+    int ctas, max_tiles;
     float scale_log2;
-    const Plan *plan;
-    const Start *starts;
-    const RowTile *recs;
+    Plan *plan;
+    RowTile *recs;
     uint32_t *tickets;
     float *part, *part_lse;
     uint32_t *hdr;
 };
 
-// The positions that the rows row0 .. row0 + rows - 1 of a request with n new
-// of kv tokens see: [lo, hi).
+// The positions that a row of a request with n new of kv tokens sees: [lo, hi).
 __device__ __forceinline__ void row_range(const AttnProblem &p, int group, int kv, int n, int row, int &lo, int &hi) {
     const int pos = kv - n + row / group;
     lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
@@ -105,35 +104,25 @@ __device__ __forceinline__ T block_scan(T v, T *red, T *total) {
     if (lane == 31)
         red[warp] = v;
     __syncthreads();
-    if (warp == 0) {
-        T w = lane < nw ? red[lane] : (T)0;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const T a = __shfl_up_sync(0xffffffffu, w, d);
-            if (lane >= d)
-                w += a;
-        }
-        red[lane] = w;
+    T sum = 0, total_sum = 0;
+    for (int w = 0; w < nw; ++w) {
+        if (w < warp)
+            sum += red[w];
+        total_sum += red[w];
     }
-    __syncthreads();
-    *total = red[nw - 1];
-    return warp > 0 ? v + red[warp - 1] : v;
+    *total = total_sum;
+    return v + sum;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnArgs a, Plan *plan, Start *starts, RowTile *recs,
-                                                                 int ctas, int max_recs) {
-    extern __shared__ int s_first[];            // first row tile of a request
-    __shared__ long long red[32];
-    pdl_wait();
-    pdl_trigger();
+// The plan, by all threads of a CTA.  first: B ints, red: 32 words of shared
+// memory; recs in shared or global memory.
+__device__ __forceinline__ void make_plan(const AttnArgs &a, int *first, long long *red, RowTile *recs, Plan *plan, bool report) {
     const AttnProblem &p = a.p;
-    const int tid = threadIdx.x;
-    for (int i = tid; i < ctas; i += kPlanThreads)
-        a.tickets[i] = 0;
+    const int tid = threadIdx.x, nt = blockDim.x;
     const long long cap = (long long)p.max_blocks << a.shift;
     int bad = 0;
     long long carry = 0, total;
-    for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+    for (int b0 = 0; b0 < p.B; b0 += nt) {
         const int b = b0 + tid;
         long long c = 0;
         if (b < p.B) {
@@ -145,30 +134,29 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnArgs a, Pla
         }
         const long long incl = block_scan(c, red, &total);
         if (b < p.B)
-            s_first[b] = (int)min(carry + incl - c, (long long)max_recs);
+            first[b] = (int)min(carry + incl - c, (long long)a.max_tiles);
         carry += total;
     }
-    if (__syncthreads_or(bad) || carry > max_recs) {
+    if (__syncthreads_or(bad) || carry > a.max_tiles) {
         if (tid == 0) {
-            record_status(a.hdr, MOE_ERR_DEVICE_ASSERT);
-            plan->work = 0;
-            plan->per = 1;
-            plan->row_tiles = 0;
-            plan->ctas = 0;
+            if (report)
+                record_status(a.hdr, MOE_ERR_DEVICE_ASSERT);
+            *plan = Plan{0, 1, 0, 0};
         }
+        __syncthreads();
         return;
     }
     const int n_recs = (int)carry;
     carry = 0;
-    for (int i0 = 0; i0 < n_recs; i0 += kPlanThreads) {
+    for (int i0 = 0; i0 < n_recs; i0 += nt) {
         const int i = i0 + tid;
         RowTile r{};
         long long c = 0;
         if (i < n_recs) {
-            int lo = 0, hi = p.B;               // the last request with s_first <= i
+            int lo = 0, hi = p.B;               // the last request with first <= i
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (s_first[mid] <= i)
+                if (first[mid] <= i)
                     lo = mid;
                 else
                     hi = mid;
@@ -178,7 +166,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnArgs a, Pla
             r.q0 = q0;
             r.n = n;
             r.kv = kv;
-            r.row0 = (i - s_first[lo]) * kRows;
+            r.row0 = (i - first[lo]) * kRows;
             const int last = min(r.row0 + kRows, n * a.group) - 1;
             int l0, h0, l1, h1;
             row_range(p, a.group, kv, n, r.row0, l0, h0);
@@ -194,33 +182,20 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnArgs a, Pla
             recs[i] = r;
         carry += total;
     }
-    __syncthreads();
-    const long long most = (carry + kMinCost - 1) / kMinCost;
-    const int used = (int)min((long long)ctas, most);
-    const long long per = used > 0 ? (carry + used - 1) / used : 1;
-    for (int i = tid; i < used; i += kPlanThreads) {
-        const long long pos = i * per;
-        Start s{pos, n_recs, 0};
-        if (pos < carry) {
-            int lo = 0, hi = n_recs;            // the last row tile with before <= pos
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (recs[mid].before <= pos)
-                    lo = mid;
-                else
-                    hi = mid;
-            }
-            s.row_tile = lo;
-            s.head = (int)((pos - recs[lo].before) / (recs[lo].tiles + kUnitCost));
-        }
-        starts[i] = s;
-    }
     if (tid == 0) {
-        plan->work = carry;
-        plan->per = per;
-        plan->row_tiles = n_recs;
-        plan->ctas = used;
+        const long long most = (carry + kMinCost - 1) / kMinCost;
+        const int used = (int)min((long long)a.ctas, most);
+        *plan = Plan{carry, used > 0 ? (carry + used - 1) / used : 1, n_recs, used};
     }
+    __syncthreads();
+}
+
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnArgs a) {
+    extern __shared__ int s_first[];
+    __shared__ long long red[32];
+    pdl_wait();
+    pdl_trigger();
+    make_plan(a, s_first, red, a.recs, a.plan, true);
 }
 
 // -------------------------------------------------------------- attention
@@ -254,21 +229,32 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &b0, uint32_t 
     b1 = e4m3x2_to_f16x2((uint16_t)(w >> 16));
 }
 
+// What the consumers need of a row.
+struct RowInfo {
+    float f;               // factor of its products
+    int lo, hi;            // positions it sees
+};
+
 template <int D>
 struct Smem {
     static constexpr int kSubBytes = 16 * D;
     static constexpr int kTileBytes = kTile * D;
     static constexpr int kStageBytes = 2 * kTileBytes;
     static constexpr int kStages = D == 128 ? 4 : 8;
-    static constexpr int kPad = D + 8;                                   // floats of a row of the join buffer
-    static constexpr size_t kJoin = (size_t)kStages * kStageBytes;       // [token group][row][D] sums
-    static constexpr size_t kStats = kJoin + (size_t)128 * kPad * 4;     // [token group][row] m, M, l
-    static constexpr size_t kExps = kStats + 3 * 128 * 4;                // [stage][2][kSubs]
-    static constexpr size_t kBars = kExps + (size_t)kStages * 2 * kSubs * 4;
-    static constexpr size_t kBytes = kBars + 2 * kStages * 8 + 16;
+    static constexpr int kQBytes = kRows * D * 2;                        // queries in operand order: [16 rows][16 dims][lane][16 bytes]
+    static constexpr size_t kQ = (size_t)kStages * kStageBytes;          // two units'
+    static constexpr size_t kInfo = kQ + 2 * kQBytes;                    // RowInfo [2][kRows]
+    static constexpr size_t kJoin = kInfo + 2 * kRows * sizeof(RowInfo); // [4 warps][64 registers][lane]
+    static constexpr size_t kStats = kJoin + (size_t)4 * (D / 2) * 128;  // m, M, l [256]
+    static constexpr size_t kExps = kStats + 3 * 256 * 4;                // [stage][2][kSubs]
+    static constexpr size_t kRecs = kExps + (size_t)kStages * 2 * kSubs * 4;
+    static constexpr size_t kFirst = kRecs + kSmallTiles * sizeof(RowTile);
+    static constexpr size_t kBars = kFirst + kSmallRequests * 4;
+    static constexpr size_t kBytes = kBars + (2 * kStages + 4) * 8 + 16;
+    static_assert(kInfo % 16 == 0 && kJoin % 16 == 0 && kRecs % 8 == 0 && kBars % 8 == 0 && kBytes <= 227 * 1024, "shared memory");
 };
 
-// One unit's piece, as producer and consumers walk through it.
+// One unit's piece, as producers and consumers walk through it.
 struct Piece {
     int request, head, row0, rows, q0, n, kv;
     int tile0, t0, t1;            // cache tiles tile0 + [t0, t1)
@@ -278,26 +264,30 @@ struct Piece {
 // Walks a CTA's range.
 struct Walk {
     const AttnArgs &a;
+    const RowTile *recs;
     long long pos, end, base, per;
     int rt, head, n_recs;
     RowTile r;
-    __device__ Walk(const AttnArgs &args) : a(args) {
-        const Plan pl = *a.plan;
+    __device__ Walk(const AttnArgs &args, const Plan &pl, const RowTile *tiles) : a(args), recs(tiles) {
         n_recs = pl.row_tiles;
         per = pl.per;
-        if ((int)blockIdx.x >= pl.ctas) {
-            rt = n_recs;
-            return;
-        }
-        const Start s = a.starts[blockIdx.x];
-        pos = s.pos;
+        pos = (long long)blockIdx.x * per;
         end = min(pos + per, pl.work);
-        rt = s.row_tile;
-        head = s.head;
-        if (rt < n_recs) {
-            r = a.recs[rt];
-            base = r.before + (long long)head * (r.tiles + kUnitCost);
+        rt = n_recs;
+        if ((int)blockIdx.x >= pl.ctas || pos >= pl.work)
+            return;
+        int lo = 0, hi = n_recs;                // the last row tile with before <= pos
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (recs[mid].before <= pos)
+                lo = mid;
+            else
+                hi = mid;
         }
+        rt = lo;
+        r = recs[rt];
+        head = (int)((pos - r.before) / (r.tiles + kUnitCost));
+        base = r.before + (long long)head * (r.tiles + kUnitCost);
     }
     // The next piece; false at the end of the range.
     __device__ bool next(Piece &pc) {
@@ -326,7 +316,7 @@ struct Walk {
             if (++head == a.p.cache.kv_heads) {
                 head = 0;
                 if (++rt < n_recs)
-                    r = a.recs[rt];
+                    r = recs[rt];
             }
             if (mine)
                 return true;
@@ -335,36 +325,74 @@ struct Walk {
     }
 };
 
+// Up to four tiles of a piece: a lane for each of their sub-blocks.
+struct Batch {
+    int tiles;                    // 0: there is none
+    int head, hi, page, ks, vs;
+    long long tok;                // the lane's first token
+    bool live;
+};
+
 template <int D>
-__device__ void produce(const AttnArgs &a, uint8_t *sm, uint64_t *full, uint64_t *empty) {
+__device__ __forceinline__ void stream_cache(const AttnArgs &a, const Plan &pl, const RowTile *recs, uint8_t *sm, uint64_t *full,
+                                             uint64_t *empty) {
     using S = Smem<D>;
     const AttnProblem &p = a.p;
     const int lane = threadIdx.x & 31, sub = lane & (kSubs - 1);
-    const bool is_v = lane >= kSubs;             // lanes 0..7: keys, 8..15: values
-    const uint8_t *codes = is_v ? p.cache.v : p.cache.k, *scales = is_v ? p.cache.v_scale : p.cache.k_scale;
     const uint64_t policy = l2_evict_first_policy();
-    Walk walk(a);
+    Walk walk(a, pl, recs);
     Piece pc;
+    int t = 0;
+    bool more = walk.next(pc);
+    if (more)
+        t = pc.t0;
+    // the next batch, its block ids asked for
+    auto pages = [&](Batch &b) {
+        b.tiles = 0;
+        while (more && t == pc.t1) {
+            more = walk.next(pc);
+            if (more)
+                t = pc.t0;
+        }
+        if (!more)
+            return;
+        b.tiles = min(4, pc.t1 - t);
+        b.head = pc.head;
+        b.hi = p.causal ? min(pc.kv, pc.kv - pc.n + (pc.row0 + pc.rows - 1) / a.group + 1) : pc.kv;
+        b.tok = (long long)(pc.tile0 + t) * kTile + lane * 16;
+        b.live = lane < kSubs * b.tiles && b.tok < b.hi;
+        b.page = b.live ? __ldg(p.table + (size_t)pc.request * p.max_blocks + (b.tok >> a.shift)) : 0;
+        t += b.tiles;
+    };
+    auto scales = [&](Batch &b) {
+        if (b.tiles == 0)
+            return;
+        if (b.page < 0 || b.page >= p.cache.num_blocks) {
+            record_status(a.hdr, MOE_ERR_DEVICE_ASSERT);
+            b.page = 0;
+        }
+        const size_t unit = (size_t)b.page * p.cache.kv_heads + b.head;
+        b.ks = b.live ? __ldg(p.cache.k_scale + unit) : 127;
+        b.vs = b.live ? __ldg(p.cache.v_scale + unit) : 127;
+    };
     long long it = 0;
     bool dead = false;
-    while (walk.next(pc)) {
-        const int hi = p.causal ? min(pc.kv, pc.kv - pc.n + (pc.row0 + pc.rows - 1) / a.group + 1) : pc.kv;
-        const int32_t *row = p.table + (size_t)pc.request * p.max_blocks;
-        for (int t = pc.t0; t < pc.t1; ++t, ++it) {
+    Batch b0, b1, b2;
+    pages(b0);
+    pages(b1);
+    scales(b0);
+    while (b0.tiles > 0) {
+        pages(b2);
+        scales(b1);
+        // sub-blocks of one block that lie in one tile are one copy, issued by the first one's lane
+        const uint32_t live = __ballot_sync(0xffffffffu, b0.live);
+        const int in_block = (int)(b0.tok & ((1 << a.shift) - 1)) >> 4, block_subs = 1 << (a.shift - 4);
+        const int left = __popc((live >> (lane & ~(kSubs - 1))) & ((1u << kSubs) - 1)) - sub;
+        const bool leads = b0.live && (sub == 0 || in_block == 0);
+        const uint32_t bytes = (uint32_t)min(block_subs - in_block, left) * S::kSubBytes;
+        const size_t src = ((((size_t)b0.page * p.cache.kv_heads + b0.head) << a.shift) + in_block * 16) * D;
+        for (int i = 0; i < b0.tiles; ++i, ++it) {
             const int st = (int)(it % S::kStages);
-            const long long tok = (long long)(pc.tile0 + t) * kTile + sub * 16;
-            const bool live = lane < 2 * kSubs && tok < hi;
-            int page = 0, e = 0;
-            if (live) {
-                page = __ldg(row + (tok >> a.shift));
-                if (page < 0 || page >= p.cache.num_blocks) {
-                    record_status(a.hdr, MOE_ERR_DEVICE_ASSERT);
-                    page = 0;
-                }
-            }
-            const size_t unit = (size_t)page * p.cache.kv_heads + pc.head;
-            if (live)
-                e = (int)__ldg(scales + unit) - 127;
             if (!dead && it >= S::kStages)
                 dead = !__all_sync(0xffffffffu, wait_phase(empty + st, (uint32_t)((it / S::kStages - 1) & 1)));
             if (dead) {
@@ -372,150 +400,203 @@ __device__ void produce(const AttnArgs &a, uint8_t *sm, uint64_t *full, uint64_t
                     record_status(a.hdr, MOE_ERR_DEVICE_TIMEOUT);
                 continue;                        // no further copies; the consumers' waits run out
             }
-            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, live)) * S::kSubBytes;
-            uint8_t *dst = sm + (size_t)st * S::kStageBytes + (is_v ? S::kTileBytes : 0) + sub * S::kSubBytes;
-            if (lane < 2 * kSubs)
-                reinterpret_cast<float *>(sm + S::kExps)[st * 2 * kSubs + lane] = is_v ? (float)e : exp2i(min(max(e, -126), 127));
+            const bool mine = lane / kSubs == i;
+            if (mine) {
+                float *ex = reinterpret_cast<float *>(sm + S::kExps) + st * 2 * kSubs + sub;
+                ex[0] = exp2i(min(max(b0.ks, 1), 254) - 127);
+                ex[kSubs] = (float)(b0.vs - 127);
+            }
             __syncwarp();
             if (lane == 0)
-                mbar_arrive_expect_tx(full + st, bytes);
+                mbar_arrive_expect_tx(full + st, 2 * S::kSubBytes * __popc((live >> (i * kSubs)) & ((1u << kSubs) - 1)));
             __syncwarp();
-            if (live) {
-                const uint8_t *src = codes + (unit << a.shift) * D + (size_t)(tok & ((1 << a.shift) - 1)) * D;
+            if (mine && leads) {
+                const uint32_t dst = smem_u32(sm + (size_t)st * S::kStageBytes + sub * S::kSubBytes), bar = smem_u32(full + st);
                 asm volatile(
                     "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, "
-                    "[%3], %4;" ::"r"(smem_u32(dst)), "l"(src), "r"(S::kSubBytes), "r"(smem_u32(full + st)), "l"(policy)
+                    "[%3], %4;" ::"r"(dst), "l"(p.cache.k + src), "r"(bytes), "r"(bar), "l"(policy)
+                    : "memory");
+                asm volatile(
+                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, "
+                    "[%3], %4;" ::"r"(dst + S::kTileBytes), "l"(p.cache.v + src), "r"(bytes), "r"(bar), "l"(policy)
                     : "memory");
             }
         }
+        b0 = b1;
+        b1 = b2;
     }
     // copies still in flight must land before the CTA's shared memory goes away
-    const long long from = it > S::kStages ? it - S::kStages : 0;
-    for (long long i = from; i < it && !dead; ++i)
+    for (long long i = it > S::kStages ? it - S::kStages : 0; i < it && !dead; ++i)
         wait_phase(full + i % S::kStages, (uint32_t)((i / S::kStages) & 1));
 }
 
-// The state of a warp: 16 rows, row g and row g + 8 of thread (g, c).
+// Queries of one unit after the other: bf16 to scaled f16 in the MMA's A operand order, 16 rows a warp.
 template <int D>
+__device__ __forceinline__ void load_queries(const AttnArgs &a, const Plan &pl, const RowTile *recs, uint8_t *sm, uint64_t *q_full,
+                                             uint64_t *q_empty) {
+    using S = Smem<D>;
+    const AttnProblem &p = a.p;
+    const int warp = (threadIdx.x >> 5) - kConsumers - 1, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    Walk walk(a, pl, recs);
+    Piece pc;
+    bool dead = false;
+    for (int u = 0; walk.next(pc); ++u) {
+        const int buf = u & 1;
+        if (!dead && u >= 2)
+            dead = !__all_sync(0xffffffffu, wait_phase(q_empty + buf, (uint32_t)((u / 2 - 1) & 1)));
+        RowInfo *info = reinterpret_cast<RowInfo *>(sm + S::kInfo) + buf * kRows;
+        // rows up to the next multiple of 32, as the consumers read them
+        for (int rg = warp; rg * 16 < (pc.rows <= 16 ? 16 : (pc.rows + 31) / 32 * 32); rg += kQWarps) {
+            uint32_t *dst = reinterpret_cast<uint32_t *>(sm + S::kQ + (size_t)buf * S::kQBytes + (size_t)rg * 32 * D) + lane * 4;
+#pragma unroll 1
+            for (int s = 0; s < 2; ++s) {
+                const int rr = rg * 16 + g + 8 * s;
+                const bool live = rr < pc.rows;
+                const int row = pc.row0 + (live ? rr : 0);
+                const uint16_t *src =
+                    p.q + (int64_t)(pc.q0 + row / a.group) * p.q_st + (int64_t)(pc.head * a.group + row % a.group) * p.q_sh + 4 * c;
+                uint2 raw[D / 16];
+                float mx = 0.0f;
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j)
+                    raw[j] = live ? __ldg(reinterpret_cast<const uint2 *>(src + 16 * j)) : make_uint2(0, 0);
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j)
+                    mx = fmaxf(mx, fmaxf(fmaxf(fabsf(__uint_as_float(raw[j].x << 16)), fabsf(__uint_as_float(raw[j].x & 0xFFFF0000u))),
+                                         fmaxf(fabsf(__uint_as_float(raw[j].y << 16)), fabsf(__uint_as_float(raw[j].y & 0xFFFF0000u)))));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const int sh = f16_shift_for_max(mx);
+                const float sc = exp2i(sh);
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                    const __half2 lo = __floats2half2_rn(__uint_as_float(raw[j].x << 16) * sc, __uint_as_float(raw[j].x & 0xFFFF0000u) * sc);
+                    const __half2 hi = __floats2half2_rn(__uint_as_float(raw[j].y << 16) * sc, __uint_as_float(raw[j].y & 0xFFFF0000u) * sc);
+                    dst[j * 128 + s] = *reinterpret_cast<const uint32_t *>(&lo);
+                    dst[j * 128 + 2 + s] = *reinterpret_cast<const uint32_t *>(&hi);
+                }
+                if (c == 0) {
+                    RowInfo r{a.scale_log2 * exp2i(-sh), 0, pc.kv};
+                    if (live)
+                        row_range(p, a.group, pc.kv, pc.n, row, r.lo, r.hi);
+                    info[rr] = r;
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(q_full + buf);
+    }
+}
+
+// The state of a warp: MT x 16 rows, rows g and g + 8 of each for thread (g, c).
+template <int D, int MT>
 struct Acc {
-    float o[D / 8][4];
-    float m[2], big[2], l[2];       // m_i, M_i, l_i (l: this thread's columns)
+    float o[MT][D / 8][4];
+    float m[MT][2], big[MT][2], l[MT][2];       // m_i, M_i, l_i (l: this thread's columns)
 };
 
-// One piece's tiles with RG row groups x TG token groups.
-template <int D, int RG>
-__device__ __forceinline__ void attend(const AttnArgs &a, const Piece &pc, uint8_t *sm, uint64_t *full, uint64_t *empty,
-                                       long long &it, bool &dead, Acc<D> &acc) {
+// One piece's tiles: RG groups of MT x 16 rows, the other warps sharing the tokens.
+template <int D, int MT, int RG>
+__device__ __forceinline__ void attend(const Piece &pc, uint8_t *sm, int qbuf, uint64_t *full, uint64_t *empty, uint32_t *hdr,
+                                       long long &it, bool &dead, Acc<D, MT> &acc) {
     using S = Smem<D>;
     constexpr int TG = kConsumers / RG, NS = kSubs / TG;    // sub-blocks of a warp in a tile
-    const AttnProblem &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int rg = warp % RG, tg = warp / RG;
-    // the rows: their query in operand order, scaled into f16, and their limits
-    uint32_t q[D / 16][4];
-    float f[2];
-    int lo[2], hi[2];
+    const uint4 *q = reinterpret_cast<const uint4 *>(sm + S::kQ + (size_t)qbuf * S::kQBytes + (size_t)rg * MT * 32 * D) + lane;
+    const RowInfo *info = reinterpret_cast<const RowInfo *>(sm + S::kInfo) + qbuf * kRows + rg * MT * 16 + g;
+    float f[MT][2];
+    int min_hi = INT_MAX, max_lo = 0;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        const int rr = rg * 16 + g + 8 * s;
-        const bool live = rr < pc.rows;
-        const int row = pc.row0 + (live ? rr : 0);
-        const uint16_t *src = p.q + (int64_t)(pc.q0 + row / a.group) * p.q_st + (int64_t)(pc.head * a.group + row % a.group) * p.q_sh + 4 * c;
-        uint2 raw[D / 16];
-        float mx = 0.0f;
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-            raw[j] = live ? __ldg(reinterpret_cast<const uint2 *>(src + 16 * j)) : make_uint2(0, 0);
-            mx = fmaxf(mx, fmaxf(fmaxf(fabsf(__uint_as_float(raw[j].x << 16)), fabsf(__uint_as_float(raw[j].x & 0xFFFF0000u))),
-                                 fmaxf(fabsf(__uint_as_float(raw[j].y << 16)), fabsf(__uint_as_float(raw[j].y & 0xFFFF0000u)))));
+        for (int s = 0; s < 2; ++s) {
+            const RowInfo r = info[mt * 16 + 8 * s];
+            f[mt][s] = r.f;
+            min_hi = min(min_hi, r.hi);
+            max_lo = max(max_lo, r.lo);
         }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const int sh = f16_shift_for_max(mx);
-        const float sc = exp2i(sh);
-        f[s] = a.scale_log2 * exp2i(-sh);
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-            const __half2 u = __floats2half2_rn(__uint_as_float(raw[j].x << 16) * sc, __uint_as_float(raw[j].x & 0xFFFF0000u) * sc);
-            const __half2 v = __floats2half2_rn(__uint_as_float(raw[j].y << 16) * sc, __uint_as_float(raw[j].y & 0xFFFF0000u) * sc);
-            q[j][s] = *reinterpret_cast<const uint32_t *>(&u);
-            q[j][2 + s] = *reinterpret_cast<const uint32_t *>(&v);
-        }
-        lo[s] = 0;
-        hi[s] = pc.kv;
-        if (live)
-            row_range(p, a.group, pc.kv, pc.n, row, lo[s], hi[s]);
-    }
-    const int min_hi = __reduce_min_sync(0xffffffffu, min(hi[0], hi[1])), max_lo = __reduce_max_sync(0xffffffffu, max(lo[0], lo[1]));
-    const bool idle = rg * 16 >= pc.rows;                    // no rows: only keeps the ring going
+    min_hi = __reduce_min_sync(0xffffffffu, min_hi);
+    max_lo = __reduce_max_sync(0xffffffffu, max_lo);
     const uint32_t base = smem_u32(sm);
-    // ldmatrix rows: matrix lane / 8, row i = lane % 8.  Keys of the MMA's column i: token 4 (i / 2) + i % 2, plus 2 in the
-    // second half; values: dim i.
+    // ldmatrix rows.  Keys: matrix = (half, chunk of 16 dims); the MMA's column i is token 4 (i / 2) + i % 2, plus 2 in the
+    // second half.  Values: matrix = 8 dims, row = dim.
     const int mi = lane >> 3, ri = lane & 7;
-    const uint32_t k_off = (uint32_t)(mi * 256 + (4 * (ri >> 1) + (ri & 1)) * 16), v_off = (uint32_t)(lane * 16);
+    const uint32_t k_off = (uint32_t)((mi >> 1) * 256 + (4 * (ri >> 1) + (ri & 1) + 2 * (mi & 1)) * 16), v_off = (uint32_t)(lane * 16);
 
     for (int t = pc.t0; t < pc.t1; ++t, ++it) {
         const int st = (int)(it % S::kStages);
         if (!dead) {
             dead = !__all_sync(0xffffffffu, wait_phase(full + st, (uint32_t)((it / S::kStages) & 1)));
             if (dead && lane == 0)
-                record_status(a.hdr, MOE_ERR_DEVICE_TIMEOUT);
+                record_status(hdr, MOE_ERR_DEVICE_TIMEOUT);
         }
         const int tok0 = (pc.tile0 + t) * kTile;
         const uint32_t ks = base + (uint32_t)(st * S::kStageBytes), vs = ks + S::kTileBytes;
         const float *ex = reinterpret_cast<const float *>(sm + S::kExps) + st * 2 * kSubs;
-        if (!idle) {
-            const bool edge = tok0 + kTile > min_hi || tok0 < max_lo;
-            float x[NS][2][4];
+        const bool edge = tok0 + kTile > min_hi || tok0 < max_lo;
+        float x[MT][NS][2][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < NS; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    x[mt][i][e >> 2][e & 3] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < D / 16; j += 2) {
+            uint4 qa[MT][2];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    qa[mt][u] = q[mt * 2 * D + (j + u) * 32];
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
-                const int sub = i * TG + tg;
+                uint32_t w[4];
+                ldmatrix4(w, ks + (uint32_t)((i * TG + tg) * S::kSubBytes + j * 256) + k_off);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        x[i][h][e] = 0.0f;
-#pragma unroll
-                for (int j = 0; j < D / 16; j += 4)
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        uint32_t w[4];
-                        ldmatrix4(w, ks + (uint32_t)(sub * S::kSubBytes + j * 256 + h * 32) + k_off);
+                        uint32_t b0, b1;
+                        codes_to_f16(w[2 * u + h], b0, b1);
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            uint32_t b0, b1;
-                            codes_to_f16(w[u], b0, b1);
-                            mma_m16n8k16_f16(x[i][h], q[j + u][0], q[j + u][1], q[j + u][2], q[j + u][3], b0, b1, x[i][h]);
-                        }
+                        for (int mt = 0; mt < MT; ++mt)
+                            mma_m16n8k16_f16(x[mt][i][h], qa[mt][u].x, qa[mt][u].y, qa[mt][u].z, qa[mt][u].w, b0, b1, x[mt][i][h]);
                     }
-                const float kf = ex[sub], f0 = f[0] * kf, f1 = f[1] * kf;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    x[i][h][0] *= f0;
-                    x[i][h][1] *= f0;
-                    x[i][h][2] *= f1;
-                    x[i][h][3] *= f1;
-                }
-                if (edge) {
-                    const int tk = tok0 + sub * 16 + 4 * c;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int j = tk + 2 * h + (e & 1);
-                            if (j < lo[e >> 1] || j >= hi[e >> 1])
-                                x[i][h][e] = -INFINITY;
-                        }
-                }
             }
-            // maxima: m over x, M over x + b
-            float nm[2] = {acc.m[0], acc.m[1]}, nb[2] = {acc.big[0], acc.big[1]};
+        }
+        uint32_t pw[MT][NS][4];
 #pragma unroll
-            for (int i = 0; i < NS; ++i) {
-                const float b = ex[kSubs + i * TG + tg];
+        for (int mt = 0; mt < MT; ++mt) {
+            if (edge) {
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    const float v = fmaxf(fmaxf(x[i][0][2 * s], x[i][0][2 * s + 1]), fmaxf(x[i][1][2 * s], x[i][1][2 * s + 1]));
+                    const int lo = info[mt * 16 + 8 * s].lo, hi = info[mt * 16 + 8 * s].hi;
+#pragma unroll
+                    for (int i = 0; i < NS; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int k = tok0 + (i * TG + tg) * 16 + 4 * c + 2 * h + e;
+                                if (k < lo || k >= hi)
+                                    x[mt][i][h][2 * s + e] = -INFINITY;
+                            }
+                }
+            }
+            // maxima: m over x, M over x + b (products times fi are x; fi > 0, so that -infinity stays)
+            float fi[NS][2], nm[2] = {acc.m[mt][0], acc.m[mt][1]}, nb[2] = {acc.big[mt][0], acc.big[mt][1]};
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                const float kf = ex[i * TG + tg], b = ex[kSubs + i * TG + tg];
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    fi[i][s] = fmaxf(f[mt][s] * kf, 1.2e-38f);
+                    const float v = fi[i][s] * fmaxf(fmaxf(x[mt][i][0][2 * s], x[mt][i][0][2 * s + 1]),
+                                                     fmaxf(x[mt][i][1][2 * s], x[mt][i][1][2 * s + 1]));
                     nm[s] = fmaxf(nm[s], v);
                     nb[s] = fmaxf(nb[s], v + b);
                 }
@@ -528,80 +609,84 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const Piece &pc, uint8
                 nb[s] = fmaxf(nb[s], __shfl_xor_sync(0xffffffffu, nb[s], 2));
             }
             float mz[2], bz[2];                               // maxima to subtract (0 where nothing is seen yet)
-            const bool grew = nb[0] > acc.big[0] || nb[1] > acc.big[1];
+            const bool grew = nb[0] > acc.big[mt][0] || nb[1] > acc.big[mt][1];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 mz[s] = nm[s] == -INFINITY ? 0.0f : nm[s];
                 bz[s] = nb[s] == -INFINITY ? 0.0f : nb[s];
-                acc.l[s] *= ex2(acc.m[s] - mz[s]);
-                acc.m[s] = nm[s];
+                acc.l[mt][s] *= ex2(acc.m[mt][s] - mz[s]);
+                acc.m[mt][s] = nm[s];
             }
             if (__any_sync(0xffffffffu, grew)) {
-                const float r0 = ex2(acc.big[0] - bz[0]), r1 = ex2(acc.big[1] - bz[1]);
+                const float r0 = ex2(acc.big[mt][0] - bz[0]), r1 = ex2(acc.big[mt][1] - bz[1]);
 #pragma unroll
                 for (int n = 0; n < D / 8; ++n) {
-                    acc.o[n][0] *= r0;
-                    acc.o[n][1] *= r0;
-                    acc.o[n][2] *= r1;
-                    acc.o[n][3] *= r1;
+                    acc.o[mt][n][0] *= r0;
+                    acc.o[mt][n][1] *= r0;
+                    acc.o[mt][n][2] *= r1;
+                    acc.o[mt][n][3] *= r1;
                 }
             }
-            acc.big[0] = nb[0];
-            acc.big[1] = nb[1];
-            uint32_t nan_seen = 0;
+            acc.big[mt][0] = nb[0];
+            acc.big[mt][1] = nb[1];
+            // weights: p 2^(b + m - M).  The power is at most 2^126: above it (M - m far below b) p is zero.
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
-                const int sub = i * TG + tg;
-                const float b = ex[kSubs + sub], d0 = b - bz[0], d1 = b - bz[1];
-                uint32_t w[4];
+                const float b = ex[kSubs + i * TG + tg];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    acc.l[0] += ex2(x[i][h][0] - mz[0]) + ex2(x[i][h][1] - mz[0]);
-                    acc.l[1] += ex2(x[i][h][2] - mz[1]) + ex2(x[i][h][3] - mz[1]);
-                    const __half2 u = __floats2half2_rn(ex2(x[i][h][0] + d0), ex2(x[i][h][1] + d0));
-                    const __half2 v = __floats2half2_rn(ex2(x[i][h][2] + d1), ex2(x[i][h][3] + d1));
-                    w[2 * h] = *reinterpret_cast<const uint32_t *>(&u);
-                    w[2 * h + 1] = *reinterpret_cast<const uint32_t *>(&v);
-                }
+                for (int s = 0; s < 2; ++s) {
+                    const float r = ex2(fminf(b + (mz[s] - bz[s]), 126.0f));
 #pragma unroll
-                for (int n = 0; n < D / 8; n += 4) {
-                    uint32_t vc[4];
-                    ldmatrix4(vc, vs + (uint32_t)(sub * S::kSubBytes + n * 128) + v_off);
-                    if (edge) {
-                        // some row does not see some token here: NaN codes (of unused slots, or of tokens past a
-                        // row) must not meet its zero weight.  They are left out, and added below to the rows that see them.
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const uint32_t nan = __vcmpeq4(vc[u] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                            vc[u] &= ~nan;
-                            nan_seen |= nan;
-                        }
-                    }
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        uint32_t b0, b1;
-                        codes_to_f16(vc[u], b0, b1);
-                        mma_m16n8k16_f16(acc.o[n + u], w[0], w[1], w[2], w[3], b0, b1, acc.o[n + u]);
+                    for (int h = 0; h < 2; ++h) {
+                        const float p0 = ex2(fmaf(x[mt][i][h][2 * s], fi[i][s], -mz[s])), p1 = ex2(fmaf(x[mt][i][h][2 * s + 1], fi[i][s], -mz[s]));
+                        acc.l[mt][s] += p0 + p1;
+                        const __half2 u = __floats2half2_rn(p0 * r, p1 * r);
+                        pw[mt][i][2 * h + s] = *reinterpret_cast<const uint32_t *>(&u);
                     }
                 }
             }
-            if (edge && __any_sync(0xffffffffu, nan_seen != 0)) {
-                const uint8_t *vb = sm + (size_t)st * S::kStageBytes + S::kTileBytes;
-#pragma unroll 1
-                for (int i = 0; i < NS; ++i) {
-                    const int sub = i * TG + tg;
-#pragma unroll 1
-                    for (int k = 0; k < 16; ++k) {
-                        const int j = tok0 + sub * 16 + k;
+        }
+        uint32_t nan_seen = 0;
 #pragma unroll
-                        for (int n = 0; n < D / 8; ++n)
+        for (int i = 0; i < NS; ++i)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int d = 8 * n + 2 * c + (e & 1);
-                                if ((vb[sub * S::kSubBytes + d * 16 + k] & 0x7F) == 0x7F && j >= lo[e >> 1] && j < hi[e >> 1])
-                                    acc.o[n][e] = __uint_as_float(0x7FFFFFFFu);
-                            }
+            for (int n = 0; n < D / 8; n += 4) {
+                uint32_t vc[4];
+                ldmatrix4(vc, vs + (uint32_t)((i * TG + tg) * S::kSubBytes + n * 128) + v_off);
+                if (edge) {
+                    // some row does not see some token here: NaN codes (of unused slots, or of tokens past a
+                    // row) must not meet its zero weight.  They are left out, and added below to the rows that see them.
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const uint32_t nan = __vcmpeq4(vc[u] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                        vc[u] &= ~nan;
+                        nan_seen |= nan;
                     }
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    uint32_t b0, b1;
+                    codes_to_f16(vc[u], b0, b1);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+                        mma_m16n8k16_f16(acc.o[mt][n + u], pw[mt][i][0], pw[mt][i][1], pw[mt][i][2], pw[mt][i][3], b0, b1, acc.o[mt][n + u]);
+                }
+            }
+        if (edge && __any_sync(0xffffffffu, nan_seen != 0)) {
+            const uint8_t *vb = sm + (size_t)st * S::kStageBytes + S::kTileBytes;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const RowInfo r0 = info[mt * 16], r1 = info[mt * 16 + 8];
+#pragma unroll 1
+                for (int k = 0; k < NS * 16; ++k) {
+                    const int at = ((k >> 4) * TG + tg) * S::kSubBytes + (k & 15), j = tok0 + ((k >> 4) * TG + tg) * 16 + (k & 15);
+                    const bool see0 = j >= r0.lo && j < r0.hi, see1 = j >= r1.lo && j < r1.hi;
+#pragma unroll
+                    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if ((e < 2 ? see0 : see1) && (vb[at + (8 * n + 2 * c + (e & 1)) * 16] & 0x7F) == 0x7F)
+                                acc.o[mt][n][e] = __uint_as_float(0x7FFFFFFFu);
                 }
             }
         }
@@ -611,191 +696,272 @@ __device__ __forceinline__ void attend(const AttnArgs &a, const Piece &pc, uint8
     }
 }
 
-__device__ __forceinline__ void store_bf16x4(uint16_t *dst, float4 v) {
-    uint32_t a, b;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(a) : "f"(v.y), "f"(v.x));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b) : "f"(v.w), "f"(v.z));
-    *reinterpret_cast<uint2 *>(dst) = make_uint2(a, b);
-}
-
 // Joins the token groups of a piece and writes the rows: to the output, or,
 // where the unit has other pieces, to the workspace, the last CTA joining those.
-template <int D, int RG>
-__device__ __forceinline__ void finish(const AttnArgs &a, const Piece &pc, uint8_t *sm, Acc<D> &acc, int *s_last) {
+template <int D, int MT, int RG>
+__device__ __forceinline__ void finish(const AttnArgs &a, const Piece &pc, uint8_t *sm, Acc<D, MT> &acc, int *s_last) {
     using S = Smem<D>;
-    constexpr int TG = kConsumers / RG, R = RG * 16;
+    constexpr int TG = kConsumers / RG, R = RG * MT * 16;
     const AttnProblem &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int rg = warp % RG, tg = warp / RG;
-    float *sum = reinterpret_cast<float *>(sm + S::kJoin), *st = reinterpret_cast<float *>(sm + S::kStats);
-    float *s_m = st, *s_b = st + 128, *s_l = st + 256;
+    float *s_m = reinterpret_cast<float *>(sm + S::kStats), *s_b = s_m + 256, *s_l = s_b + 256;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        acc.l[s] += __shfl_xor_sync(0xffffffffu, acc.l[s], 1);
-        acc.l[s] += __shfl_xor_sync(0xffffffffu, acc.l[s], 2);
-        if (c == 0) {
-            const int i = tg * R + rg * 16 + g + 8 * s;
-            s_m[i] = acc.m[s];
-            s_b[i] = acc.big[s];
-            s_l[i] = acc.l[s];
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            acc.l[mt][s] += __shfl_xor_sync(0xffffffffu, acc.l[mt][s], 1);
+            acc.l[mt][s] += __shfl_xor_sync(0xffffffffu, acc.l[mt][s], 2);
+            if (c == 0) {
+                const int i = tg * R + rg * MT * 16 + mt * 16 + g + 8 * s;
+                s_m[i] = acc.m[mt][s];
+                s_b[i] = acc.big[mt][s];
+                s_l[i] = acc.l[mt][s];
+            }
         }
-    }
-#pragma unroll
-    for (int n = 0; n < D / 8; ++n) {
-        float *dst = sum + (size_t)(tg * R + rg * 16 + g) * S::kPad + 8 * n + 2 * c;
-        *reinterpret_cast<float2 *>(dst) = make_float2(acc.o[n][0], acc.o[n][1]);
-        *reinterpret_cast<float2 *>(dst + 8 * S::kPad) = make_float2(acc.o[n][2], acc.o[n][3]);
-    }
     named_barrier_sync(1, kConsumers * 32);
+    float f[MT][2], lse2[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int i = rg * MT * 16 + mt * 16 + g + 8 * s;
+            float m = -INFINITY, b = -INFINITY, l = 0.0f;
+#pragma unroll
+            for (int t = 0; t < TG; ++t) {
+                m = fmaxf(m, s_m[t * R + i]);
+                b = fmaxf(b, s_b[t * R + i]);
+            }
+            const float mz = m == -INFINITY ? 0.0f : m, bz = b == -INFINITY ? 0.0f : b;
+#pragma unroll
+            for (int t = 0; t < TG; ++t)
+                l += s_l[t * R + i] * ex2(s_m[t * R + i] - mz);
+            // l is NaN where a score was: then so is the row
+            f[mt][s] = l == 0.0f ? 0.0f : exp2f(bz - mz) / l;
+            lse2[mt][s] = l == 0.0f ? -INFINITY : mz + log2f(l);
+            const float w = ex2(acc.big[mt][s] - bz);
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+                acc.o[mt][n][2 * s] *= w;
+                acc.o[mt][n][2 * s + 1] *= w;
+            }
+        }
+    // sums of the token groups, halving their number; a warp's registers [register / 4][lane]
+    float4 *join = reinterpret_cast<float4 *>(sm + S::kJoin);
+#pragma unroll
+    for (int half = TG / 2; half > 0; half >>= 1)
+#pragma unroll
+        for (int part = 0; part < MT; ++part) {
+            if (tg >= half && tg < 2 * half) {
+                float4 *to = join + ((tg - half) * RG + rg) * (D / 8) * 32 + lane;
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n)
+                    to[n * 32] = make_float4(acc.o[part][n][0], acc.o[part][n][1], acc.o[part][n][2], acc.o[part][n][3]);
+            }
+            named_barrier_sync(1, kConsumers * 32);
+            if (tg < half) {
+                const float4 *from = join + (tg * RG + rg) * (D / 8) * 32 + lane;
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) {
+                    const float4 v = from[n * 32];
+                    acc.o[part][n][0] += v.x;
+                    acc.o[part][n][1] += v.y;
+                    acc.o[part][n][2] += v.z;
+                    acc.o[part][n][3] += v.w;
+                }
+            }
+            if (half > 1 || part < MT - 1)
+                named_barrier_sync(1, kConsumers * 32);
+        }
     const int pieces = pc.last - pc.first + 1;
     const int slot = (int)blockIdx.x * 2 + (pc.first == (int)blockIdx.x);
-    constexpr int Q = D / 4;
-    for (int i = tid; i < pc.rows * Q; i += kConsumers * 32) {
-        const int row = i / Q, d = i % Q * 4;
-        float m = -INFINITY, b = -INFINITY;
+    if (tg == 0) {
 #pragma unroll
-        for (int t = 0; t < TG; ++t) {
-            m = fmaxf(m, s_m[t * R + row]);
-            b = fmaxf(b, s_b[t * R + row]);
-        }
-        const float mz = m == -INFINITY ? 0.0f : m, bz = b == -INFINITY ? 0.0f : b;
-        float l = 0.0f;
-        float4 o = make_float4(0, 0, 0, 0);
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int t = 0; t < TG; ++t) {
-            l += s_l[t * R + row] * ex2(s_m[t * R + row] - mz);
-            const float w = ex2(s_b[t * R + row] - bz);
-            const float4 v = *reinterpret_cast<const float4 *>(sum + (size_t)(t * R + row) * S::kPad + d);
-            o.x += v.x * w;
-            o.y += v.y * w;
-            o.z += v.z * w;
-            o.w += v.w * w;
-        }
-        // l is NaN where a score was: then so is the row
-        const float f = l == 0.0f ? 0.0f : exp2f(bz - mz) / l;
-        o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-        const float lse2 = l == 0.0f ? -INFINITY : mz + log2f(l);
-        if (pieces == 1) {
-            const int r = pc.row0 + row;
-            const size_t at = (size_t)(pc.q0 + r / a.group) * p.q_heads + pc.head * a.group + r % a.group;
-            store_bf16x4(p.out + at * D + d, o);
-            if (d == 0 && p.lse)
-                p.lse[at] = lse2 * 0.69314718055994530942f;
-        } else {
-            __stcg(reinterpret_cast<float4 *>(a.part + ((size_t)slot * kRows + row) * D + d), o);
-            if (d == 0)
-                __stcg(a.part_lse + slot * kRows + row, lse2);
-        }
+            for (int s = 0; s < 2; ++s) {
+                const int row = rg * MT * 16 + mt * 16 + g + 8 * s;
+                if (row >= pc.rows)
+                    continue;
+                const float w = f[mt][s];
+                if (pieces == 1) {
+                    const int r = pc.row0 + row;
+                    const size_t at = (size_t)(pc.q0 + r / a.group) * p.q_heads + pc.head * a.group + r % a.group;
+#pragma unroll
+                    for (int n = 0; n < D / 8; ++n) {
+                        uint32_t v;
+                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(acc.o[mt][n][2 * s + 1] * w), "f"(acc.o[mt][n][2 * s] * w));
+                        *reinterpret_cast<uint32_t *>(p.out + at * D + 8 * n + 2 * c) = v;
+                    }
+                    if (c == 0 && p.lse)
+                        p.lse[at] = lse2[mt][s] * 0.69314718055994530942f;
+                } else {
+                    float *to = a.part + ((size_t)slot * kRows + row) * D + 2 * c;
+#pragma unroll
+                    for (int n = 0; n < D / 8; ++n)
+                        __stcg(reinterpret_cast<float2 *>(to + 8 * n), make_float2(acc.o[mt][n][2 * s] * w, acc.o[mt][n][2 * s + 1] * w));
+                    if (c == 0)
+                        __stcg(a.part_lse + slot * kRows + row, lse2[mt][s]);
+                }
+            }
     }
     if (pieces > 1) {
         __threadfence();
         named_barrier_sync(1, kConsumers * 32);
         if (tid == 0) {
             __threadfence();
-            *s_last = atomicAdd(a.tickets + pc.first, 1u) == (uint32_t)(pieces - 1);
+            const bool last = atomicAdd(a.tickets + pc.first, 1u) == (uint32_t)(pieces - 1);
+            if (last)
+                a.tickets[pc.first] = 0;              // for the next call
+            *s_last = last;
             __threadfence();
         }
         named_barrier_sync(1, kConsumers * 32);
         if (*s_last) {
+            constexpr int Q = D / 4, U = 8;           // U parts' loads in flight
             for (int i = tid; i < pc.rows * Q; i += kConsumers * 32) {
                 const int row = i / Q, d = i % Q * 4;
-                auto at = [&](int k) { return (size_t)(pc.first + k) * 2 + (k == 0); };
-                float m = -INFINITY;
-                for (int k = 0; k < pieces; ++k)
-                    m = fmaxf(m, __ldcg(a.part_lse + at(k) * kRows + row));
-                const float mz = m == -INFINITY ? 0.0f : m;
-                float l = 0.0f;
+                float m = -INFINITY, l = 0.0f;
                 float4 o = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-                for (int k = 0; k < pieces; ++k) {
-                    const float w = ex2(__ldcg(a.part_lse + at(k) * kRows + row) - mz);
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part + (at(k) * kRows + row) * D + d));
-                    l += w;
-                    o.x += v.x * w;
-                    o.y += v.y * w;
-                    o.z += v.z * w;
-                    o.w += v.w * w;
+                for (int k0 = 0; k0 < pieces; k0 += U) {
+                    float e[U];
+                    float4 v[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int k = k0 + u;
+                        const size_t at = ((size_t)(pc.first + k) * 2 + (k == 0)) * kRows + row;
+                        e[u] = k < pieces ? __ldcg(a.part_lse + at) : -INFINITY;
+                        v[u] = k < pieces ? __ldcg(reinterpret_cast<const float4 *>(a.part + at * D + d)) : make_float4(0, 0, 0, 0);
+                    }
+                    float nm = m;
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        nm = fmaxf(nm, e[u]);
+                    const float mz = nm == -INFINITY ? 0.0f : nm, w0 = ex2(m - mz);
+                    l *= w0;
+                    o = make_float4(o.x * w0, o.y * w0, o.z * w0, o.w * w0);
+                    m = nm;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const float w = ex2(e[u] - mz);
+                        l += w;
+                        o.x += v[u].x * w;
+                        o.y += v[u].y * w;
+                        o.z += v[u].z * w;
+                        o.w += v[u].w * w;
+                    }
                 }
-                const float f = l == 0.0f ? 0.0f : 1.0f / l;
+                const float w = l == 0.0f ? 0.0f : 1.0f / l;
                 const int r = pc.row0 + row;
                 const size_t to = (size_t)(pc.q0 + r / a.group) * p.q_heads + pc.head * a.group + r % a.group;
-                store_bf16x4(p.out + to * D + d, make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
+                uint32_t lo, hi;
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(o.y * w), "f"(o.x * w));
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(o.w * w), "f"(o.z * w));
+                *reinterpret_cast<uint2 *>(p.out + to * D + d) = make_uint2(lo, hi);
                 if (d == 0 && p.lse)
-                    p.lse[to] = l == 0.0f ? -INFINITY : (mz + log2f(l)) * 0.69314718055994530942f;
+                    p.lse[to] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
             }
         }
     }
-    named_barrier_sync(1, kConsumers * 32);       // the join buffer is free again
 }
 
-template <int D, int RG>
-__device__ __forceinline__ void consume_piece(const AttnArgs &a, const Piece &pc, uint8_t *sm, uint64_t *full,
-                                              uint64_t *empty, long long &it, bool &dead, int *s_last) {
-    Acc<D> acc;
+template <int D, int MT, int RG>
+__device__ __forceinline__ void consume_piece(const AttnArgs &a, const Piece &pc, uint8_t *sm, int qbuf, uint64_t *full, uint64_t *empty,
+                                              uint64_t *q_empty, long long &it, bool &dead, int *s_last) {
+    Acc<D, MT> acc;
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n)
+    for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            acc.o[n][e] = 0.0f;
+        for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        acc.m[s] = acc.big[s] = -INFINITY;
-        acc.l[s] = 0.0f;
+            for (int e = 0; e < 4; ++e)
+                acc.o[mt][n][e] = 0.0f;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            acc.m[mt][s] = acc.big[mt][s] = -INFINITY;
+            acc.l[mt][s] = 0.0f;
+        }
     }
-    attend<D, RG>(a, pc, sm, full, empty, it, dead, acc);
-    finish<D, RG>(a, pc, sm, acc, s_last);
+    attend<D, MT, RG>(pc, sm, qbuf, full, empty, a.hdr, it, dead, acc);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(q_empty);
+    finish<D, MT, RG>(a, pc, sm, acc, s_last);
 }
 
-template <int D>
+template <int D, bool SMALL>
 __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ AttnArgs a) {
     using S = Smem<D>;
     extern __shared__ __align__(128) uint8_t sm[];
+    __shared__ long long red[32];
+    __shared__ Plan s_plan;
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + S::kBars), *empty = full + S::kStages;
-    int *s_last = reinterpret_cast<int *>(empty + S::kStages);
+    uint64_t *q_full = empty + S::kStages, *q_empty = q_full + 2;
+    int *s_last = reinterpret_cast<int *>(q_empty + 2);
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(full + i, 1);
             mbar_init(empty + i, kConsumers);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full + i, kQWarps);
+            mbar_init(q_empty + i, kConsumers);
         }
         fence_barrier_init();
     }
     __syncthreads();
     pdl_wait();
     pdl_trigger();
-    if (threadIdx.x >= kConsumers * 32) {
-        produce<D>(a, sm, full, empty);
+    const RowTile *recs = a.recs;
+    if (SMALL) {
+        RowTile *mine = reinterpret_cast<RowTile *>(sm + S::kRecs);
+        make_plan(a, reinterpret_cast<int *>(sm + S::kFirst), red, mine, &s_plan, blockIdx.x == 0);
+        recs = mine;
+    }
+    const Plan pl = SMALL ? s_plan : *a.plan;
+    const int warp = threadIdx.x >> 5;
+    if (warp >= kConsumers) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == kConsumers)
+            stream_cache<D>(a, pl, recs, sm, full, empty);
+        else
+            load_queries<D>(a, pl, recs, sm, q_full, q_empty);
         return;
     }
-    Walk walk(a);
+    // 256 threads x 216 + 128 x 72 registers = the 384 x 168 of the launch
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    Walk walk(a, pl, recs);
     Piece pc;
     long long it = 0;
     bool dead = false;
-    while (walk.next(pc)) {
+    for (int u = 0; walk.next(pc); ++u) {
+        const int buf = u & 1;
+        if (!dead) {
+            dead = !__all_sync(0xffffffffu, wait_phase(q_full + buf, (uint32_t)((u / 2) & 1)));
+            if (dead && (threadIdx.x & 31) == 0)
+                record_status(a.hdr, MOE_ERR_DEVICE_TIMEOUT);
+        }
         if (pc.rows <= 16)
-            consume_piece<D, 1>(a, pc, sm, full, empty, it, dead, s_last);
+            consume_piece<D, 1, 1>(a, pc, sm, buf, full, empty, q_empty + buf, it, dead, s_last);
         else if (pc.rows <= 32)
-            consume_piece<D, 2>(a, pc, sm, full, empty, it, dead, s_last);
+            consume_piece<D, 2, 1>(a, pc, sm, buf, full, empty, q_empty + buf, it, dead, s_last);
         else
-            consume_piece<D, 4>(a, pc, sm, full, empty, it, dead, s_last);
+            consume_piece<D, 2, 2>(a, pc, sm, buf, full, empty, q_empty + buf, it, dead, s_last);
     }
 }
 
-constexpr int kMaxCtas = 256;
+int max_row_tiles(int T, int B, int group) { return (int)((long long)T * group / kRows + B); }
 
 }  // namespace
 
 AttnLayout AttnLayout::make(int T, int B, int q_heads, int kv_heads, int head_dim) {
     AttnLayout L{};
-    const long long group = q_heads / kv_heads;
-    const size_t recs = (size_t)((long long)T * group / kRows + B);
-    size_t o = kHeaderBytes;
+    size_t o = kInitBytes;
     auto take = [&](size_t bytes) { o = align_up(o, 256); size_t r = o; o += bytes; return r; };
     L.plan = take(sizeof(Plan));
-    L.starts = take(kMaxCtas * sizeof(Start));
-    L.tickets = take(kMaxCtas * sizeof(uint32_t));
-    L.recs = take(recs * sizeof(RowTile));
-    L.part = take((size_t)2 * kMaxCtas * kRows * head_dim * sizeof(float));
-    L.part_lse = take((size_t)2 * kMaxCtas * kRows * sizeof(float));
+    L.recs = take((size_t)max_row_tiles(T, B, q_heads / kv_heads) * sizeof(RowTile));
+    L.part = take((size_t)2 * kMaxAttnCtas * kRows * head_dim * sizeof(float));
+    L.part_lse = take((size_t)2 * kMaxAttnCtas * kRows * sizeof(float));
     L.total = align_up(o, 256);
     return L;
 }
@@ -803,23 +969,22 @@ AttnLayout AttnLayout::make(int T, int B, int q_heads, int kv_heads, int head_di
 cudaError_t launch_kv_attention(const AttnProblem &p, void *ws, int sms, cudaStream_t stream) {
     const AttnLayout L = AttnLayout::make(p.T, p.B, p.q_heads, p.cache.kv_heads, p.cache.head_dim);
     const int group = p.q_heads / p.cache.kv_heads;
-    const int max_recs = (int)((long long)p.T * group / kRows + p.B);
     int shift = 4;
     while ((1 << shift) < p.cache.block_size)
         ++shift;
-    AttnArgs a{p, group, shift, p.scale * 1.44269504088896340736f, ws_at<Plan>(ws, L.plan), ws_at<Start>(ws, L.starts),
-               ws_at<RowTile>(ws, L.recs), ws_at<uint32_t>(ws, L.tickets), ws_at<float>(ws, L.part),
-               ws_at<float>(ws, L.part_lse), ws_at<uint32_t>(ws, 0)};
-    const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
-    cudaError_t e = launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), p.B * sizeof(int), stream, a,
-                               ws_at<Plan>(ws, L.plan), ws_at<Start>(ws, L.starts), ws_at<RowTile>(ws, L.recs), ctas, max_recs);
-    if (e != cudaSuccess)
-        return e;
+    const AttnArgs a{p, group, shift, sms < kMaxAttnCtas ? sms : kMaxAttnCtas, max_row_tiles(p.T, p.B, group),
+                     p.scale * 1.44269504088896340736f, ws_at<Plan>(ws, L.plan), ws_at<RowTile>(ws, L.recs),
+                     ws_at<uint32_t>(ws, kHeaderBytes), ws_at<float>(ws, L.part), ws_at<float>(ws, L.part_lse), ws_at<uint32_t>(ws, 0)};
     auto go = [&](auto kernel, size_t smem) {
         cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        return r != cudaSuccess ? r : launch_pdl(kernel, dim3(ctas), dim3(kThreads), smem, stream, a);
+        return r != cudaSuccess ? r : launch_pdl(kernel, dim3(a.ctas), dim3(kThreads), smem, stream, a);
     };
-    return p.cache.head_dim == 64 ? go(attn_kernel<64>, Smem<64>::kBytes) : go(attn_kernel<128>, Smem<128>::kBytes);
+    if (p.B <= kSmallRequests && a.max_tiles <= kSmallTiles)
+        return p.cache.head_dim == 64 ? go(attn_kernel<64, true>, Smem<64>::kBytes) : go(attn_kernel<128, true>, Smem<128>::kBytes);
+    cudaError_t e = launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), p.B * sizeof(int), stream, a);
+    if (e != cudaSuccess)
+        return e;
+    return p.cache.head_dim == 64 ? go(attn_kernel<64, false>, Smem<64>::kBytes) : go(attn_kernel<128, false>, Smem<128>::kBytes);
 }
 
 }  // namespace moe

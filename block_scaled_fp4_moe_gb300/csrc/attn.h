@@ -104,9 +104,9 @@ struct AttnProblem {
     uint16_t *out;
     float *lse;
 };
-// Workspace regions of the attention; grid = CTAs of its persistent kernel.
+// Workspace regions of the attention.
 struct AttnLayout {
-    size_t plan, starts, tickets, recs, part, part_lse, total;
+    size_t plan, recs, part, part_lse, total;
     static AttnLayout make(int T, int B, int q_heads, int kv_heads, int head_dim);
 };
 cudaError_t launch_kv_attention(const AttnProblem &p, void *ws, int sms, cudaStream_t stream);

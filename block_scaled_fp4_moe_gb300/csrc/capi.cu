@@ -289,7 +289,7 @@ moe_status_t moe_workspace_init(void *ws, size_t ws_bytes, cudaStream_t stream) 
         return MOE_ERR_MISALIGNED;
     if (ws_bytes < kHdrWords * sizeof(uint32_t))
         return MOE_ERR_WORKSPACE_TOO_SMALL;
-    return from_cuda(cudaMemsetAsync(ws, 0, ws_bytes < kHeaderBytes ? ws_bytes : kHeaderBytes, stream));
+    return from_cuda(cudaMemsetAsync(ws, 0, ws_bytes < kInitBytes ? ws_bytes : kInitBytes, stream));
 }
 
 moe_status_t moe_route_topk(const uint16_t *x, const float *router_w, const float *logit_bias, int T, int H, int E,

@@ -61,6 +61,12 @@ constexpr size_t kCtaStampOffset = kHdrWords * sizeof(uint32_t);
 constexpr int kFusedMaxCtaStamps = 256;
 constexpr size_t kHeaderBytes = kCtaStampOffset + kFusedMaxCtaStamps * 4 * sizeof(unsigned long long);
 
+// Behind them the attention's arrival counters, one per CTA of its grid, which
+// every completed call leaves at zero (attn.cu).  moe_workspace_init clears
+// all of this; the calls' regions begin after it.
+constexpr int kMaxAttnCtas = 256;
+constexpr size_t kInitBytes = kHeaderBytes + kMaxAttnCtas * sizeof(uint32_t);
+
 // Most K pieces the tensor-memory FFN kernels split their last items into.
 constexpr int kTcMaxPieces = 256;
 
@@ -143,7 +149,7 @@ struct WsLayout {
         const long long active = entries < (size_t)n_tot ? (long long)entries : n_tot;
         L.n_kc_gu = pick_kchunks(H / 64, active * (I / 8), entries * 2 * (size_t)I * sizeof(float));
         L.n_kc_dn = pick_kchunks(I / 64, active * (H / 16), entries * (size_t)H * sizeof(float));
-        size_t o = kHeaderBytes;
+        size_t o = kInitBytes;
         auto take = [&](size_t bytes) { o = align_up(o, 256); size_t r = o; o += bytes; return r; };
         L.route_part = take((size_t)nh * T * E * 2 * sizeof(float));
         L.topk_ids = take(entries * sizeof(int32_t));

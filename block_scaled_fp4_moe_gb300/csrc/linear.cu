@@ -434,7 +434,7 @@ struct Layout {
                 const size_t n = (size_t)((T + tile - 1) / tile) * ((tile + 127) / 128);
                 blobs = n > blobs ? n : blobs;
             }
-        size_t o = kHeaderBytes;
+        size_t o = kInitBytes;
         auto take = [&](size_t bytes) { o = align_up(o, 256); size_t r = o; o += bytes; return r; };
         L.codes = take((size_t)T * KB * 128);
         L.scales = take(blobs * KB * 512);
