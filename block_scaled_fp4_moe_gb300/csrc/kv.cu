@@ -144,7 +144,7 @@ constexpr int kAppendThreads = 128;
 // holds the new tokens of the block in registers (at most 128 x 128 bf16 =
 // 16 x 16 bytes a thread), takes their largest magnitude, settles the exponent,
 // re-rounds the codes that the block held where the exponent grew, and
-// writes the new codes: one pass over the input, no atomics.  A CTA looks at
+// writes the new codes: one pass over the input, no atomics on global memory.  A CTA looks at
 // `window` consecutive tokens and works for those that begin a run of tokens in one
 // block (a run may reach past the window); the launcher's window is 1 while
 // T tokens x heads x 2 fill the GPU few times over (a CTA then has one
@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendProblem
     __shared__ __align__(16) uint8_t s_code[128 * D];   // values: codes [token][dim] before the transpose
     __shared__ uint32_t s_max[kAppendThreads / 32];
     __shared__ int s_len;
+    __shared__ uint32_t s_begins;
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, h = blockIdx.y;
@@ -165,24 +166,25 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendProblem
     const uint16_t *src = (is_v ? p.v + h * p.v_sh : p.k + h * p.k_sh);
     const int64_t st = is_v ? p.v_st : p.k_st;
     const int64_t n_slots = (int64_t)p.cache.num_blocks << sh;
-    const int t_end = min(p.T, ((int)blockIdx.x + 1) * window);
-    for (int t = blockIdx.x * window; t < t_end; ++t) {
-        const int64_t slot = p.slots[t];
-        if (slot < 0)
-            continue;
-        if (slot >= n_slots) {
-            if (tid == 0)
-                record_status(p.hdr, MOE_ERR_DEVICE_ASSERT);
-            continue;
-        }
-        const int64_t blk = slot >> sh;
-        if (t > 0 && p.slots[t - 1] >= 0 && (p.slots[t - 1] >> sh) == blk)
-            continue;                                   // not the first of its run
-        // run length: the first of the next block_size tokens that lies elsewhere
-        __syncthreads();
-        if (tid == 0)
+    const int t0 = blockIdx.x * window;
+    // which tokens of the window begin a run: their block is not that of the token before
+    if (tid < 32) {
+        const int t = t0 + tid;
+        const int64_t slot = tid < window && t < p.T ? p.slots[t] : -1;
+        const int64_t prev = slot >= 0 && t > 0 ? p.slots[t - 1] : -1;
+        if (slot >= n_slots)
+            record_status(p.hdr, MOE_ERR_DEVICE_ASSERT);
+        const uint32_t begins = __ballot_sync(0xffffffffu, slot >= 0 && slot < n_slots && (prev < 0 || (prev >> sh) != (slot >> sh)));
+        if (tid == 0) {
+            s_begins = begins;
             s_len = bs;
-        __syncthreads();
+        }
+    }
+    __syncthreads();
+    for (uint32_t begins = s_begins; begins; begins &= begins - 1) {
+        const int t = t0 + __ffs(begins) - 1;
+        const int64_t slot = p.slots[t], blk = slot >> sh;
+        // run length: the first of the next block_size tokens that lies elsewhere
         if (tid < bs && (t + tid >= p.T || p.slots[t + tid] < 0 || (p.slots[t + tid] >> sh) != blk))
             atomicMin(&s_len, tid);
         __syncthreads();
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendProblem
                 if (is_v) {
                     *reinterpret_cast<uint2 *>(s_code + r * D + lane8) = c;
                 } else {
-                    const int o = (int)(p.slots[t + r] & (bs - 1));
+                    const int o = off0 + r;
                     *reinterpret_cast<uint2 *>(codes + (o >> 4) * 16 * D + (lane8 >> 4) * 256 + (o & 15) * 16 + (lane8 & 15)) = c;
                 }
             }
@@ -277,7 +279,9 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendProblem
                 }
             }
         }
-        __syncthreads();                                // s_code, s_max, s_len free for the next run
+        if (tid == 0)
+            s_len = bs;
+        __syncthreads();                                // s_code, s_max free for the next run
     }
 }
 

@@ -339,7 +339,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) fp8_gemm_kernel(const
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kCols));
 }
 
-// x to codes [T][KB * 128] and scale blobs: half a warp for each group of 128.
+constexpr int kQuantGroups = 4;
+
+// x to codes [T][KB * 128] and scale blobs: half a warp for each group of 128, four loads in flight a thread.
 // A token tile's blob for a K stage holds token r's byte, four times, in word
 // (r % 32) * 4 + r / 32: the order in which tensor memory keeps the scales of 128 rows.
 __global__ void __launch_bounds__(256) fp8_quant_kernel(const uint16_t *__restrict__ x, int64_t ldx, int T, int K, int KB,
@@ -347,21 +349,28 @@ __global__ void __launch_bounds__(256) fp8_quant_kernel(const uint16_t *__restri
                                                         uint32_t *__restrict__ scales) {
     pdl_wait();
     pdl_trigger();
-    const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) >> 4;
-    const int l = threadIdx.x & 15;
-    const bool live = i < (long long)T * KB;
-    const int t = live ? (int)(i / KB) : 0, kb = live ? (int)(i - (long long)t * KB) : 0, k = kb * 128 + l * 8;
-    const uint4 v = live && k < K ? *reinterpret_cast<const uint4 *>(x + t * ldx + k) : make_uint4(0, 0, 0, 0);
-    uint32_t m = amax_bf16x8(v);
+    const int l = threadIdx.x & 15, groups = T * KB, first = blockIdx.x * (16 * kQuantGroups) + (threadIdx.x >> 4);
+    uint4 v[kQuantGroups];
 #pragma unroll
-    for (int d = 8; d > 0; d >>= 1)
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const int s = fp8_scale_byte(m);
-    if (live) {
-        *reinterpret_cast<uint2 *>(codes + (size_t)t * KB * 128 + k) = fp8_from_bf16x8(v, exp2i(127 - s));
-        if (l == 0) {
-            const int r = t % tile;
-            scales[(((size_t)(t / tile) * KB + kb) * blobs + r / 128) * 128 + (r % 32) * 4 + (r % 128) / 32] = s * 0x01010101u;
+    for (int u = 0; u < kQuantGroups; ++u) {
+        const int i = first + 16 * u, t = i / KB, k = (i - t * KB) * 128 + l * 8;
+        v[u] = i < groups && k < K ? __ldg(reinterpret_cast<const uint4 *>(x + t * ldx + k)) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kQuantGroups; ++u) {
+        const int i = first + 16 * u;
+        uint32_t m = amax_bf16x8(v[u]);
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1)
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const int s = fp8_scale_byte(m);
+        if (i < groups) {
+            const int t = i / KB, kb = i - t * KB;
+            *reinterpret_cast<uint2 *>(codes + (size_t)i * 128 + l * 8) = fp8_from_bf16x8(v[u], exp2i(127 - s));
+            if (l == 0) {
+                const int tt = t / tile, r = t - tt * tile;
+                scales[(((size_t)tt * KB + kb) * blobs + r / 128) * 128 + (r % 32) * 4 + (r % 128) / 32] = s * 0x01010101u;
+            }
         }
     }
 }
@@ -499,8 +508,8 @@ cudaError_t launch_linear_fp8(const LinearProblem &p, void *ws, int sms, cudaStr
     cudaError_t e = encode_tiled(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p.codes, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess)
         return e;
-    const long long groups = (long long)p.T * KB;
-    e = launch_pdl(fp8_quant_kernel, dim3((unsigned)((groups + 15) / 16)), dim3(256), 0, stream, p.x, p.ldx, p.T, p.K, KB,
+    const int groups = p.T * KB, per = 16 * kQuantGroups;       // at most 2^29
+    e = launch_pdl(fp8_quant_kernel, dim3((groups + per - 1) / per), dim3(256), 0, stream, p.x, p.ldx, p.T, p.K, KB,
                    f.tile, (f.tile + 127) / 128, codes, scales);
     if (e != cudaSuccess)
         return e;
