@@ -26,7 +26,7 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 256;
 constexpr int kStageK = 128;
 constexpr int kABytes = 128 * kStageK;
 constexpr int kMaxSplit = 8;       // CTAs of a cluster
@@ -62,6 +62,9 @@ struct GemmArgs {
     uint32_t *hdr;
     int T, N, KB, n_tiles, tiles;
     int split;                    // CTAs of a cluster
+    const uint16_t *x;            // fused form
+    int64_t ldx;
+    int K;
 };
 
 __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity) {
@@ -98,8 +101,32 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int
         : "memory");
 }
 
+// The tensor-core instructions are issued by a converged warp, one elected
+// lane of it doing so: their operands stay warp-uniform.  (From a branch of one lane an MMA took
+// about 200 cycles to issue: 880 a stage instead of the 384 of its products at N = 192.)
 __device__ __forceinline__ void commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+    asm volatile(
+        "{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\n"
+        "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
+        : "memory");
+}
+
+// 512 bytes of scales to four columns of every lane quarter.
+__device__ __forceinline__ void copy_scales(uint32_t col, uint32_t blob) {
+    asm volatile(
+        "{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\n"
+        "@p tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}\n" ::"r"(col),
+        "l"(desc_rows16(blob))
+        : "memory");
+}
+
+template <int NN>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t da, uint64_t db, uint32_t sfa, uint32_t sfb, uint32_t acc) {
+    asm volatile(
+        "{\n.reg .pred p, q;\nelect.sync _|p, 0xffffffff;\nsetp.ne.b32 q, %4, 0;\n"
+        "@p tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], q;\n}\n" ::"r"(d),
+        "l"(da), "l"(db), "n"(idesc<NN>()), "r"(acc), "r"(sfa), "r"(sfb)
+        : "memory");
 }
 
 // The K stages of one tile that a CTA sums; the tiles of a CTA, one after the other.
@@ -120,10 +147,14 @@ __device__ __forceinline__ void store_bf16(uint16_t *dst, float v) {
     *dst = b;
 }
 
-template <int NN, bool SPLIT>
+// FUSED (split form, up to 8 tokens): the warps that drain the accumulators first
+// quantise x, each cluster for itself, straight into the operand's
+// shared-memory layout: no quantisation kernel before this one.
+template <int NN, bool SPLIT, bool FUSED>
 __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) fp8_gemm_kernel(const __grid_constant__ GemmArgs a,
                                                                            const __grid_constant__ CUtensorMap wmap,
                                                                            const __grid_constant__ CUtensorMap xmap) {
+    static_assert(SPLIT || !FUSED, "form");
     using S = Tile<NN, SPLIT>;
     constexpr int kStages = S::kStages;
     extern __shared__ uint8_t raw_smem[];
@@ -134,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) fp8_gemm_kernel(const
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(full + i, 1);
+            mbar_init(full + i, FUSED ? 6 : 2);
             mbar_init(empty + i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -159,10 +190,12 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) fp8_gemm_kernel(const
         // ---- copies.  W does not depend on the quantisation of x: the first
         // stages' W goes out before the wait for that kernel.
         auto stage_w = [&](int st, int tile, int kb) {
-            mbar_arrive_expect_tx(full + st, kABytes + S::kB + 512 * S::kBlobs);
+            mbar_arrive_expect_tx(full + st, kABytes + (FUSED ? 0 : S::kB + 512 * S::kBlobs));
             tma_2d(smem_u32(sm + (size_t)st * kABytes), &wmap, kb * kStageK, tile % a.n_tiles * 128, full + st);
         };
         auto stage_x = [&](int st, int tile, int kb) {
+            if (FUSED)
+                return;
             const int tt = tile / a.n_tiles;
             tma_2d(smem_u32(sm + S::kOffB + (size_t)st * S::kB), &xmap, kb * kStageK, tt * NN, full + st);
             asm volatile(
@@ -174,12 +207,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) fp8_gemm_kernel(const
         long long it = 0;                   // stages issued
         bool dead = false, waited = false;
         for (int tile = r0.tile; tile < a.tiles && !dead; tile += r0.step) {
-            const uint8_t *wsrow = a.wscale + (size_t)(tile % a.n_tiles) * a.KB;
-            uint32_t wsc = 0;               // W's scale of 32 stages, a byte a lane
             for (int kb = r0.kb0; kb < r0.kb1; ++kb, ++it) {
-                const int st = (int)(it % kStages), o = (kb - r0.kb0) & 31;
-                if (o == 0)
-                    wsc = kb + lane < r0.kb1 ? __ldg(wsrow + kb + lane) : 0;
+                const int st = (int)(it % kStages);
                 if (it >= kStages) {
                     if (!waited) {          // the ring is full of W: now x's part of it
                         pdl_wait();
@@ -197,15 +226,12 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) fp8_gemm_kernel(const
                         break;
                     }
                 }
-                const uint32_t w = __shfl_sync(0xffffffffu, wsc, o) * 0x01010101u;
-                *reinterpret_cast<uint4 *>(sm + S::kOffSf + (size_t)st * S::kSf + lane * 16) = make_uint4(w, w, w, w);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
                 if (lane == 0) {
                     stage_w(st, tile, kb);
                     if (waited)
                         stage_x(st, tile, kb);
                 }
+                __syncwarp();
             }
         }
         if (!waited) {                      // the whole range fits in the ring
@@ -221,55 +247,114 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) fp8_gemm_kernel(const
             wait_phase(full + i % kStages, (uint32_t)((i / kStages) & 1));
     } else if (warp == 1) {
         // ---- MMAs
-        if (lane == 0) {
-            bool dead = false;
-            long long it = 0;
-            int piece = 0;
-            for (int tile = r0.tile; tile < a.tiles && !dead; tile += r0.step, ++piece) {
-                const int buf = SPLIT ? 0 : piece & 1;
-                if (piece >= 2 && !wait_phase(d_empty + buf, (uint32_t)((piece / 2 - 1) & 1)))
+        bool dead = false;
+        int it = 0, piece = 0;
+        for (int tile = r0.tile; tile < a.tiles && !dead; tile += r0.step, ++piece) {
+            const int buf = SPLIT ? 0 : piece & 1;
+            if (piece >= 2)
+                dead = !__all_sync(0xffffffffu, wait_phase(d_empty + buf, (uint32_t)((piece / 2 - 1) & 1)));
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t d = tmem + buf * S::kDCols;
+            for (int kb = r0.kb0; kb < r0.kb1 && !dead; ++kb, ++it) {
+                const int st = it % kStages;
+                if (!__all_sync(0xffffffffu, wait_phase(full + st, (uint32_t)((it / kStages) & 1)))) {
                     dead = true;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t d = tmem + buf * S::kDCols;
-                for (int kb = r0.kb0; kb < r0.kb1 && !dead; ++kb, ++it) {
-                    const int st = (int)(it % kStages);
-                    if (!wait_phase(full + st, (uint32_t)((it / kStages) & 1))) {
-                        dead = true;
-                        break;
-                    }
-                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const uint32_t sfa = tmem + S::kSfCol + 32 * st, sfb = sfa + 16;
-                    const uint32_t sf = smem_u32(sm + S::kOffSf + (size_t)st * S::kSf);
-                    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(sfa), "l"(desc_rows16(sf)) : "memory");
-#pragma unroll
-                    for (int j = 0; j < S::kBlobs; ++j)
-                        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(sfb + 4 * j),
-                                     "l"(desc_rows16(sf + 512 * (j + 1)))
-                                     : "memory");
-                    const uint32_t sa = smem_u32(sm + (size_t)st * kABytes), sb = smem_u32(sm + S::kOffB + (size_t)st * S::kB);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t acc = kb > r0.kb0 || j > 0;
-                        asm volatile(
-                            "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-                            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n}\n" ::"r"(d),
-                            "l"(desc_sw128(sa + 32 * j)), "l"(desc_sw128(sb + 32 * j)), "r"(idesc<NN>()), "r"(acc), "r"(sfa), "r"(sfb)
-                            : "memory");
-                    }
-                    commit(empty + st);
+                    break;
                 }
-                commit(d_full + buf);
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t sfa = tmem + S::kSfCol + 32 * st, sfb = sfa + 16;
+                const uint32_t sf = smem_u32(sm + S::kOffSf + (size_t)st * S::kSf);
+                copy_scales(sfa, sf);
+#pragma unroll
+                for (int j = 0; j < S::kBlobs; ++j)
+                    copy_scales(sfb + 4 * j, sf + 512 * (j + 1));
+                const uint64_t da = desc_sw128(smem_u32(sm + (size_t)st * kABytes)), db = desc_sw128(smem_u32(sm + S::kOffB + (size_t)st * S::kB));
+#pragma unroll
+                for (int j = 0; j < 4; ++j)              // 32 elements of K: 32 bytes, 2 in the descriptor's unit
+                    mma<NN>(d, da + 2 * j, db + 2 * j, sfa, sfb, kb > r0.kb0 || j > 0);
+                commit(empty + st);
             }
-            if (dead) {
+            commit(d_full + buf);
+        }
+        if (dead) {
+            if (lane == 0)
                 record_status(a.hdr, MOE_ERR_DEVICE_TIMEOUT);
-                commit(spare);                     // issued MMAs end before the CTA's memory goes away
-                wait_phase(spare, 0);
-            }
+            commit(spare);                     // issued MMAs end before the CTA's memory goes away
+            wait_phase(spare, 0);
         }
         __syncwarp();
+    } else if (warp >= 6) {
+        // ---- W's scale, warps in turn: a stage's blob is one byte throughout
+        long long it = 0;
+        bool dead = false;
+        for (int tile = r0.tile; tile < a.tiles && !dead; tile += r0.step) {
+            const uint8_t *wsrow = a.wscale + (size_t)(tile % a.n_tiles) * a.KB;
+            uint32_t wsc = 0;               // of 32 stages, a byte a lane
+            for (int kb = r0.kb0; kb < r0.kb1; ++kb, ++it) {
+                const int st = (int)(it % kStages), o = (kb - r0.kb0) & 31;
+                if (o == 0)
+                    wsc = kb + lane < r0.kb1 ? __ldg(wsrow + kb + lane) : 0;
+                if ((it & 1) != (warp & 1))
+                    continue;
+                if (it >= kStages && !__all_sync(0xffffffffu, wait_phase(empty + st, (uint32_t)((it / kStages - 1) & 1)))) {
+                    dead = true;
+                    break;
+                }
+                const uint32_t w = __shfl_sync(0xffffffffu, wsc, o) * 0x01010101u;
+                *reinterpret_cast<uint4 *>(sm + S::kOffSf + (size_t)st * S::kSf + lane * 16) = make_uint4(w, w, w, w);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(full + st);
+            }
+        }
     } else {
         // ---- accumulators to y (split: to shared memory, joined below)
         pdl_wait();
+        if (FUSED) {
+            // half a warp for each token and stage, four loads in flight
+            const int l = lane & 15, r = (warp - 2) * 2 + (lane >> 4), tok0 = r0.tile / a.n_tiles * NN;
+            constexpr int kPasses = 1, kAhead = 4;      // 8 tokens a pass
+            const int jobs = (r0.kb1 - r0.kb0) * kPasses;
+            bool dead = false;
+            for (int j0 = 0; j0 < jobs; j0 += kAhead) {
+                uint4 v[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int j = j0 + u, t = tok0 + j % kPasses * 8 + r, k = (r0.kb0 + j / kPasses) * 128 + l * 8;
+                    v[u] = j < jobs && t < a.T && k < a.K ? __ldg(reinterpret_cast<const uint4 *>(a.x + t * a.ldx + k)) : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int j = j0 + u, s = j / kPasses, row = j % kPasses * 8 + r, st = s % kStages;
+                    if (j >= jobs)
+                        break;
+                    if (s >= kStages && j % kPasses == 0 && !dead) {
+                        dead = !__all_sync(0xffffffffu, wait_phase(empty + st, (uint32_t)((s / kStages - 1) & 1)));
+                        if (dead && lane == 0)
+                            record_status(a.hdr, MOE_ERR_DEVICE_TIMEOUT);
+                    }
+                    uint32_t m = amax_bf16x8(v[u]);
+#pragma unroll
+                    for (int d = 8; d > 0; d >>= 1)
+                        m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+                    const int sc = fp8_scale_byte(m);
+                    if (tok0 + row < a.T) {
+                        // 128-byte rows, their 16-byte chunks permuted by the row within an atom of 8
+                        uint8_t *dst = sm + S::kOffB + (size_t)st * S::kB + row * 128 + (((l >> 1) ^ (row & 7)) << 4) + (l & 1) * 8;
+                        *reinterpret_cast<uint2 *>(dst) = fp8_from_bf16x8(v[u], exp2i(127 - sc));
+                        if (l == 0)
+                            reinterpret_cast<uint32_t *>(sm + S::kOffSf + (size_t)st * S::kSf + 512)[(row % 32) * 4 + row / 32] = sc * 0x01010101u;
+                    }
+                    if (j % kPasses == kPasses - 1) {
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(full + st);
+                    }
+                }
+            }
+        }
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         int piece = 0;
@@ -314,21 +399,38 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) fp8_gemm_kernel(const
         // the cluster's sums of the tile, each CTA adding every split-th token's; K ascends with the rank
         asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
         const int rank = blockIdx.x % a.split, tok0 = r0.tile / a.n_tiles * NN, toks = min(NN, a.T - tok0);
-        for (int i = tid; i < 128 * ((toks - rank + a.split - 1) / a.split); i += kThreads) {
-            const int row = i & 127, q = rank + (i >> 7) * a.split, n = r0.tile % a.n_tiles * 128 + row;
+        for (int i = tid; i < 32 * ((toks - rank + a.split - 1) / a.split); i += kThreads) {
+            const int row = (i & 31) * 4, q = rank + (i >> 5) * a.split, n = r0.tile % a.n_tiles * 128 + row;
             const uint32_t at = smem_u32(reinterpret_cast<float *>(sm) + q * 128 + row);
-            float sum = 0.0f;
+            float4 v[kMaxSplit];
 #pragma unroll
             for (int c = 0; c < kMaxSplit; ++c)
                 if (c < a.split) {
                     uint32_t remote;
-                    float v;
                     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(c));
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote));
-                    sum += v;
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[c].x), "=f"(v[c].y), "=f"(v[c].z), "=f"(v[c].w) : "r"(remote));
                 }
-            if (n < a.N)
-                store_bf16(a.y + (size_t)(tok0 + q) * a.N + n, sum);
+            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int c = 0; c < kMaxSplit; ++c)
+                if (c < a.split) {
+                    s[0] += v[c].x;
+                    s[1] += v[c].y;
+                    s[2] += v[c].z;
+                    s[3] += v[c].w;
+                }
+            uint16_t *dst = a.y + (size_t)(tok0 + q) * a.N + n;
+            if (n + 4 <= a.N && a.N % 4 == 0) {
+                uint32_t lo, hi;
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(s[1]), "f"(s[0]));
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(s[3]), "f"(s[2]));
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(lo, hi);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + e < a.N)
+                        store_bf16(dst + e, s[e]);
+            }
         }
         asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
@@ -422,14 +524,19 @@ struct Form {
         f.split = 1;
         if (f.split_form) {
             const int tiles = n_tiles * ((T + f.tile - 1) / f.tile);
-            f.split = 2 * sms / tiles;
-            f.split = f.split < 1 ? 1 : f.split > kMaxSplit ? kMaxSplit : f.split;
-            if (f.split > KB)
-                f.split = KB;
+            // the largest cluster of which all run at once: two CTAs on an SM, a cluster within one of the eight
+            // groups of SMs, a tenth to spare (7168 x 5120, 17 tokens: 10.9 us with 4, 16.4 with 5, whose 56 clusters
+            // just do not fit)
+            for (int s = 1; s <= kMaxSplit && s <= KB; ++s)
+                if (tiles * 11 <= 10 * 8 * (2 * (sms / 8) / s))
+                    f.split = s;
         }
         return f;
     }
 };
+
+// quantising x in the GEMM costs a stage about as much as its copies at 8 tokens; a kernel before it about 2 us
+constexpr int kFusedTokens = 8;
 
 struct Layout {
     size_t codes, scales, total;
@@ -452,15 +559,18 @@ struct Layout {
     }
 };
 
-template <int NN, bool SPLIT>
+template <int NN, bool SPLIT, bool FUSED>
 cudaError_t launch_gemm(const GemmArgs &a, const CUtensorMap &wmap, const uint8_t *codes, int ctas, cudaStream_t stream) {
     using S = Tile<NN, SPLIT>;
-    CUtensorMap xmap;
+    CUtensorMap xmap = wmap;                        // not read by the fused form
     const uint64_t dims[2] = {(uint64_t)a.KB * 128, (uint64_t)a.T}, str[1] = {(uint64_t)a.KB * 128};
     const uint32_t box[2] = {128, NN};
-    cudaError_t e = encode_tiled(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, codes, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    cudaError_t e = FUSED ? cudaSuccess
+                          : encode_tiled(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, codes, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(fp8_gemm_kernel<NN, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+        e = cudaFuncSetAttribute(fp8_gemm_kernel<NN, SPLIT, FUSED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    if (e == cudaSuccess && SPLIT)
+        e = cudaFuncSetAttribute(fp8_gemm_kernel<NN, SPLIT, FUSED>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
@@ -475,7 +585,7 @@ cudaError_t launch_gemm(const GemmArgs &a, const CUtensorMap &wmap, const uint8_
     attr[1].val.clusterDim = {(unsigned)a.split, 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<NN, SPLIT>, a, wmap, xmap);
+    return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<NN, SPLIT, FUSED>, a, wmap, xmap);
 }
 
 }  // namespace
@@ -508,18 +618,24 @@ cudaError_t launch_linear_fp8(const LinearProblem &p, void *ws, int sms, cudaStr
     cudaError_t e = encode_tiled(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p.codes, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess)
         return e;
+    a.x = p.x;
+    a.ldx = p.ldx;
+    a.K = p.K;
+    const int ctas = a.tiles * f.split;
+    if (f.split_form && p.T <= kFusedTokens)
+        return launch_gemm<16, true, true>(a, wmap, codes, ctas, stream);
     const int groups = p.T * KB, per = 16 * kQuantGroups;       // at most 2^29
     e = launch_pdl(fp8_quant_kernel, dim3((groups + per - 1) / per), dim3(256), 0, stream, p.x, p.ldx, p.T, p.K, KB,
                    f.tile, (f.tile + 127) / 128, codes, scales);
     if (e != cudaSuccess)
         return e;
     if (!f.split_form)
-        return launch_gemm<192, false>(a, wmap, codes, a.tiles < sms ? a.tiles : sms, stream);
+        return launch_gemm<192, false, false>(a, wmap, codes, a.tiles < sms ? a.tiles : sms, stream);
     switch (f.tile) {
-    case 16: return launch_gemm<16, true>(a, wmap, codes, a.tiles * f.split, stream);
-    case 32: return launch_gemm<32, true>(a, wmap, codes, a.tiles * f.split, stream);
-    case 64: return launch_gemm<64, true>(a, wmap, codes, a.tiles * f.split, stream);
-    default: return launch_gemm<128, true>(a, wmap, codes, a.tiles * f.split, stream);
+    case 16: return launch_gemm<16, true, false>(a, wmap, codes, ctas, stream);
+    case 32: return launch_gemm<32, true, false>(a, wmap, codes, ctas, stream);
+    case 64: return launch_gemm<64, true, false>(a, wmap, codes, ctas, stream);
+    default: return launch_gemm<128, true, false>(a, wmap, codes, ctas, stream);
     }
 }
 
