@@ -36,159 +36,17 @@
 // B operand of one MMA, or of two with 32 rows.  Thread (g, c) of a warp holds codes
 // 4c .. 4c+3, as K positions 2c, 2c+1, 2c+8, 2c+9: q's dims (and, for the
 // values, the weights' tokens) are taken in that order.
-#include "attn.h"
+#include "attn_plan.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kTile = 128;             // tokens of a tile
-constexpr int kSubs = kTile / 16;      // sub-blocks of a tile
 constexpr int kRows = 64;              // rows of a unit
 constexpr int kConsumers = 8;          // consumer warps
 constexpr int kThreads = 384;          // three warpgroups: two of consumers, one of producers
 constexpr int kQWarps = 3;
-constexpr int kUnitCost = 2;           // a unit's fixed work, in tiles
-constexpr int kMinCost = 4;            // least range of a CTA, in tiles
-constexpr int kPlanThreads = 1024;
 constexpr int kSmallRequests = 256;    // most requests and row tiles of a plan in shared memory
 constexpr int kSmallTiles = 288;
-constexpr unsigned long long kWaitLimitNs = 200ull * 1000 * 1000;
-
-// A row tile of a request.
-struct RowTile {
-    long long before;         // work of the row tiles before it (all heads), in tiles
-    int request, q0, n, kv;   // its first row of q, new tokens, tokens
-    int row0;                 // first row (of new tokens x group)
-    int tile0, tiles;         // cache tiles it sees
-};
-
-struct Plan {
-    long long work;        // of all units
-    long long per;         // of a CTA
-    int row_tiles, ctas;
-};
-
-struct AttnArgs {
-    AttnProblem p;
-    int group, shift;                    // query heads of a key/value head; log2(block_size)
-    int ctas, max_tiles;
-    float scale_log2;
-    Plan *plan;
-    RowTile *recs;
-    uint32_t *tickets;
-    float *part, *part_lse;
-    uint32_t *hdr;
-};
-
-// The positions that a row of a request with n new of kv tokens sees: [lo, hi).
-__device__ __forceinline__ void row_range(const AttnProblem &p, int group, int kv, int n, int row, int &lo, int &hi) {
-    const int pos = kv - n + row / group;
-    lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-    hi = p.causal ? max(0, min(kv, pos + 1)) : kv;
-    if (lo > hi)
-        lo = hi;
-}
-
-// ------------------------------------------------------------------- plan
-
-template <typename T>
-__device__ __forceinline__ T block_scan(T v, T *red, T *total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const T a = __shfl_up_sync(0xffffffffu, v, d);
-        if (lane >= d)
-            v += a;
-    }
-    __syncthreads();
-    if (lane == 31)
-        red[warp] = v;
-    __syncthreads();
-    T sum = 0, total_sum = 0;
-    for (int w = 0; w < nw; ++w) {
-        if (w < warp)
-            sum += red[w];
-        total_sum += red[w];
-    }
-    *total = total_sum;
-    return v + sum;
-}
-
-// The plan, by all threads of a CTA.  first: B ints, red: 32 words of shared
-// memory; recs in shared or global memory.
-__device__ __forceinline__ void make_plan(const AttnArgs &a, int *first, long long *red, RowTile *recs, Plan *plan, bool report) {
-    const AttnProblem &p = a.p;
-    const int tid = threadIdx.x, nt = blockDim.x;
-    const long long cap = (long long)p.max_blocks << a.shift;
-    int bad = 0;
-    long long carry = 0, total;
-    for (int b0 = 0; b0 < p.B; b0 += nt) {
-        const int b = b0 + tid;
-        long long c = 0;
-        if (b < p.B) {
-            const int lo = p.q_offsets[b], hi = p.q_offsets[b + 1], kv = p.kv_lens[b];
-            if (lo < 0 || hi < lo || hi > p.T || kv < 0 || kv > cap)
-                bad = 1;
-            else
-                c = ((long long)(hi - lo) * a.group + kRows - 1) / kRows;
-        }
-        const long long incl = block_scan(c, red, &total);
-        if (b < p.B)
-            first[b] = (int)min(carry + incl - c, (long long)a.max_tiles);
-        carry += total;
-    }
-    if (__syncthreads_or(bad) || carry > a.max_tiles) {
-        if (tid == 0) {
-            if (report)
-                record_status(a.hdr, MOE_ERR_DEVICE_ASSERT);
-            *plan = Plan{0, 1, 0, 0};
-        }
-        __syncthreads();
-        return;
-    }
-    const int n_recs = (int)carry;
-    carry = 0;
-    for (int i0 = 0; i0 < n_recs; i0 += nt) {
-        const int i = i0 + tid;
-        RowTile r{};
-        long long c = 0;
-        if (i < n_recs) {
-            int lo = 0, hi = p.B;               // the last request with first <= i
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (first[mid] <= i)
-                    lo = mid;
-                else
-                    hi = mid;
-            }
-            const int q0 = p.q_offsets[lo], n = p.q_offsets[lo + 1] - q0, kv = p.kv_lens[lo];
-            r.request = lo;
-            r.q0 = q0;
-            r.n = n;
-            r.kv = kv;
-            r.row0 = (i - first[lo]) * kRows;
-            const int last = min(r.row0 + kRows, n * a.group) - 1;
-            int l0, h0, l1, h1;
-            row_range(p, a.group, kv, n, r.row0, l0, h0);
-            row_range(p, a.group, kv, n, last, l1, h1);
-            // the first row sees furthest back, the last one furthest on
-            r.tile0 = l0 / kTile;
-            r.tiles = h1 > l0 ? (h1 + kTile - 1) / kTile - r.tile0 : 0;
-            c = (long long)(r.tiles + kUnitCost) * p.cache.kv_heads;
-        }
-        const long long incl = block_scan(c, red, &total);
-        r.before = carry + incl - c;
-        if (i < n_recs)
-            recs[i] = r;
-        carry += total;
-    }
-    if (tid == 0) {
-        const long long most = (carry + kMinCost - 1) / kMinCost;
-        const int used = (int)min((long long)a.ctas, most);
-        *plan = Plan{carry, used > 0 ? (carry + used - 1) / used : 1, n_recs, used};
-    }
-    __syncthreads();
-}
 
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnArgs a) {
     extern __shared__ int s_first[];
@@ -199,23 +57,6 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnArgs a) {
 }
 
 // -------------------------------------------------------------- attention
-
-// Wait for a phase; false after kWaitLimitNs.
-__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity))
-        return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity))
-        if (globaltimer_ns() - t0 > kWaitLimitNs)
-            return false;
-    return true;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -252,77 +93,6 @@ struct Smem {
     static constexpr size_t kBars = kFirst + kSmallRequests * 4;
     static constexpr size_t kBytes = kBars + (2 * kStages + 4) * 8 + 16;
     static_assert(kInfo % 16 == 0 && kJoin % 16 == 0 && kRecs % 8 == 0 && kBars % 8 == 0 && kBytes <= 227 * 1024, "shared memory");
-};
-
-// One unit's piece, as producers and consumers walk through it.
-struct Piece {
-    int request, head, row0, rows, q0, n, kv;
-    int tile0, t0, t1;            // cache tiles tile0 + [t0, t1)
-    int first, last;              // CTAs of the unit's first and last tile
-};
-
-// Walks a CTA's range.
-struct Walk {
-    const AttnArgs &a;
-    const RowTile *recs;
-    long long pos, end, base, per;
-    int rt, head, n_recs;
-    RowTile r;
-    __device__ Walk(const AttnArgs &args, const Plan &pl, const RowTile *tiles) : a(args), recs(tiles) {
-        n_recs = pl.row_tiles;
-        per = pl.per;
-        pos = (long long)blockIdx.x * per;
-        end = min(pos + per, pl.work);
-        rt = n_recs;
-        if ((int)blockIdx.x >= pl.ctas || pos >= pl.work)
-            return;
-        int lo = 0, hi = n_recs;                // the last row tile with before <= pos
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (recs[mid].before <= pos)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        rt = lo;
-        r = recs[rt];
-        head = (int)((pos - r.before) / (r.tiles + kUnitCost));
-        base = r.before + (long long)head * (r.tiles + kUnitCost);
-    }
-    // The next piece; false at the end of the range.
-    __device__ bool next(Piece &pc) {
-        while (rt < n_recs && base < end) {
-            const int lo = (int)min(max(pos - base - kUnitCost, 0ll), (long long)r.tiles);
-            const int hi = (int)max(min(end - base - kUnitCost, (long long)r.tiles), 0ll);
-            const bool mine = r.tiles == 0 ? base >= pos : hi > lo;
-            if (mine) {
-                pc.request = r.request;
-                pc.head = head;
-                pc.row0 = r.row0;
-                pc.q0 = r.q0;
-                pc.n = r.n;
-                pc.kv = r.kv;
-                pc.rows = min(kRows, r.n * a.group - r.row0);
-                pc.tile0 = r.tile0;
-                pc.t0 = lo;
-                pc.t1 = hi;
-                pc.first = pc.last = (int)blockIdx.x;
-                if (r.tiles > 0) {
-                    pc.first = (int)((base + kUnitCost) / per);
-                    pc.last = (int)((base + kUnitCost + r.tiles - 1) / per);
-                }
-            }
-            base += r.tiles + kUnitCost;
-            if (++head == a.p.cache.kv_heads) {
-                head = 0;
-                if (++rt < n_recs)
-                    r = recs[rt];
-            }
-            if (mine)
-                return true;
-        }
-        return false;
-    }
 };
 
 // Up to four tiles of a piece: a lane for each of their sub-blocks.
@@ -950,18 +720,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     }
 }
 
-int max_row_tiles(int T, int B, int group) { return (int)((long long)T * group / kRows + B); }
+int max_row_tiles(int T, int B, int group, int rows) { return (int)((long long)T * group / rows + B); }
 
 }  // namespace
 
 AttnLayout AttnLayout::make(int T, int B, int q_heads, int kv_heads, int head_dim) {
     AttnLayout L{};
+    const int group = q_heads / kv_heads;
+    const long long rows = (long long)T * group;
     size_t o = kInitBytes;
     auto take = [&](size_t bytes) { o = align_up(o, 256); size_t r = o; o += bytes; return r; };
     L.plan = take(sizeof(Plan));
-    L.recs = take((size_t)max_row_tiles(T, B, q_heads / kv_heads) * sizeof(RowTile));
-    L.part = take((size_t)2 * kMaxAttnCtas * kRows * head_dim * sizeof(float));
-    L.part_lse = take((size_t)2 * kMaxAttnCtas * kRows * sizeof(float));
+    L.recs = take((size_t)max_row_tiles(T, B, group, kRows) * sizeof(RowTile));
+    // a CTA has parts of at most two units; in the tensor-memory form of up to two row halves or token halves each
+    const size_t cut = rows < kRows ? rows : kRows, tall = rows <= kAttnTcMinRows ? 0 : rows < 128 ? rows : 128;
+    const size_t parts = (size_t)kMaxAttnCtas * (2 * cut > 4 * tall ? 2 * cut : 4 * tall);
+    L.part = take(parts * head_dim * sizeof(float));
+    L.part_lse = take(parts * sizeof(float));
+    L.nans = take(tall ? (size_t)kMaxAttnCtas * kAttnNanBytes : 0);
     L.total = align_up(o, 256);
     return L;
 }
@@ -972,18 +748,26 @@ cudaError_t launch_kv_attention(const AttnProblem &p, void *ws, int sms, cudaStr
     int shift = 4;
     while ((1 << shift) < p.cache.block_size)
         ++shift;
-    const AttnArgs a{p, group, shift, sms < kMaxAttnCtas ? sms : kMaxAttnCtas, max_row_tiles(p.T, p.B, group),
-                     p.scale * 1.44269504088896340736f, ws_at<Plan>(ws, L.plan), ws_at<RowTile>(ws, L.recs),
-                     ws_at<uint32_t>(ws, kHeaderBytes), ws_at<float>(ws, L.part), ws_at<float>(ws, L.part_lse), ws_at<uint32_t>(ws, 0)};
+    AttnArgs a{p, group, shift, kRows, sms < kMaxAttnCtas ? sms : kMaxAttnCtas, max_row_tiles(p.T, p.B, group, kRows),
+               p.scale * 1.44269504088896340736f, ws_at<Plan>(ws, L.plan), ws_at<RowTile>(ws, L.recs),
+               ws_at<uint32_t>(ws, kHeaderBytes), ws_at<float>(ws, L.part), ws_at<float>(ws, L.part_lse),
+               ws_at<uint8_t>(ws, L.nans), ws_at<uint32_t>(ws, 0)};
+    const bool tall = (long long)p.T * group > (long long)kAttnTcMinRows * p.B;
     auto go = [&](auto kernel, size_t smem) {
         cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         return r != cudaSuccess ? r : launch_pdl(kernel, dim3(a.ctas), dim3(kThreads), smem, stream, a);
     };
-    if (p.B <= kSmallRequests && a.max_tiles <= kSmallTiles)
+    if (!tall && p.B <= kSmallRequests && a.max_tiles <= kSmallTiles)
         return p.cache.head_dim == 64 ? go(attn_kernel<64, true>, Smem<64>::kBytes) : go(attn_kernel<128, true>, Smem<128>::kBytes);
+    if (tall) {
+        a.rows = kAttnTcRows;
+        a.max_tiles = max_row_tiles(p.T, p.B, group, kAttnTcRows);
+    }
     cudaError_t e = launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), p.B * sizeof(int), stream, a);
     if (e != cudaSuccess)
         return e;
+    if (tall)
+        return launch_attn_tc(&a, p.cache.head_dim, a.ctas, stream);
     return p.cache.head_dim == 64 ? go(attn_kernel<64, false>, Smem<64>::kBytes) : go(attn_kernel<128, false>, Smem<128>::kBytes);
 }
 

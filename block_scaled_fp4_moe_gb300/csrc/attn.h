@@ -106,9 +106,15 @@ struct AttnProblem {
 };
 // Workspace regions of the attention.
 struct AttnLayout {
-    size_t plan, recs, part, part_lse, total;
+    size_t plan, recs, part, part_lse, nans, total;
     static AttnLayout make(int T, int B, int q_heads, int kv_heads, int head_dim);
 };
+// The tensor-memory form (attn_tc.cu) for requests of more than this many rows on average, its units' rows, and the
+// bytes of a CTA's list of NaN values.
+constexpr int kAttnTcMinRows = 64;
+constexpr int kAttnTcRows = 256;
+constexpr size_t kAttnNanBytes = 2048 * 32;
+cudaError_t launch_attn_tc(const void *args, int head_dim, int ctas, cudaStream_t stream);
 cudaError_t launch_kv_attention(const AttnProblem &p, void *ws, int sms, cudaStream_t stream);
 
 size_t linear_fp8_workspace(int T, int N, int K);

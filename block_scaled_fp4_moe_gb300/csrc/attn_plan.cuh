@@ -1,0 +1,247 @@
+// attn_plan.cuh -- what the two attention kernels share: units of work, the
+// plan that lists them, and a CTA's walk through its range (attn.cu says how).
+#pragma once
+
+#include "attn.h"
+
+namespace moe {
+namespace {
+
+constexpr int kTile = 128;             // tokens of a tile
+constexpr int kSubs = kTile / 16;      // sub-blocks of a tile
+constexpr int kUnitCost = 2;           // a unit's fixed work, in tiles
+constexpr int kMinCost = 4;            // least range of a CTA, in tiles
+constexpr int kPlanThreads = 1024;
+constexpr unsigned long long kWaitLimitNs = 200ull * 1000 * 1000;
+
+// A row tile of a request.
+struct RowTile {
+    long long before;         // work of the row tiles before it (all heads), in tiles
+    int request, q0, n, kv;   // its first row of q, new tokens, tokens
+    int row0;                 // first row (of new tokens x group)
+    int tile0, tiles;         // cache tiles it sees
+};
+
+struct Plan {
+    long long work;        // of all units
+    long long per;         // of a CTA
+    int row_tiles, ctas;
+};
+
+struct AttnArgs {
+    AttnProblem p;
+    int group, shift;                    // query heads of a key/value head; log2(block_size)
+    int rows;                            // of a unit
+    int ctas, max_tiles;
+    float scale_log2;
+    Plan *plan;
+    RowTile *recs;
+    uint32_t *tickets;
+    float *part, *part_lse;              // parts of cut units
+    void *nans;                          // lists of NaN values (attn_tc.cu)
+    uint32_t *hdr;
+};
+
+// The positions that a row of a request with n new of kv tokens sees: [lo, hi).
+__device__ __forceinline__ void row_range(const AttnProblem &p, int group, int kv, int n, int row, int &lo, int &hi) {
+    const int pos = kv - n + row / group;
+    lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+    hi = p.causal ? max(0, min(kv, pos + 1)) : kv;
+    if (lo > hi)
+        lo = hi;
+}
+
+// ------------------------------------------------------------------- plan
+
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T *red, T *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const T a = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d)
+            v += a;
+    }
+    __syncthreads();
+    if (lane == 31)
+        red[warp] = v;
+    __syncthreads();
+    T sum = 0, total_sum = 0;
+    for (int w = 0; w < nw; ++w) {
+        if (w < warp)
+            sum += red[w];
+        total_sum += red[w];
+    }
+    *total = total_sum;
+    return v + sum;
+}
+
+// The plan, by all threads of a CTA.  first: B ints, red: 32 words of shared
+// memory; recs in shared or global memory.
+__device__ __forceinline__ void make_plan(const AttnArgs &a, int *first, long long *red, RowTile *recs, Plan *plan, bool report) {
+    const AttnProblem &p = a.p;
+    const int tid = threadIdx.x, nt = blockDim.x;
+    const long long cap = (long long)p.max_blocks << a.shift;
+    int bad = 0;
+    long long carry = 0, total;
+    for (int b0 = 0; b0 < p.B; b0 += nt) {
+        const int b = b0 + tid;
+        long long c = 0;
+        if (b < p.B) {
+            const int lo = p.q_offsets[b], hi = p.q_offsets[b + 1], kv = p.kv_lens[b];
+            if (lo < 0 || hi < lo || hi > p.T || kv < 0 || kv > cap)
+                bad = 1;
+            else
+                c = ((long long)(hi - lo) * a.group + a.rows - 1) / a.rows;
+        }
+        const long long incl = block_scan(c, red, &total);
+        if (b < p.B)
+            first[b] = (int)min(carry + incl - c, (long long)a.max_tiles);
+        carry += total;
+    }
+    if (__syncthreads_or(bad) || carry > a.max_tiles) {
+        if (tid == 0) {
+            if (report)
+                record_status(a.hdr, MOE_ERR_DEVICE_ASSERT);
+            *plan = Plan{0, 1, 0, 0};
+        }
+        __syncthreads();
+        return;
+    }
+    const int n_recs = (int)carry;
+    carry = 0;
+    for (int i0 = 0; i0 < n_recs; i0 += nt) {
+        const int i = i0 + tid;
+        RowTile r{};
+        long long c = 0;
+        if (i < n_recs) {
+            int lo = 0, hi = p.B;               // the last request with first <= i
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (first[mid] <= i)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            const int q0 = p.q_offsets[lo], n = p.q_offsets[lo + 1] - q0, kv = p.kv_lens[lo];
+            r.request = lo;
+            r.q0 = q0;
+            r.n = n;
+            r.kv = kv;
+            r.row0 = (i - first[lo]) * a.rows;
+            const int last = min(r.row0 + a.rows, n * a.group) - 1;
+            int l0, h0, l1, h1;
+            row_range(p, a.group, kv, n, r.row0, l0, h0);
+            row_range(p, a.group, kv, n, last, l1, h1);
+            // the first row sees furthest back, the last one furthest on
+            r.tile0 = l0 / kTile;
+            r.tiles = h1 > l0 ? (h1 + kTile - 1) / kTile - r.tile0 : 0;
+            c = (long long)(r.tiles + kUnitCost) * p.cache.kv_heads;
+        }
+        const long long incl = block_scan(c, red, &total);
+        r.before = carry + incl - c;
+        if (i < n_recs)
+            recs[i] = r;
+        carry += total;
+    }
+    if (tid == 0) {
+        const long long most = (carry + kMinCost - 1) / kMinCost;
+        const int used = (int)min((long long)a.ctas, most);
+        *plan = Plan{carry, used > 0 ? (carry + used - 1) / used : 1, n_recs, used};
+    }
+    __syncthreads();
+}
+
+// Wait for a phase; false after kWaitLimitNs.
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity))
+        return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > kWaitLimitNs)
+            return false;
+    return true;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// One unit's piece, as producers and consumers walk through it.
+struct Piece {
+    int request, head, row0, rows, q0, n, kv;
+    int tile0, t0, t1;            // cache tiles tile0 + [t0, t1)
+    int first, last;              // CTAs of the unit's first and last tile
+    int first_tiles, last_tiles;  // the unit's tiles in those (where they differ)
+};
+
+// Walks a CTA's range.
+struct Walk {
+    const AttnArgs &a;
+    const RowTile *recs;
+    long long pos, end, base, per;
+    int rt, head, n_recs;
+    RowTile r;
+    __device__ Walk(const AttnArgs &args, const Plan &pl, const RowTile *tiles) : a(args), recs(tiles) {
+        n_recs = pl.row_tiles;
+        per = pl.per;
+        pos = (long long)blockIdx.x * per;
+        end = min(pos + per, pl.work);
+        rt = n_recs;
+        if ((int)blockIdx.x >= pl.ctas || pos >= pl.work)
+            return;
+        int lo = 0, hi = n_recs;                // the last row tile with before <= pos
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (recs[mid].before <= pos)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        rt = lo;
+        r = recs[rt];
+        head = (int)((pos - r.before) / (r.tiles + kUnitCost));
+        base = r.before + (long long)head * (r.tiles + kUnitCost);
+    }
+    // The next piece; false at the end of the range.
+    __device__ bool next(Piece &pc) {
+        while (rt < n_recs && base < end) {
+            const int lo = (int)min(max(pos - base - kUnitCost, 0ll), (long long)r.tiles);
+            const int hi = (int)max(min(end - base - kUnitCost, (long long)r.tiles), 0ll);
+            const bool mine = r.tiles == 0 ? base >= pos : hi > lo;
+            if (mine) {
+                pc.request = r.request;
+                pc.head = head;
+                pc.row0 = r.row0;
+                pc.q0 = r.q0;
+                pc.n = r.n;
+                pc.kv = r.kv;
+                pc.rows = min(a.rows, r.n * a.group - r.row0);
+                pc.tile0 = r.tile0;
+                pc.t0 = lo;
+                pc.t1 = hi;
+                pc.first = pc.last = (int)blockIdx.x;
+                if (r.tiles > 0) {
+                    pc.first = (int)((base + kUnitCost) / per);
+                    pc.last = (int)((base + kUnitCost + r.tiles - 1) / per);
+                    pc.first_tiles = (int)min((pc.first + 1) * per - base - kUnitCost, (long long)r.tiles);
+                    pc.last_tiles = (int)(base + kUnitCost + r.tiles - pc.last * per);
+                }
+            }
+            base += r.tiles + kUnitCost;
+            if (++head == a.p.cache.kv_heads) {
+                head = 0;
+                if (++rt < n_recs)
+                    r = recs[rt];
+            }
+            if (mine)
+                return true;
+        }
+        return false;
+    }
+};
+
+}  // namespace
+}  // namespace moe

@@ -61,11 +61,11 @@ constexpr size_t kCtaStampOffset = kHdrWords * sizeof(uint32_t);
 constexpr int kFusedMaxCtaStamps = 256;
 constexpr size_t kHeaderBytes = kCtaStampOffset + kFusedMaxCtaStamps * 4 * sizeof(unsigned long long);
 
-// Behind them the attention's arrival counters, one per CTA of its grid, which
+// Behind them the attention's arrival counters, two per CTA of its grid, which
 // every completed call leaves at zero (attn.cu).  moe_workspace_init clears
 // all of this; the calls' regions begin after it.
-constexpr int kMaxAttnCtas = 256;
-constexpr size_t kInitBytes = kHeaderBytes + kMaxAttnCtas * sizeof(uint32_t);
+constexpr int kMaxAttnCtas = 160;
+constexpr size_t kInitBytes = kHeaderBytes + 512 * sizeof(uint32_t);
 
 // Most K pieces the tensor-memory FFN kernels split their last items into.
 constexpr int kTcMaxPieces = 256;

@@ -153,7 +153,7 @@ size_t moe_workspace_size(int T, int H, int I, int E, int top_k, int has_shared)
 size_t moe_workspace_offset(int T, int H, int I, int E, int top_k, int has_shared, const char *region);
 
 /* Clears the workspace header (status word, counters and diagnostics, the
- * first 9,728 bytes or ws_bytes if smaller) on `stream`.  Call it once on a newly
+ * first 10,752 bytes or ws_bytes if smaller) on `stream`.  Call it once on a newly
  * allocated workspace before its first use (a zero-filled workspace needs no
  * call), and after a call that reported MOE_ERR_DEVICE_TIMEOUT.  ws: device
  * pointer, 256-byte aligned; ws_bytes at least 512. */
