@@ -111,7 +111,7 @@ struct AttnLayout {
 };
 // The tensor-memory form (attn_tc.cu) for requests of more than this many rows on average, its units' rows, and the
 // bytes of a CTA's list of NaN values.
-constexpr int kAttnTcMinRows = 64;
+constexpr int kAttnTcMinRows = 24;
 constexpr int kAttnTcRows = 256;
 constexpr size_t kAttnNanBytes = 2048 * 32;
 cudaError_t launch_attn_tc(const void *args, int head_dim, int ctas, cudaStream_t stream);

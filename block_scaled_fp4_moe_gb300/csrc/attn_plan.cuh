@@ -224,8 +224,14 @@ struct Walk {
                 pc.t1 = hi;
                 pc.first = pc.last = (int)blockIdx.x;
                 if (r.tiles > 0) {
-                    pc.first = (int)((base + kUnitCost) / per);
-                    pc.last = (int)((base + kUnitCost + r.tiles - 1) / per);
+                    const long long t0 = base + kUnitCost, t1 = t0 + r.tiles - 1;
+                    if (t1 < 0x7FFFFFFF) {     // the usual sizes: 32-bit divisions
+                        pc.first = (int)((uint32_t)t0 / (uint32_t)per);
+                        pc.last = (int)((uint32_t)t1 / (uint32_t)per);
+                    } else {
+                        pc.first = (int)(t0 / per);
+                        pc.last = (int)(t1 / per);
+                    }
                     pc.first_tiles = (int)min((pc.first + 1) * per - base - kUnitCost, (long long)r.tiles);
                     pc.last_tiles = (int)(base + kUnitCost + r.tiles - pc.last * per);
                 }

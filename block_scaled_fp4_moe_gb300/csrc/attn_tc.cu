@@ -7,29 +7,32 @@
 // codes that every warp of a tile repeats and the softmax share the same issue slots: 64 rows ran
 // at 29 % of the mma.sync rate.  Here the codes are converted once for up to 256 rows, and the products cost no issue slots.
 //
-// A unit has up to 256 rows.  Two warpgroups ("halves") each own 128 TMEM lanes = rows: with more than 128 rows
+// A unit has up to 256 rows.  Two "halves" each own 128 TMEM lanes = rows: with more than 128 rows
 // the halves take rows 0..127 and 128..255 of every tile; with up to 128 they take the same
 // rows and every other tile, and their sums are joined like those of two CTAs.  Half h: S_h = Q_h K^T
-// (M = 128 rows, N = 128 tokens) in TMEM columns 128 h.., the f16 weights over the scores just
-// read (64 columns), O_h += W_h V (A in TMEM, N = head dim) in columns 256 + D h...  One half's softmax runs beside the
-// other half's products.
+// (M = 128 rows, N = 128 tokens) in TMEM columns 128 h.., the f16 weights W_h, O_h += W_h V (A in TMEM, N = head
+// dim) in columns 256 + D h...  At D = 64 the weights have columns of their own and the next scores are issued before the
+// product that they wait for; at D = 128 they lie over the scores just read.  One half's softmax runs
+// beside the other half's products.
 //
-// Warps: 0..7 softmax (thread = row; warp % 4 = TMEM lane quarter), 8..11 convert, 12 streams the
-// cache, 13 issues the MMAs.  The operands pass in the order K0, K1, V0, K2, V1, ...: as codes into a ring of raw tiles
+// Warps: 0..7 softmax (warp % 4 = TMEM lane quarter, warp / 4 the half; a thread has a row), 8..13 convert, 14 streams the cache, 15 issues the
+// MMAs.  What bounds it is the issue of the softmax and of the conversion.  (Two threads to a row, 16 warps of at most 88 registers, took as long:
+// more latency hidden, more moves and exchanges.)  The operands pass in the order K0, K1, V0, K2, V1, ...: as codes into a ring of raw tiles
 // by bulk copies, then as f16 into a ring of operand tiles, rows (tokens of K, dims of V) of 64
 // elements in the 128-byte swizzle.  The cache's innermost 16 bytes run along the summed axis for both, so the two
 // conversions are the same code.
 //
-// The running maximum M of a row moves only when it has grown by more than 2^8 (w stays below 2^8 and f16's
-// rounding is relative): then the half waits for its last product and rescales O in TMEM.
+// The running maxima of a row are references that move only where a score has outgrown them (M by 2^8: w stays below
+// that, and f16's rounding is relative): then the half waits for its last product and rescales O in TMEM.  Where the
+// weights have columns of their own a tile is tried with the references as they are and made again if they move: its
+// scores are read once.
 #include "attn_plan.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kTcThreads = 14 * 32;
-constexpr int kConvWarps = 4;
-constexpr int kMetaTiles = 16;
+constexpr int kSoftWarps = 8, kConvWarps = 6;
+constexpr int kTcThreads = (kSoftWarps + kConvWarps + 2) * 32;
 constexpr int kNanEntries = 2048;
 constexpr float kLazy = 8.0f;
 
@@ -47,12 +50,16 @@ struct TcSmem {
     static constexpr int kOpBytes = 2 * kTile * D;           // in f16
     static constexpr int kRaw = D == 128 ? 4 : 8, kOps = D == 128 ? 3 : 4;
     static constexpr int kQBytes = 128 * D * 2;              // of a half
+    // tiles whose exponents are kept: the stream is at most (kRaw + kOps + 1) / 2 + 1 ahead of the softmax
+    static constexpr int kMetaTiles = D == 128 ? 8 : 16;
     static constexpr size_t kOffOps = 2 * kQBytes;
     static constexpr size_t kOffRaw = kOffOps + (size_t)kOps * kOpBytes;
     static constexpr size_t kOffMeta = kOffRaw + (size_t)kRaw * kRawBytes;     // float [tile][2][kSubs]
     static constexpr size_t kOffBars = kOffMeta + kMetaTiles * 2 * kSubs * 4;
+    static constexpr bool kOwnW = D == 64;                   // weights in columns of their own
+    __host__ __device__ static constexpr int w_col(int h, int tok) { return kOwnW ? 384 + 64 * h + tok / 2 : 128 * h + (tok >= 64 ? 64 : 0) + (tok % 64) / 2; }
     static constexpr int kBarCount = 2 * kRaw + 2 * kOps + 8 + 1;
-    static constexpr size_t kBytes = kOffBars + kBarCount * 8 + 64 + 1024;     // + alignment to 1024
+    static constexpr size_t kBytes = kOffBars + kBarCount * 8 + 32 + 1024;     // + alignment to 1024
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -90,19 +97,20 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
         : "memory");
 }
 
+// The load and its wait are one statement: nothing that uses v can come between.
 __device__ __forceinline__ void tmem_ld32(float (&v)[32], uint32_t addr) {
     uint32_t *u = reinterpret_cast<uint32_t *>(v);
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
-        "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        "tcgen05.wait::ld.sync.aligned;"
         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]), "=r"(u[9]),
           "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]),
           "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]),
           "=r"(u[30]), "=r"(u[31])
-        : "r"(addr));
+        : "r"(addr)
+        : "memory");
 }
-
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // Two fp32 values in one instruction each.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -230,7 +238,7 @@ __device__ __forceinline__ void tc_stream(const AttnArgs &a, const Plan &pl, uin
                     }
                     const bool mine = lane / kSubs == at;
                     if (!is_v && mine) {
-                        float *m = reinterpret_cast<float *>(sm + S::kOffMeta) + ((tile + t) % kMetaTiles) * 2 * kSubs + sub;
+                        float *m = reinterpret_cast<float *>(sm + S::kOffMeta) + ((tile + t) % S::kMetaTiles) * 2 * kSubs + sub;
                         m[0] = exp2i(min(max(ks, 1), 254) - 127);
                         m[kSubs] = (float)(vs - 127);
                     }
@@ -267,7 +275,7 @@ __device__ __forceinline__ void tc_stream(const AttnArgs &a, const Plan &pl, uin
 template <int D>
 __device__ __forceinline__ void tc_convert(const AttnArgs &a, const Plan &pl, uint8_t *sm, const Bars &b, uint32_t *nan_count) {
     using S = TcSmem<D>;
-    const int tid = threadIdx.x - 256, lane = tid & 31;
+    const int tid = threadIdx.x - kSoftWarps * 32, lane = tid & 31;
     NanEntry *nans = reinterpret_cast<NanEntry *>(static_cast<uint8_t *>(a.nans) + (size_t)blockIdx.x * kAttnNanBytes);
     Walk walk(a, pl, a.recs);
     Piece pc;
@@ -317,17 +325,19 @@ __device__ __forceinline__ void tc_convert(const AttnArgs &a, const Plan &pl, ui
             constexpr int kUnits = kTile * D / 16, kStep = kConvWarps * 32;
             if (!edge) {
 #pragma unroll 1
-                for (int u0 = tid; u0 < kUnits; u0 += 4 * kStep) {
-                    uint4 c[4];
+                for (int u0 = tid; u0 < kUnits; u0 += 3 * kStep) {
+                    uint4 c[3];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        c[i] = raw[u0 + i * kStep];
+                    for (int i = 0; i < 3; ++i)
+                        if (u0 + i * kStep < kUnits)
+                            c[i] = raw[u0 + i * kStep];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        int row, chunk;
-                        place(u0 + i * kStep, row, chunk);
-                        store(c[i], row, chunk);
-                    }
+                    for (int i = 0; i < 3; ++i)
+                        if (u0 + i * kStep < kUnits) {
+                            int row, chunk;
+                            place(u0 + i * kStep, row, chunk);
+                            store(c[i], row, chunk);
+                        }
                 }
             } else {
 #pragma unroll 1
@@ -402,7 +412,7 @@ __device__ __forceinline__ void tc_issue(const AttnArgs &a, const Plan &pl, uint
         if (!dead) {
 #pragma unroll
             for (int j = 0; j < kTile / 16; ++j)       // atoms of 64 tokens: D rows x 128 bytes
-                mma_ts<D>(tmem + 256 + D * h, tmem + 128 * h + 8 * j, dv + (j >> 2) * (D * 8) + (j & 3) * 2, !first || j > 0);
+                mma_ts<D>(tmem + 256 + D * h, tmem + S::w_col(h, 16 * j), dv + (j >> 2) * (D * 8) + (j & 3) * 2, !first || j > 0);
         }
         commit(b.o_done + h);
     };
@@ -434,34 +444,43 @@ __device__ __forceinline__ void tc_issue(const AttnArgs &a, const Plan &pl, uint
             scores(1, op + k_order(1));
             commit(b.op_empty + (op + k_order(1)) % S::kOps);
         }
+        // weights of a tile are the sign that its scores were read too
+        auto half_step = [&](int h, uint32_t ov, bool first, uint32_t ok, bool more) {
+            weights(h);
+            if (S::kOwnW && more)
+                scores(h, ok);
+            values(h, ov, first);
+            if (!S::kOwnW && more)
+                scores(h, ok);
+        };
         for (int t = 0; t < n; ++t) {
             const uint32_t ov = op + v_order(t, n);
+            const int tk = pair ? t + 1 : t + 2;
+            const bool more = tk < n;
+            const uint32_t ok = op + k_order(tk);
             if (pair) {
-                const uint32_t ok = op + k_order(t + 1);
-                weights(0);
-                acquire(ov);
-                values(0, ov, t == 0);
-                if (t + 1 < n) {
+                if (more)
                     acquire(ok);
-                    scores(0, ok);
-                }
-                weights(1);
-                values(1, ov, t == 0);
+                acquire(ov);
+                half_step(0, ov, t == 0, ok, more);
+                half_step(1, ov, t == 0, ok, more);
                 commit(b.op_empty + ov % S::kOps);
-                if (t + 1 < n) {
-                    scores(1, ok);
+                if (more)
+                    commit(b.op_empty + ok % S::kOps);
+            } else {
+                acquire(ov);
+                if (more && S::kOwnW)
+                    acquire(ok);
+                weights(t & 1);
+                if (S::kOwnW && more) {
+                    scores(t & 1, ok);
                     commit(b.op_empty + ok % S::kOps);
                 }
-            } else {
-                const int h = t & 1;
-                weights(h);
-                acquire(ov);
-                values(h, ov, t < 2);
+                values(t & 1, ov, t < 2);
                 commit(b.op_empty + ov % S::kOps);
-                if (t + 2 < n) {
-                    const uint32_t ok = op + k_order(t + 2);
+                if (!S::kOwnW && more) {
                     acquire(ok);
-                    scores(h, ok);
+                    scores(t & 1, ok);
                     commit(b.op_empty + ok % S::kOps);
                 }
             }
@@ -479,12 +498,14 @@ struct Workers {
     int count, slot, ticket;
 };
 
-// Scores of positions outside [lo, hi) to -infinity; x holds those of k .. k + 63.
-__device__ __forceinline__ void hide(float (&x)[2][32], int k, int lo, int hi) {
+// Scores of positions outside [lo, hi) to -infinity; x holds those of k .. k + 31.
+// The warp-wide step keeps it behind a branch: as predicated instructions it cost every tile 400 issue slots a warp.
+__device__ __forceinline__ void hide(float (&x)[32], int k, int lo, int hi) {
+    __syncwarp();
 #pragma unroll
-    for (int e = 0; e < 64; ++e)
+    for (int e = 0; e < 32; ++e)
         if (k + e < lo || k + e >= hi)
-            x[e >> 5][e & 31] = -INFINITY;
+            x[e] = -INFINITY;
 }
 
 template <int D>
@@ -492,7 +513,8 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
                                            uint32_t *nan_count, int *s_last) {
     using S = TcSmem<D>;
     const AttnProblem &p = a.p;
-    const int h = threadIdx.x >> 7, tid = threadIdx.x & 127, lane = tid & 31;      // tid = TMEM lane = row
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int h = warp >> 2, tid = threadIdx.x & 127;                                   // tid = TMEM lane = row
     const uint32_t lanes = tmem + ((uint32_t)(tid & ~31) << 16), s_at = lanes + 128 * h, o_at = lanes + 256 + D * h;
     uint8_t *q_at = sm + (size_t)h * S::kQBytes + tid * 128;
     uint32_t sn = 0, on = 0, tile = 0;             // score tiles and products of this half, tiles of the CTA
@@ -512,7 +534,7 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
         const bool pair = pc.rows > 128;
         const int mine = half_tiles(pc, pair, h);
         const int rr = pair ? 128 * h + tid : tid;
-        const bool live = rr < pc.rows;
+        const bool live = rr < pc.rows, idle = (rr & ~31) >= pc.rows;
         const int row = pc.row0 + (live ? rr : 0);
         if (mine == 0 && (n > 0 || (h > 0 && !pair))) {     // one tile for two halves, or none: the first half's
             tile += n;
@@ -520,21 +542,23 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
         }
         // the row's query, scaled into f16, and its limits
         const uint16_t *src = p.q + (int64_t)(pc.q0 + row / a.group) * p.q_st + (int64_t)(pc.head * a.group + row % a.group) * p.q_sh;
+        uint2 raw[D / 4];
         float mx = 0.0f;
-#pragma unroll 4
-        for (int j = 0; j < D / 4; ++j) {
-            const uint2 v = live ? __ldg(reinterpret_cast<const uint2 *>(src + 4 * j)) : make_uint2(0, 0);
-            mx = fmaxf(mx, fmaxf(fmaxf(fabsf(__uint_as_float(v.x << 16)), fabsf(__uint_as_float(v.x & 0xFFFF0000u))),
-                                 fmaxf(fabsf(__uint_as_float(v.y << 16)), fabsf(__uint_as_float(v.y & 0xFFFF0000u)))));
-        }
+#pragma unroll
+        for (int j = 0; j < D / 4; ++j)
+            raw[j] = live ? __ldg(reinterpret_cast<const uint2 *>(src + 4 * j)) : make_uint2(0, 0);
+#pragma unroll
+        for (int j = 0; j < D / 4; ++j)
+            mx = fmaxf(mx, fmaxf(fmaxf(fabsf(__uint_as_float(raw[j].x << 16)), fabsf(__uint_as_float(raw[j].x & 0xFFFF0000u))),
+                                 fmaxf(fabsf(__uint_as_float(raw[j].y << 16)), fabsf(__uint_as_float(raw[j].y & 0xFFFF0000u)))));
         const int sh = f16_shift_for_max(mx);
         const float sc = exp2i(sh), f = a.scale_log2 * exp2i(-sh);
-#pragma unroll 4
+#pragma unroll
         for (int j = 0; j < D / 8; ++j) {
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const uint2 v = live ? __ldg(reinterpret_cast<const uint2 *>(src + 8 * j + 4 * e)) : make_uint2(0, 0);
+                const uint2 v = raw[2 * j + e];
                 const __half2 x = __floats2half2_rn(__uint_as_float(v.x << 16) * sc, __uint_as_float(v.x & 0xFFFF0000u) * sc);
                 const __half2 y = __floats2half2_rn(__uint_as_float(v.y << 16) * sc, __uint_as_float(v.y & 0xFFFF0000u) * sc);
                 w[2 * e] = *reinterpret_cast<const uint32_t *>(&x);
@@ -551,96 +575,120 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
             row_range(p, a.group, pc.kv, pc.n, row, lo, hi);
         const int min_hi = __reduce_min_sync(0xffffffffu, hi), max_lo = __reduce_max_sync(0xffffffffu, lo);
 
-        float m = -INFINITY, big = -INFINITY, l = 0.0f;
+        float m = -INFINITY, big = -INFINITY, l = 0.0f;     // references, and l with respect to m
         for (int i = 0; i < mine; ++i) {
             const int t = pair ? i : 2 * i + h;
             const int tok0 = (pc.tile0 + pc.t0 + t) * kTile;
-            const bool edge = tok0 + kTile > min_hi || tok0 < max_lo;
             wait(b.s_full + h, sn & 1);
             ++sn;
-            const float *meta = reinterpret_cast<const float *>(sm + S::kOffMeta) + ((tile + t) % kMetaTiles) * 2 * kSubs;
-            // maxima: m over x, M over x + b
-            float nm = m, nb = big;
-#pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-                float x[2][32];
-                tmem_ld32(x[0], s_at + 64 * c);
-                tmem_ld32(x[1], s_at + 64 * c + 32);
-                tmem_wait_ld();
-                if (edge)
-                    hide(x, tok0 + 64 * c, lo, hi);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const float *y = x[u >> 1] + 16 * (u & 1);
+            if (!idle) {
+                const bool edge = tok0 + kTile > min_hi || tok0 < max_lo;
+                const float *meta = reinterpret_cast<const float *>(sm + S::kOffMeta) + ((tile + t) % S::kMetaTiles) * 2 * kSubs;
+                // the largest score of 16, in x's units
+                auto top_of = [&](const float *y, float fi) {
                     float v0 = max3(y[0], y[1], y[2]), v1 = max3(y[3], y[4], y[5]), v2 = max3(y[6], y[7], y[8]), v3 = max3(y[9], y[10], y[11]);
                     v0 = max3(v0, y[12], y[13]);
                     v1 = max3(v1, y[14], y[15]);
-                    const float v = fmaxf(max3(v0, v1, v2), v3) * fmaxf(f * meta[4 * c + u], 1.2e-38f);
-                    nm = fmaxf(nm, v);
-                    nb = fmaxf(nb, v + meta[kSubs + 4 * c + u]);
-                }
-            }
-            const float mz = nm == -INFINITY ? 0.0f : nm;
-            l *= ex2(m - mz);
-            m = nm;
-            // M follows where it grew by 2^kLazy (or is the row's first)
-            const bool grew = nb > big + kLazy || (big == -INFINITY && nb > big);
-            if (__any_sync(0xffffffffu, grew)) {
-                const float to = grew ? nb : big, r = big == -INFINITY ? 0.0f : ex2(big - to);
-                if (i > 0) {                       // the half's last product is done
-                    wait(b.o_done + h, (on - 1) & 1);
-#pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        float x[32];
-                        tmem_ld32(x, o_at + 32 * c);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            x[e] *= r;
-                        tmem_st32(o_at + 32 * c, x);
+                    return fmaxf(max3(v0, v1, v2), v3) * fi;
+                };
+                auto factor = [&](int k) { return fmaxf(f * meta[k], 1.2e-38f); };
+                // whether a score with this exponent outgrows the references
+                auto outgrows = [&](float top, float b) {
+                    return m == -INFINITY || big == -INFINITY ? top > -INFINITY : fmaxf(top + b - big, top - m - 32.0f) > kLazy + 0.01f;
+                };
+                // moves the references to the tile's maxima (of x, and of x + b) where they lie above
+                auto move = [&](float nm, float nb) {
+                    if (nm > m) {
+                        l *= m == -INFINITY ? 0.0f : ex2(m - nm);
+                        m = nm;
                     }
-                }
-                big = to;
-            }
-            const float bz = big == -INFINITY ? 0.0f : big;
-            // weights, over the scores as they are read
-            const uint64_t minus_m = pack2(-mz, -mz);
-            uint64_t sum0 = 0, sum1 = 0;
+                    const float to = nb > big + kLazy || big == -INFINITY ? nb : big, r = big == -INFINITY ? 0.0f : ex2(big - to);
+                    if (i > 0) {                   // the half's last product is done
+                        wait(b.o_done + h, (on - 1) & 1);
 #pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-                float x[2][32];
-                tmem_ld32(x[0], s_at + 64 * c);
-                tmem_ld32(x[1], s_at + 64 * c + 32);
-                tmem_wait_ld();
-                if (edge)
-                    hide(x, tok0 + 64 * c, lo, hi);
+                        for (int c = 0; c < D / 32; ++c) {
+                            float x[32];
+                            tmem_ld32(x, o_at + 32 * c);
 #pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const float fi = fmaxf(f * meta[4 * c + 2 * v + u], 1.2e-38f);
-                        const float r = ex2(fminf(meta[kSubs + 4 * c + 2 * v + u] + (mz - bz), 126.0f));
-                        const uint64_t fi2 = pack2(fi, fi), r2 = pack2(r, r);
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const float2 t2 = unpack2(fma2(pack2(x[v][16 * u + e], x[v][16 * u + e + 1]), fi2, minus_m));
-                            const uint64_t p2 = pack2(ex2(t2.x), ex2(t2.y));
-                            if (e & 2)
-                                sum0 = add2(sum0, p2);
-                            else
-                                sum1 = add2(sum1, p2);
-                            const float2 w2 = unpack2(mul2(p2, r2));
-                            const __half2 h2 = __floats2half2_rn(w2.x, w2.y);
-                            w[8 * u + e / 2] = *reinterpret_cast<const uint32_t *>(&h2);
+                            for (int e = 0; e < 32; ++e)
+                                x[e] *= r;
+                            tmem_st32(o_at + 32 * c, x);
                         }
                     }
-                    tmem_st16(s_at + 32 * c + 16 * v, w);
+                    big = to;
+                };
+                auto maxima = [&](float &nm, float &nb) {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        float x[32];
+                        tmem_ld32(x, s_at + 32 * c);
+                        if (edge)
+                            hide(x, tok0 + 32 * c, lo, hi);
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const float v = top_of(x + 16 * u, factor(2 * c + u));
+                            nm = fmaxf(nm, v);
+                            nb = fmaxf(nb, v + meta[kSubs + 2 * c + u]);
+                        }
+                    }
+                };
+                if (!S::kOwnW) {
+                    // the weights will lie over the scores: the references are settled first
+                    float nm = -INFINITY, nb = -INFINITY;
+                    maxima(nm, nb);
+                    if (__any_sync(0xffffffffu, outgrows(nm, nb - nm)))
+                        move(nm, nb);
+                } else if (i > 0) {
+                    // the last tile's product, issued after these scores, must have read its weights
+                    wait(b.o_done + h, (on - 1) & 1);
                 }
+                for (;;) {
+                    const float mz = m == -INFINITY ? 0.0f : m, bz = big == -INFINITY ? 0.0f : big;
+                    const uint64_t minus_m = pack2(-mz, -mz);
+                    uint64_t sum0 = 0, sum1 = 0;
+                    bool grew = false;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float x[32];
+                        tmem_ld32(x, s_at + 32 * c);
+                        if (edge)
+                            hide(x, tok0 + 32 * c, lo, hi);
+                        uint32_t w[16];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const float fi = factor(2 * c + u), bb = meta[kSubs + 2 * c + u];
+                            const float *y = x + 16 * u;
+                            if (S::kOwnW)
+                                grew |= outgrows(top_of(y, fi), bb);
+                            const float r = ex2(fminf(bb + (mz - bz), 126.0f));
+                            const uint64_t fi2 = pack2(fi, fi), r2 = pack2(r, r);
+#pragma unroll
+                            for (int e = 0; e < 16; e += 2) {
+                                const float2 t2 = unpack2(fma2(pack2(y[e], y[e + 1]), fi2, minus_m));
+                                const uint64_t p2 = pack2(ex2(t2.x), ex2(t2.y));
+                                if (e & 2)
+                                    sum0 = add2(sum0, p2);
+                                else
+                                    sum1 = add2(sum1, p2);
+                                const float2 w2 = unpack2(mul2(p2, r2));
+                                const __half2 h2 = __floats2half2_rn(w2.x, w2.y);
+                                w[8 * u + e / 2] = *reinterpret_cast<const uint32_t *>(&h2);
+                            }
+                        }
+                        tmem_st16(lanes + S::w_col(h, 32 * c), w);
+                    }
+                    if (!S::kOwnW || !__any_sync(0xffffffffu, grew)) {
+                        const float2 s2 = unpack2(add2(sum0, sum1));
+                        l += s2.x + s2.y;
+                        break;
+                    }
+                    // made again with the references moved (a unit's first tile, and rarely after that)
+                    float nm = -INFINITY, nb = -INFINITY;
+                    maxima(nm, nb);
+                    move(nm, nb);
+                }
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             }
-            const float2 s2 = unpack2(add2(sum0, sum1));
-            l += s2.x + s2.y;
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
             if (lane == 0)
@@ -685,7 +733,6 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
             float x[32];
             if (mine > 0) {
                 tmem_ld32(x, o_at + 32 * c);
-                tmem_wait_ld();
             } else {
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
@@ -741,50 +788,76 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
             }
             named_barrier_sync(1 + h, 128);
             if (s_last[h]) {
-                // parts in the order of the cache's CTAs, a CTA's first half before its second
-                constexpr int Q = D / 4, U = 4;
+                // Parts in the order of the cache's CTAs, a CTA's first half before its second.  A thread has 16 dims of
+                // a row at a time: the row's log-sum, then four parts' loads in flight.
                 auto has_two = [&](int k) { return !pair && (k == 0 ? pc.first_tiles : k == ctas - 1 ? pc.last_tiles : pl.per) >= 2; };
-                for (int i = tid; i < rows_here * Q; i += 128) {
-                    const int r = i % rows_here, d4 = i / rows_here;
+                const int parts = pair ? ctas : 2 * ctas;
+                auto slot_of = [&](int k) {        // -1: the part does not exist
+                    const int c = pair ? k : k >> 1, g = pair ? h : k & 1;
+                    return k < parts && (pair || g == 0 || has_two(c)) ? ((pc.first + c) * 2 + (c == 0)) * 2 + g : -1;
+                };
+                constexpr int U = 4;
+                for (int i = tid; i < rows_here * (D / 16); i += 128) {
+                    const int r = i % rows_here, d = i / rows_here * 4;
                     float rm = -INFINITY, rl = 0.0f;
-                    float4 o = make_float4(0, 0, 0, 0);
-                    for (int k0 = 0; k0 < ctas; k0 += U) {
+                    for (int k0 = 0; k0 < parts; k0 += 2 * U) {
                         float e[2 * U];
-                        float4 v[2 * U];
 #pragma unroll
                         for (int u = 0; u < 2 * U; ++u) {
-                            const int k = k0 + (u >> 1), g = pair ? h : u & 1;
-                            const bool there = k < ctas && (pair ? (u & 1) == 0 : (g == 0 || has_two(k)));
-                            const size_t slot = ((size_t)(pc.first + k) * 2 + (k == 0)) * 2 + g;
-                            e[u] = there ? __ldcg(a.part_lse + slot * cap + r) : -INFINITY;
-                            v[u] = there ? __ldcg(reinterpret_cast<const float4 *>(a.part + slot * cap * D) + (size_t)d4 * cap + r) : make_float4(0, 0, 0, 0);
+                            const int slot = slot_of(k0 + u);
+                            e[u] = slot >= 0 ? __ldcg(a.part_lse + (size_t)slot * cap + r) : -INFINITY;
                         }
                         float nm = rm;
 #pragma unroll
                         for (int u = 0; u < 2 * U; ++u)
                             nm = fmaxf(nm, e[u]);
-                        const float z = nm == -INFINITY ? 0.0f : nm, w0 = ex2(rm - z);
-                        rl *= w0;
-                        o = make_float4(o.x * w0, o.y * w0, o.z * w0, o.w * w0);
+                        const float z = nm == -INFINITY ? 0.0f : nm;
+                        rl *= ex2(rm - z);
                         rm = nm;
 #pragma unroll
-                        for (int u = 0; u < 2 * U; ++u) {
-                            const float wt = ex2(e[u] - z);
-                            rl += wt;
-                            o.x += v[u].x * wt;
-                            o.y += v[u].y * wt;
-                            o.z += v[u].z * wt;
-                            o.w += v[u].w * wt;
-                        }
+                        for (int u = 0; u < 2 * U; ++u)
+                            rl += ex2(e[u] - z);
                     }
-                    const float wt = rl == 0.0f ? 0.0f : 1.0f / rl;
+                    const float z = rm == -INFINITY ? 0.0f : rm, wt = rl == 0.0f ? 0.0f : 1.0f / rl;
                     const int grow = pc.row0 + (pair ? 128 * h : 0) + r;
                     const size_t at = (size_t)(pc.q0 + grow / a.group) * p.q_heads + pc.head * a.group + grow % a.group;
-                    uint32_t x0, x1;
-                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x0) : "f"(o.y * wt), "f"(o.x * wt));
-                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x1) : "f"(o.w * wt), "f"(o.z * wt));
-                    *reinterpret_cast<uint2 *>(p.out + at * D + d4 * 4) = make_uint2(x0, x1);
-                    if (d4 == 0 && p.lse)
+                    float o[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        o[e] = 0.0f;
+                    for (int k0 = 0; k0 < parts; k0 += U) {
+                        float e[U];
+                        float4 v[U][4];
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            const int slot = slot_of(k0 + u);
+                            e[u] = slot >= 0 ? __ldcg(a.part_lse + (size_t)slot * cap + r) : -INFINITY;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                v[u][q] = slot >= 0 ? __ldcg(reinterpret_cast<const float4 *>(a.part + (size_t)slot * cap * D) + (size_t)(d + q) * cap + r)
+                                                    : make_float4(0, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            const float w = ex2(e[u] - z);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                o[4 * q] += v[u][q].x * w;
+                                o[4 * q + 1] += v[u][q].y * w;
+                                o[4 * q + 2] += v[u][q].z * w;
+                                o[4 * q + 3] += v[u][q].w * w;
+                            }
+                        }
+                    }
+                    uint2 *dst = reinterpret_cast<uint2 *>(p.out + at * D + d * 4);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t x0, x1;
+                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x0) : "f"(o[4 * q + 1] * wt), "f"(o[4 * q] * wt));
+                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x1) : "f"(o[4 * q + 3] * wt), "f"(o[4 * q + 2] * wt));
+                        dst[q] = make_uint2(x0, x1);
+                    }
+                    if (d == 0 && p.lse)
                         p.lse[at] = rl == 0.0f ? -INFINITY : (rm + log2f(rl)) * 0.69314718055994530942f;
                 }
             }
@@ -796,7 +869,7 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs a) {
     using S = TcSmem<D>;
-    extern __shared__ uint8_t raw_smem[];
+    extern __shared__ __align__(1024) uint8_t raw_smem[];
     uint8_t *sm = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + S::kOffBars);
     Bars b;
@@ -831,7 +904,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         nan_count[0] = nan_count[1] = 0;            // entries begun, entries written
         fence_barrier_init();
     }
-    if (warp == 13) {
+    if (warp == kSoftWarps + kConvWarps + 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(s_taddr)));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
@@ -842,18 +915,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     pdl_wait();
     pdl_trigger();
     const Plan pl = *a.plan;
-    if (warp < 8)
+    // 256 threads x 176 + 256 x 80 registers = the 512 x 128 of the launch
+    if (warp < kSoftWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         tc_softmax<D>(a, pl, sm, b, tmem, nan_count, s_last);
-    else if (warp < 8 + kConvWarps)
-        tc_convert<D>(a, pl, sm, b, nan_count);
-    else if (warp == 12)
-        tc_stream<D>(a, pl, sm, b);
-    else
-        tc_issue<D>(a, pl, sm, b, tmem);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (warp < kSoftWarps + kConvWarps)
+            tc_convert<D>(a, pl, sm, b, nan_count);
+        else if (warp == kSoftWarps + kConvWarps)
+            tc_stream<D>(a, pl, sm, b);
+        else
+            tc_issue<D>(a, pl, sm, b, tmem);
+    }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    if (warp == 13)
+    if (warp == kSoftWarps + kConvWarps + 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 

@@ -373,11 +373,12 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) fp8_gemm_kernel(const
                 if (q < toks) {
                     uint32_t v[16];
                     asm volatile(
-                        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+                        "tcgen05.wait::ld.sync.aligned;"
                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
                           "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-                        : "r"(tmem + lanes + buf * S::kDCols + q));
-                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                        : "r"(tmem + lanes + buf * S::kDCols + q)
+                        : "memory");
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         if (q + j >= toks)

@@ -605,3 +605,64 @@ def test_binding_refusals():
         attn.moe_linear_fp8(bf16(np.ones((2, 16))), w, torch.empty(2, 16, dtype=torch.bfloat16, device="cuda"), ws)
     with pytest.raises(ValueError):
         attn.FP8Weight(w.codes, w.scale[:0])
+
+
+# ------------------------------------- units of many rows (tensor-memory form)
+
+@pytest.mark.parametrize("dim,size", [(64, 32), (128, 16), (128, 128), (64, 64)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 130), (False, 33)])
+def test_attention_many_rows(dim, size, causal, window):
+    """More than 24 rows a request and 64 units: row tiles of 1 .. 256 rows, one half or two, requests that see nothing, a cut
+    last tile, a request without new tokens."""
+    lens = [(30, 300), (1, 129), (64, 64), (17, 515), (0, 40), (9, 3), (100, 260), (33, 640), (5, 128)]
+    Problem(lens, 8, 8, dim, size, seed=dim + size).check(causal, window)
+
+
+def test_attention_many_rows_cut_into_pieces():
+    """Fewer units than CTAs: every unit lies in several, with one or both halves in each."""
+    Problem([(30, 6000)], 8, 8, 64, 64, seed=31).check()
+    Problem([(8, 5000)] * 8, 8, 4, 128, 16, seed=32).check()
+    Problem([(8, 300 + 17 * i) for i in range(9)], 8, 6, 64, 128, seed=33).check(window=200)
+
+
+def test_attention_many_rows_ranges():
+    """Block exponents far apart, rows of q of very different size, scores that grow along the cache."""
+    p = Problem([(12, 400), (12, 300)] * 5, 8, 4, 64, 16, seed=34)
+    rng = np.random.default_rng(35)
+    p.cache.ve[:] = rng.integers(-60, 30, p.cache.ve.shape)
+    p.cache.v[::3] = 0
+    p.cache.ve[::3] = -126
+    p.check()
+    p = Problem([(12, 700)] * 10, 8, 4, 128, 64, seed=36, q_scale=6.0)
+    p.cache.ke[:] = np.sort(rng.integers(-12, -4, p.cache.ke.shape), axis=0)
+    p.check()
+
+
+def test_attention_many_rows_nan_reaches_only_rows_that_see_it():
+    for which in ("v", "k"):
+        for window in (0, 8):
+            p = Problem([(40, 200), (33, 90), (20, 130)] * 4, 8, 4, 64, 32, seed=37)
+            clean_out, clean_lse = p.run(window=window)
+            page = p.table[0, 170 // 32]
+            getattr(p.cache, which)[page, 1, 170 % 32, 5] = 0x7F
+            out, lse = p.run(window=window)
+            assert p.status == 0
+            pos = np.arange(160, 200)
+            sees = (pos >= 170) & ((window == 0) | (170 > pos - window))
+            o, co = out.float().cpu().numpy(), clean_out.float().cpu().numpy()
+            hit = slice(4, 8)                              # the query heads of key/value head 1
+            assert np.array_equal(o[40:], co[40:]) and np.array_equal(o[:40, :4], co[:40, :4]) and np.array_equal(o[:40, 8:], co[:40, 8:])
+            assert np.array_equal(o[:40, hit][~sees], co[:40, hit][~sees])
+            if which == "v":
+                keep = np.arange(64) != 5
+                assert np.isnan(o[:40, hit][sees][..., 5]).all()
+                assert np.array_equal(o[:40, hit][sees][..., keep], co[:40, hit][sees][..., keep]) and torch.equal(lse, clean_lse)
+            else:
+                assert np.isnan(o[:40, hit][sees]).all()
+
+
+def test_attention_many_rows_repeats_bit_for_bit():
+    p = Problem([(30, 2000), (64, 900), (40, 40)], 8, 8, 128, 64, seed=38)
+    a, la = p.run()
+    b, lb = p.run()
+    assert torch.equal(a, b) and torch.equal(la, lb)
