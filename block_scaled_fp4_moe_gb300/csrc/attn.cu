@@ -25,8 +25,8 @@
 // row tiles (a decode step): every CTA makes the plan itself in shared memory; many:
 // a kernel before this one makes it in the workspace.
 //
-// CTA: eight consumer warps, one warp that streams the cache and three that
-// prepare the queries of the next unit.  The cache comes in tiles (16-token
+// CTA: eight consumer warps, one warp that streams the keys, one that streams the values (a warp issues a
+// copy in about 100 cycles, and blocks of 16 tokens need 8 of each for a tile) and two that prepare the queries of the next unit.  The cache comes in tiles (16-token
 // sub-blocks, 16 * D consecutive bytes of a block, as bulk copies of all
 // that lies together) through a ring of shared-memory stages; block ids and scales are
 // loaded two batches of four tiles ahead.  A consumer warp takes 16 rows (units
@@ -44,7 +44,7 @@ namespace {
 constexpr int kRows = 64;              // rows of a unit
 constexpr int kConsumers = 8;          // consumer warps
 constexpr int kThreads = 384;          // three warpgroups: two of consumers, one of producers
-constexpr int kQWarps = 3;
+constexpr int kQWarps = 2;
 constexpr int kSmallRequests = 256;    // most requests and row tiles of a plan in shared memory
 constexpr int kSmallTiles = 288;
 
@@ -98,18 +98,19 @@ struct Smem {
 // Up to four tiles of a piece: a lane for each of their sub-blocks.
 struct Batch {
     int tiles;                    // 0: there is none
-    int head, hi, page, ks, vs;
+    int head, hi, page, scale;
     long long tok;                // the lane's first token
     bool live;
 };
 
 template <int D>
 __device__ __forceinline__ void stream_cache(const AttnArgs &a, const Plan &pl, const RowTile *recs, uint8_t *sm, uint64_t *full,
-                                             uint64_t *empty) {
+                                             uint64_t *empty, bool is_v) {
     using S = Smem<D>;
     const AttnProblem &p = a.p;
     const int lane = threadIdx.x & 31, sub = lane & (kSubs - 1);
     const uint64_t policy = l2_evict_first_policy();
+    const uint8_t *codes = is_v ? p.cache.v : p.cache.k, *scale = is_v ? p.cache.v_scale : p.cache.k_scale;
     Walk walk(a, pl, recs);
     Piece pc;
     int t = 0;
@@ -142,8 +143,7 @@ __device__ __forceinline__ void stream_cache(const AttnArgs &a, const Plan &pl, 
             b.page = 0;
         }
         const size_t unit = (size_t)b.page * p.cache.kv_heads + b.head;
-        b.ks = b.live ? __ldg(p.cache.k_scale + unit) : 127;
-        b.vs = b.live ? __ldg(p.cache.v_scale + unit) : 127;
+        b.scale = b.live ? __ldg(scale + unit) : 127;
     };
     long long it = 0;
     bool dead = false;
@@ -173,22 +173,20 @@ __device__ __forceinline__ void stream_cache(const AttnArgs &a, const Plan &pl, 
             const bool mine = lane / kSubs == i;
             if (mine) {
                 float *ex = reinterpret_cast<float *>(sm + S::kExps) + st * 2 * kSubs + sub;
-                ex[0] = exp2i(min(max(b0.ks, 1), 254) - 127);
-                ex[kSubs] = (float)(b0.vs - 127);
+                if (is_v)
+                    ex[kSubs] = (float)(b0.scale - 127);
+                else
+                    ex[0] = exp2i(min(max(b0.scale, 1), 254) - 127);
             }
             __syncwarp();
             if (lane == 0)
-                mbar_arrive_expect_tx(full + st, 2 * S::kSubBytes * __popc((live >> (i * kSubs)) & ((1u << kSubs) - 1)));
+                mbar_arrive_expect_tx(full + st, S::kSubBytes * __popc((live >> (i * kSubs)) & ((1u << kSubs) - 1)));
             __syncwarp();
             if (mine && leads) {
-                const uint32_t dst = smem_u32(sm + (size_t)st * S::kStageBytes + sub * S::kSubBytes), bar = smem_u32(full + st);
+                const uint32_t dst = smem_u32(sm + (size_t)st * S::kStageBytes + (is_v ? S::kTileBytes : 0) + sub * S::kSubBytes);
                 asm volatile(
                     "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, "
-                    "[%3], %4;" ::"r"(dst), "l"(p.cache.k + src), "r"(bytes), "r"(bar), "l"(policy)
-                    : "memory");
-                asm volatile(
-                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, "
-                    "[%3], %4;" ::"r"(dst + S::kTileBytes), "l"(p.cache.v + src), "r"(bytes), "r"(bar), "l"(policy)
+                    "[%3], %4;" ::"r"(dst), "l"(codes + src), "r"(bytes), "r"(smem_u32(full + st)), "l"(policy)
                     : "memory");
             }
         }
@@ -206,7 +204,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs &a, const Plan &pl, 
                                              uint64_t *q_empty) {
     using S = Smem<D>;
     const AttnProblem &p = a.p;
-    const int warp = (threadIdx.x >> 5) - kConsumers - 1, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int warp = (threadIdx.x >> 5) - kConsumers - 2, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     Walk walk(a, pl, recs);
     Piece pc;
     bool dead = false;
@@ -266,14 +264,16 @@ struct Acc {
     float m[MT][2], big[MT][2], l[MT][2];       // m_i, M_i, l_i (l: this thread's columns)
 };
 
-// One piece's tiles: RG groups of MT x 16 rows, the other warps sharing the tokens.
-template <int D, int MT, int RG>
+// One piece's tiles: RG groups of MT x 16 rows; the warps of a row group form SG sets that take tiles in turn, those of
+// a set sharing a tile's sub-blocks.  (SG = 2 at 16 rows: a warp's chain of products, maxima and powers is as long for 32
+// tokens as for 16.)
+template <int D, int MT, int RG, int SG>
 __device__ __forceinline__ void attend(const Piece &pc, uint8_t *sm, int qbuf, uint64_t *full, uint64_t *empty, uint32_t *hdr,
                                        long long &it, bool &dead, Acc<D, MT> &acc) {
     using S = Smem<D>;
-    constexpr int TG = kConsumers / RG, NS = kSubs / TG;    // sub-blocks of a warp in a tile
+    constexpr int TG = kConsumers / RG / SG, NS = kSubs / TG;    // warps of a set, sub-blocks of a warp in a tile
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int rg = warp % RG, tg = warp / RG;
+    const int rg = warp % RG, tg = warp / RG % TG, sg = warp / RG / TG;
     const uint4 *q = reinterpret_cast<const uint4 *>(sm + S::kQ + (size_t)qbuf * S::kQBytes + (size_t)rg * MT * 32 * D) + lane;
     const RowInfo *info = reinterpret_cast<const RowInfo *>(sm + S::kInfo) + qbuf * kRows + rg * MT * 16 + g;
     float f[MT][2];
@@ -295,15 +295,15 @@ __device__ __forceinline__ void attend(const Piece &pc, uint8_t *sm, int qbuf, u
     const int mi = lane >> 3, ri = lane & 7;
     const uint32_t k_off = (uint32_t)((mi >> 1) * 256 + (4 * (ri >> 1) + (ri & 1) + 2 * (mi & 1)) * 16), v_off = (uint32_t)(lane * 16);
 
-    for (int t = pc.t0; t < pc.t1; ++t, ++it) {
-        const int st = (int)(it % S::kStages);
+    for (int t = pc.t0 + sg; t < pc.t1; t += SG) {
+        const uint32_t at = (uint32_t)(it + (t - pc.t0)), st = at % S::kStages;
         if (!dead) {
-            dead = !__all_sync(0xffffffffu, wait_phase(full + st, (uint32_t)((it / S::kStages) & 1)));
+            dead = !__all_sync(0xffffffffu, wait_phase(full + st, (at / S::kStages) & 1));
             if (dead && lane == 0)
                 record_status(hdr, MOE_ERR_DEVICE_TIMEOUT);
         }
         const int tok0 = (pc.tile0 + t) * kTile;
-        const uint32_t ks = base + (uint32_t)(st * S::kStageBytes), vs = ks + S::kTileBytes;
+        const uint32_t ks = base + st * S::kStageBytes, vs = ks + S::kTileBytes;
         const float *ex = reinterpret_cast<const float *>(sm + S::kExps) + st * 2 * kSubs;
         const bool edge = tok0 + kTile > min_hi || tok0 < max_lo;
         float x[MT][NS][2][4];
@@ -461,9 +461,10 @@ __device__ __forceinline__ void attend(const Piece &pc, uint8_t *sm, int qbuf, u
             }
         }
         __syncwarp();
-        if (lane == 0)
-            mbar_arrive(empty + st);
+        if (lane == 0)                  // for the warps of the other sets too
+            asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(empty + st)), "r"(SG) : "memory");
     }
+    it += pc.t1 - pc.t0;
 }
 
 // Joins the token groups of a piece and writes the rows: to the output, or,
@@ -652,7 +653,7 @@ __device__ __forceinline__ void consume_piece(const AttnArgs &a, const Piece &pc
             acc.l[mt][s] = 0.0f;
         }
     }
-    attend<D, MT, RG>(pc, sm, qbuf, full, empty, a.hdr, it, dead, acc);
+    attend<D, MT, RG, MT == 1 ? 2 : 1>(pc, sm, qbuf, full, empty, a.hdr, it, dead, acc);
     __syncwarp();
     if ((threadIdx.x & 31) == 0)
         mbar_arrive(q_empty);
@@ -670,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     int *s_last = reinterpret_cast<int *>(q_empty + 2);
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(full + i, 1);
+            mbar_init(full + i, 2);                // keys, values
             mbar_init(empty + i, kConsumers);
         }
         for (int i = 0; i < 2; ++i) {
@@ -692,8 +693,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     const int warp = threadIdx.x >> 5;
     if (warp >= kConsumers) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp == kConsumers)
-            stream_cache<D>(a, pl, recs, sm, full, empty);
+        if (warp < kConsumers + 2)
+            stream_cache<D>(a, pl, recs, sm, full, empty, warp > kConsumers);
         else
             load_queries<D>(a, pl, recs, sm, q_full, q_empty);
         return;
