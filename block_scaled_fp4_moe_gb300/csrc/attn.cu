@@ -85,15 +85,27 @@ struct Smem {
     static constexpr int kQBytes = kRows * D * 2;                        // queries in operand order: [16 rows][16 dims][lane][16 bytes]
     static constexpr size_t kQ = (size_t)kStages * kStageBytes;          // two units'
     static constexpr size_t kInfo = kQ + 2 * kQBytes;                    // RowInfo [2][kRows]
-    static constexpr size_t kJoin = kInfo + 2 * kRows * sizeof(RowInfo); // [4 warps][64 registers][lane]
-    static constexpr size_t kStats = kJoin + (size_t)4 * (D / 2) * 128;  // m, M, l [256]
+    static constexpr size_t kPieces = kInfo + 2 * kRows * sizeof(RowInfo);      // Piece [2]
+    static constexpr int kPad = D + 8;                                   // floats of a row of the join buffer
+    static constexpr size_t kJoin = kPieces + 128;                       // [8 warps][8 rows][kPad]
+    static constexpr size_t kStats = kJoin + (size_t)kConsumers * 8 * kPad * 4; // m, M, l [256]
     static constexpr size_t kExps = kStats + 3 * 256 * 4;                // [stage][2][kSubs]
     static constexpr size_t kRecs = kExps + (size_t)kStages * 2 * kSubs * 4;
-    static constexpr size_t kFirst = kRecs + kSmallTiles * sizeof(RowTile);
-    static constexpr size_t kBars = kFirst + kSmallRequests * 4;
+    static constexpr size_t kBars = kRecs + kSmallTiles * sizeof(RowTile);
     static constexpr size_t kBytes = kBars + (2 * kStages + 4) * 8 + 16;
-    static_assert(kInfo % 16 == 0 && kJoin % 16 == 0 && kRecs % 8 == 0 && kBars % 8 == 0 && kBytes <= 227 * 1024, "shared memory");
+    static_assert(2 * sizeof(Piece) <= 128 && kInfo % 16 == 0 && kJoin % 16 == 0 && kRecs % 8 == 0 && kBars % 8 == 0 && kBytes <= 227 * 1024, "shared memory");
 };
+
+// A barrier that or's a predicate.
+__device__ __forceinline__ bool barrier_any(int id, int threads, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, %2, %3, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(id), "r"(threads)
+        : "memory");
+    return r != 0;
+}
 
 // Up to four tiles of a piece: a lane for each of their sub-blocks.
 struct Batch {
@@ -207,14 +219,19 @@ __device__ __forceinline__ void load_queries(const AttnArgs &a, const Plan &pl, 
     const int warp = (threadIdx.x >> 5) - kConsumers - 2, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     Walk walk(a, pl, recs);
     Piece pc;
-    bool dead = false;
-    for (int u = 0; walk.next(pc); ++u) {
+    bool dead = false, more = true;
+    for (int u = 0; more; ++u) {
         const int buf = u & 1;
+        more = walk.next(pc);
+        if (!more)
+            pc.rows = 0;                        // there is no further piece
         if (!dead && u >= 2)
             dead = !__all_sync(0xffffffffu, wait_phase(q_empty + buf, (uint32_t)((u / 2 - 1) & 1)));
+        if (warp == 0 && lane == 0)
+            reinterpret_cast<Piece *>(sm + S::kPieces)[buf] = pc;
         RowInfo *info = reinterpret_cast<RowInfo *>(sm + S::kInfo) + buf * kRows;
         // rows up to the next multiple of 32, as the consumers read them
-        for (int rg = warp; rg * 16 < (pc.rows <= 16 ? 16 : (pc.rows + 31) / 32 * 32); rg += kQWarps) {
+        for (int rg = warp; rg * 16 < (pc.rows <= 16 ? pc.rows : (pc.rows + 31) / 32 * 32); rg += kQWarps) {
             uint32_t *dst = reinterpret_cast<uint32_t *>(sm + S::kQ + (size_t)buf * S::kQBytes + (size_t)rg * 32 * D) + lane * 4;
 #pragma unroll 1
             for (int s = 0; s < 2; ++s) {
@@ -469,113 +486,88 @@ __device__ __forceinline__ void attend(const Piece &pc, uint8_t *sm, int qbuf, u
 
 // Joins the token groups of a piece and writes the rows: to the output, or,
 // where the unit has other pieces, to the workspace, the last CTA joining those.
+// Eight rows of each warp at a time go through shared memory; a thread then adds four dims of a row over the warps.
 template <int D, int MT, int RG>
 __device__ __forceinline__ void finish(const AttnArgs &a, const Piece &pc, uint8_t *sm, Acc<D, MT> &acc, int *s_last) {
     using S = Smem<D>;
-    constexpr int TG = kConsumers / RG, R = RG * MT * 16;
+    constexpr int TG = kConsumers / RG, R = RG * MT * 16, Q = D / 4;
     const AttnProblem &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int rg = warp % RG, tg = warp / RG;
-    float *s_m = reinterpret_cast<float *>(sm + S::kStats), *s_b = s_m + 256, *s_l = s_b + 256;
+    float *s_m = reinterpret_cast<float *>(sm + S::kStats), *s_b = s_m + 256, *s_l = s_b + 256, *join = reinterpret_cast<float *>(sm + S::kJoin);
+    const int pieces = pc.last - pc.first + 1;
+    const int slot = (int)blockIdx.x * 2 + (pc.first == (int)blockIdx.x);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             acc.l[mt][s] += __shfl_xor_sync(0xffffffffu, acc.l[mt][s], 1);
             acc.l[mt][s] += __shfl_xor_sync(0xffffffffu, acc.l[mt][s], 2);
-            if (c == 0) {
-                const int i = tg * R + rg * MT * 16 + mt * 16 + g + 8 * s;
-                s_m[i] = acc.m[mt][s];
-                s_b[i] = acc.big[mt][s];
-                s_l[i] = acc.l[mt][s];
-            }
         }
-    named_barrier_sync(1, kConsumers * 32);
-    float f[MT][2], lse2[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int i = rg * MT * 16 + mt * 16 + g + 8 * s;
-            float m = -INFINITY, b = -INFINITY, l = 0.0f;
+            if (mt * 16 + 8 * s >= pc.rows)
+                break;
+            if (mt > 0 || s > 0)
+                named_barrier_sync(1, kConsumers * 32);      // the buffer is free
+            if (mt == 0 && s == 0 && c == 0) {
 #pragma unroll
-            for (int t = 0; t < TG; ++t) {
-                m = fmaxf(m, s_m[t * R + i]);
-                b = fmaxf(b, s_b[t * R + i]);
-            }
-            const float mz = m == -INFINITY ? 0.0f : m, bz = b == -INFINITY ? 0.0f : b;
-#pragma unroll
-            for (int t = 0; t < TG; ++t)
-                l += s_l[t * R + i] * ex2(s_m[t * R + i] - mz);
-            // l is NaN where a score was: then so is the row
-            f[mt][s] = l == 0.0f ? 0.0f : exp2f(bz - mz) / l;
-            lse2[mt][s] = l == 0.0f ? -INFINITY : mz + log2f(l);
-            const float w = ex2(acc.big[mt][s] - bz);
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
-                acc.o[mt][n][2 * s] *= w;
-                acc.o[mt][n][2 * s + 1] *= w;
-            }
-        }
-    // sums of the token groups, halving their number; a warp's registers [register / 4][lane]
-    float4 *join = reinterpret_cast<float4 *>(sm + S::kJoin);
-#pragma unroll
-    for (int half = TG / 2; half > 0; half >>= 1)
-#pragma unroll
-        for (int part = 0; part < MT; ++part) {
-            if (tg >= half && tg < 2 * half) {
-                float4 *to = join + ((tg - half) * RG + rg) * (D / 8) * 32 + lane;
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n)
-                    to[n * 32] = make_float4(acc.o[part][n][0], acc.o[part][n][1], acc.o[part][n][2], acc.o[part][n][3]);
-            }
-            named_barrier_sync(1, kConsumers * 32);
-            if (tg < half) {
-                const float4 *from = join + (tg * RG + rg) * (D / 8) * 32 + lane;
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n) {
-                    const float4 v = from[n * 32];
-                    acc.o[part][n][0] += v.x;
-                    acc.o[part][n][1] += v.y;
-                    acc.o[part][n][2] += v.z;
-                    acc.o[part][n][3] += v.w;
+                for (int i = 0; i < 2 * MT; ++i) {
+                    const int at = tg * R + rg * MT * 16 + 8 * i + g;
+                    s_m[at] = acc.m[i >> 1][i & 1];
+                    s_b[at] = acc.big[i >> 1][i & 1];
+                    s_l[at] = acc.l[i >> 1][i & 1];
                 }
             }
-            if (half > 1 || part < MT - 1)
-                named_barrier_sync(1, kConsumers * 32);
-        }
-    const int pieces = pc.last - pc.first + 1;
-    const int slot = (int)blockIdx.x * 2 + (pc.first == (int)blockIdx.x);
-    if (tg == 0) {
+            float *to = join + (size_t)(warp * 8 + g) * S::kPad + 2 * c;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+            for (int n = 0; n < D / 8; ++n)
+                *reinterpret_cast<float2 *>(to + 8 * n) = make_float2(acc.o[mt][n][2 * s], acc.o[mt][n][2 * s + 1]);
+            named_barrier_sync(1, kConsumers * 32);
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const int row = rg * MT * 16 + mt * 16 + g + 8 * s;
-                if (row >= pc.rows)
+            for (int i0 = 0; i0 < RG * 8 * Q; i0 += kConsumers * 32) {
+                const int i = i0 + tid, r8 = i / Q % 8, wr = i / (8 * Q), d = i % Q * 4, row = wr * MT * 16 + mt * 16 + 8 * s + r8;
+                if (row >= pc.rows || (RG * 8 * Q < kConsumers * 32 && i >= RG * 8 * Q))
                     continue;
-                const float w = f[mt][s];
+                float m = -INFINITY, b = -INFINITY, l = 0.0f;
+#pragma unroll
+                for (int t = 0; t < TG; ++t) {
+                    m = fmaxf(m, s_m[t * R + row]);
+                    b = fmaxf(b, s_b[t * R + row]);
+                }
+                const float mz = m == -INFINITY ? 0.0f : m, bz = b == -INFINITY ? 0.0f : b;
+                float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll
+                for (int t = 0; t < TG; ++t) {
+                    l += s_l[t * R + row] * ex2(s_m[t * R + row] - mz);
+                    const float w = ex2(s_b[t * R + row] - bz);
+                    const float4 v = *reinterpret_cast<const float4 *>(join + (size_t)((t * RG + wr) * 8 + r8) * S::kPad + d);
+                    o.x += v.x * w;
+                    o.y += v.y * w;
+                    o.z += v.z * w;
+                    o.w += v.w * w;
+                }
+                // l is NaN where a score was: then so is the row
+                const float f = l == 0.0f ? 0.0f : exp2f(bz - mz) / l, lse2 = l == 0.0f ? -INFINITY : mz + log2f(l);
+                o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
                 if (pieces == 1) {
                     const int r = pc.row0 + row;
                     const size_t at = (size_t)(pc.q0 + r / a.group) * p.q_heads + pc.head * a.group + r % a.group;
-#pragma unroll
-                    for (int n = 0; n < D / 8; ++n) {
-                        uint32_t v;
-                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(acc.o[mt][n][2 * s + 1] * w), "f"(acc.o[mt][n][2 * s] * w));
-                        *reinterpret_cast<uint32_t *>(p.out + at * D + 8 * n + 2 * c) = v;
-                    }
-                    if (c == 0 && p.lse)
-                        p.lse[at] = lse2[mt][s] * 0.69314718055994530942f;
+                    uint32_t x, y;
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(o.y), "f"(o.x));
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(o.w), "f"(o.z));
+                    *reinterpret_cast<uint2 *>(p.out + at * D + d) = make_uint2(x, y);
+                    if (d == 0 && p.lse)
+                        p.lse[at] = lse2 * 0.69314718055994530942f;
                 } else {
-                    float *to = a.part + ((size_t)slot * kRows + row) * D + 2 * c;
-#pragma unroll
-                    for (int n = 0; n < D / 8; ++n)
-                        __stcg(reinterpret_cast<float2 *>(to + 8 * n), make_float2(acc.o[mt][n][2 * s] * w, acc.o[mt][n][2 * s + 1] * w));
-                    if (c == 0)
-                        __stcg(a.part_lse + slot * kRows + row, lse2[mt][s]);
+                    __stcg(reinterpret_cast<float4 *>(a.part + ((size_t)slot * kRows + row) * D + d), o);
+                    if (d == 0)
+                        __stcg(a.part_lse + slot * kRows + row, lse2);
                 }
             }
-    }
+        }
     if (pieces > 1) {
         __threadfence();
         named_barrier_sync(1, kConsumers * 32);
@@ -589,7 +581,7 @@ __device__ __forceinline__ void finish(const AttnArgs &a, const Piece &pc, uint8
         }
         named_barrier_sync(1, kConsumers * 32);
         if (*s_last) {
-            constexpr int Q = D / 4, U = 8;           // U parts' loads in flight
+            constexpr int U = 8;                      // parts' loads in flight
             for (int i = tid; i < pc.rows * Q; i += kConsumers * 32) {
                 const int row = i / Q, d = i % Q * 4;
                 float m = -INFINITY, l = 0.0f;
@@ -686,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     const RowTile *recs = a.recs;
     if (SMALL) {
         RowTile *mine = reinterpret_cast<RowTile *>(sm + S::kRecs);
-        make_plan(a, reinterpret_cast<int *>(sm + S::kFirst), red, mine, &s_plan, blockIdx.x == 0);
+        make_small_plan(a, red, mine, &s_plan, blockIdx.x == 0);
         recs = mine;
     }
     const Plan pl = SMALL ? s_plan : *a.plan;
@@ -701,17 +693,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     }
     // 256 threads x 216 + 128 x 72 registers = the 384 x 168 of the launch
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    Walk walk(a, pl, recs);
-    Piece pc;
     long long it = 0;
     bool dead = false;
-    for (int u = 0; walk.next(pc); ++u) {
+    for (int u = 0;; ++u) {
         const int buf = u & 1;
         if (!dead) {
             dead = !__all_sync(0xffffffffu, wait_phase(q_full + buf, (uint32_t)((u / 2) & 1)));
             if (dead && (threadIdx.x & 31) == 0)
                 record_status(a.hdr, MOE_ERR_DEVICE_TIMEOUT);
         }
+        // all eight warps leave together, or none; and the last piece's join buffer is free
+        const Piece pc = reinterpret_cast<const Piece *>(sm + S::kPieces)[buf];
+        if (barrier_any(1, kConsumers * 32, dead || pc.rows == 0))
+            break;
         if (pc.rows <= 16)
             consume_piece<D, 1, 1>(a, pc, sm, buf, full, empty, q_empty + buf, it, dead, s_last);
         else if (pc.rows <= 32)

@@ -76,6 +76,67 @@ __device__ __forceinline__ T block_scan(T v, T *red, T *total) {
     return v + sum;
 }
 
+__device__ __forceinline__ RowTile row_tile(const AttnArgs &a, int request, int q0, int n, int kv, int row0) {
+    RowTile r{};
+    r.request = request;
+    r.q0 = q0;
+    r.n = n;
+    r.kv = kv;
+    r.row0 = row0;
+    const int last = min(row0 + a.rows, n * a.group) - 1;
+    int l0, h0, l1, h1;
+    row_range(a.p, a.group, kv, n, row0, l0, h0);
+    row_range(a.p, a.group, kv, n, last, l1, h1);
+    // the first row sees furthest back, the last one furthest on
+    r.tile0 = l0 / kTile;
+    r.tiles = h1 > l0 ? (h1 + kTile - 1) / kTile - r.tile0 : 0;
+    return r;
+}
+
+__device__ __forceinline__ Plan plan_of(const AttnArgs &a, long long work, int row_tiles) {
+    const long long most = (work + kMinCost - 1) / kMinCost;
+    const int used = (int)min((long long)a.ctas, most);
+    return Plan{work, used > 0 ? (work + used - 1) / used : 1, row_tiles, used};
+}
+
+// The plan of no more requests than threads: a thread lists its request's row tiles.  red: 2 x 32 words of shared memory.
+__device__ __forceinline__ void make_small_plan(const AttnArgs &a, long long *red, RowTile *recs, Plan *plan, bool report) {
+    const AttnProblem &p = a.p;
+    const int tid = threadIdx.x;
+    int lo = 0, n = 0, kv = 0, bad = 0;
+    if (tid < p.B) {
+        const int hi = p.q_offsets[tid + 1];
+        lo = p.q_offsets[tid];
+        kv = p.kv_lens[tid];
+        n = hi - lo;
+        bad = lo < 0 || hi < lo || hi > p.T || kv < 0 || kv > ((long long)p.max_blocks << a.shift);
+    }
+    bad = __syncthreads_or(bad);
+    const int count = bad ? 0 : (int)(((long long)n * a.group + a.rows - 1) / a.rows);     // at most a.max_tiles in all
+    long long cost = 0, total;
+    for (int i = 0; i < count; ++i)
+        cost += (long long)(row_tile(a, tid, lo, n, kv, i * a.rows).tiles + kUnitCost) * p.cache.kv_heads;
+    // row tiles in the upper bits, work (below 2^48) in the lower
+    const long long mine = ((long long)count << 48) + cost, incl = block_scan(mine, red, &total);
+    const int tiles = (int)(total >> 48), first = (int)((incl - mine) >> 48);
+    const bool fits = tiles <= a.max_tiles;
+    if (fits) {
+        long long before = (incl - mine) & ((1ll << 48) - 1);
+        for (int i = 0; i < count; ++i) {
+            RowTile r = row_tile(a, tid, lo, n, kv, i * a.rows);
+            r.before = before;
+            before += (long long)(r.tiles + kUnitCost) * p.cache.kv_heads;
+            recs[first + i] = r;
+        }
+    }
+    if (tid == 0) {
+        if ((bad || !fits) && report)
+            record_status(a.hdr, MOE_ERR_DEVICE_ASSERT);
+        *plan = bad || !fits ? Plan{0, 1, 0, 0} : plan_of(a, total & ((1ll << 48) - 1), tiles);
+    }
+    __syncthreads();
+}
+
 // The plan, by all threads of a CTA.  first: B ints, red: 32 words of shared
 // memory; recs in shared or global memory.
 __device__ __forceinline__ void make_plan(const AttnArgs &a, int *first, long long *red, RowTile *recs, Plan *plan, bool report) {
@@ -123,19 +184,8 @@ __device__ __forceinline__ void make_plan(const AttnArgs &a, int *first, long lo
                 else
                     hi = mid;
             }
-            const int q0 = p.q_offsets[lo], n = p.q_offsets[lo + 1] - q0, kv = p.kv_lens[lo];
-            r.request = lo;
-            r.q0 = q0;
-            r.n = n;
-            r.kv = kv;
-            r.row0 = (i - first[lo]) * a.rows;
-            const int last = min(r.row0 + a.rows, n * a.group) - 1;
-            int l0, h0, l1, h1;
-            row_range(p, a.group, kv, n, r.row0, l0, h0);
-            row_range(p, a.group, kv, n, last, l1, h1);
-            // the first row sees furthest back, the last one furthest on
-            r.tile0 = l0 / kTile;
-            r.tiles = h1 > l0 ? (h1 + kTile - 1) / kTile - r.tile0 : 0;
+            const int q0 = p.q_offsets[lo];
+            r = row_tile(a, lo, q0, p.q_offsets[lo + 1] - q0, p.kv_lens[lo], (i - first[lo]) * a.rows);
             c = (long long)(r.tiles + kUnitCost) * p.cache.kv_heads;
         }
         const long long incl = block_scan(c, red, &total);
@@ -144,11 +194,8 @@ __device__ __forceinline__ void make_plan(const AttnArgs &a, int *first, long lo
             recs[i] = r;
         carry += total;
     }
-    if (tid == 0) {
-        const long long most = (carry + kMinCost - 1) / kMinCost;
-        const int used = (int)min((long long)a.ctas, most);
-        *plan = Plan{carry, used > 0 ? (carry + used - 1) / used : 1, n_recs, used};
-    }
+    if (tid == 0)
+        *plan = plan_of(a, carry, n_recs);
     __syncthreads();
 }
 
@@ -174,7 +221,7 @@ struct Piece {
     int request, head, row0, rows, q0, n, kv;
     int tile0, t0, t1;            // cache tiles tile0 + [t0, t1)
     int first, last;              // CTAs of the unit's first and last tile
-    int first_tiles, last_tiles;  // the unit's tiles in those (where they differ)
+    int first_tiles, last_tiles;  // the unit's tiles in those
 };
 
 // Walks a CTA's range.
@@ -202,7 +249,8 @@ struct Walk {
         }
         rt = lo;
         r = recs[rt];
-        head = (int)((pos - r.before) / (r.tiles + kUnitCost));
+        head = pos - r.before < 0x7FFFFFFF ? (int)((uint32_t)(pos - r.before) / (uint32_t)(r.tiles + kUnitCost))
+                                           : (int)((pos - r.before) / (r.tiles + kUnitCost));
         base = r.before + (long long)head * (r.tiles + kUnitCost);
     }
     // The next piece; false at the end of the range.
@@ -223,17 +271,18 @@ struct Walk {
                 pc.t0 = lo;
                 pc.t1 = hi;
                 pc.first = pc.last = (int)blockIdx.x;
-                if (r.tiles > 0) {
-                    const long long t0 = base + kUnitCost, t1 = t0 + r.tiles - 1;
-                    if (t1 < 0x7FFFFFFF) {     // the usual sizes: 32-bit divisions
+                pc.first_tiles = pc.last_tiles = r.tiles;
+                const long long t0 = base + kUnitCost, t1 = t0 + r.tiles - 1;
+                if (r.tiles > 0 && (t0 < pos || t1 >= end)) {      // cut
+                    if (t1 < 0x7FFFFFFF) {                         // the usual sizes: 32-bit divisions
                         pc.first = (int)((uint32_t)t0 / (uint32_t)per);
                         pc.last = (int)((uint32_t)t1 / (uint32_t)per);
                     } else {
                         pc.first = (int)(t0 / per);
                         pc.last = (int)(t1 / per);
                     }
-                    pc.first_tiles = (int)min((pc.first + 1) * per - base - kUnitCost, (long long)r.tiles);
-                    pc.last_tiles = (int)(base + kUnitCost + r.tiles - pc.last * per);
+                    pc.first_tiles = (int)min((pc.first + 1) * per - t0, (long long)r.tiles);
+                    pc.last_tiles = (int)(t1 + 1 - pc.last * per);
                 }
             }
             base += r.tiles + kUnitCost;
