@@ -7,6 +7,9 @@ CUDA runtime linked statically.  Nothing is installed outside the package.
 build(debug=True) builds the same sources with -DMOE_DEBUG_BOUNDS into
 libmoe_fp4_debug.so: device-side range checks on routing-derived indices that
 report MOE_ERR_DEVICE_ASSERT instead of touching memory out of bounds.
+
+build() also compiles csrc/binding.cpp, the Python side of moe_attn.h, against
+the installed torch into _attn_native.so.
 """
 from __future__ import annotations
 
@@ -15,6 +18,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,6 +28,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libmoe_fp4.so")
 DEBUG_BUILD_DIR = os.path.join(PKG, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(PKG, "libmoe_fp4_debug.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_PATH = os.path.join(PKG, "_attn_native.so")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -54,10 +60,31 @@ def up_to_date(debug: bool = False) -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def build_binding(force: bool = False) -> str:
+    """The torch-facing module of attn.py (host code only)."""
+    deps = [BINDING_SRC, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and os.path.exists(BINDING_PATH) and all(os.path.getmtime(d) <= os.path.getmtime(BINDING_PATH) for d in deps):
+        return BINDING_PATH
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    tmp = f"{BINDING_PATH}.{os.getpid()}.tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", os.path.join(root, "include"), "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
+           BINDING_SRC, "-o", tmp, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None,
           debug: bool = False) -> str:
     lib_path = DEBUG_LIB_PATH if debug else LIB_PATH
     build_dir = DEBUG_BUILD_DIR if debug else BUILD_DIR
+    if not debug:
+        build_binding(force)
     if not force and up_to_date(debug):
         return lib_path
     nvcc = nvcc_path()
