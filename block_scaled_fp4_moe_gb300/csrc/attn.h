@@ -46,13 +46,18 @@ __device__ __forceinline__ uint2 fp8_from_bf16x8(uint4 v, float inv) {
                       fp8_pair(lo(v.z), hi(v.z), inv) | fp8_pair(lo(v.w), hi(v.w), inv) << 16);
 }
 
-// Largest finite magnitude bits of 8 bf16.
+// Largest finite magnitude bits of 8 bf16: as pairs of 16-bit integers, which
+// order as the magnitudes do; where an infinity or NaN is among them, one by one.
 __device__ __forceinline__ uint32_t amax_bf16x8(uint4 v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t m = 0;
+    const uint32_t two = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+    uint32_t m = max(two << 16, two & 0xFFFF0000u);
+    if (m >= 0x7F800000u) {
+        m = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        m = max(m, max(finite_abs_bits(__uint_as_float(w[i] << 16)), finite_abs_bits(__uint_as_float(w[i] & 0xFFFF0000u))));
+        for (int i = 0; i < 4; ++i)
+            m = max(m, max(finite_abs_bits(__uint_as_float(w[i] << 16)), finite_abs_bits(__uint_as_float(w[i] & 0xFFFF0000u))));
+    }
     return m;
 }
 

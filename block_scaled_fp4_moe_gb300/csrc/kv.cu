@@ -138,109 +138,196 @@ __global__ void __launch_bounds__(kTablesThreads) kv_tables_kernel(TablesProblem
 
 // ----------------------------------------------------------------- append
 
-constexpr int kAppendThreads = 128;
+constexpr int kAppendThreads = 256, kAppendWarps = kAppendThreads / 32;
+constexpr int kAppendWindow = 32;       // tokens a CTA looks at, at most
+constexpr int kShortRun = 4;            // tokens of a run that one warp appends
 
-// One CTA owns a (block, head) of the keys (blockIdx.z = 0) or values (1): it
-// holds the new tokens of the block in registers (at most 128 x 128 bf16 =
-// 16 x 16 bytes a thread), takes their largest magnitude, settles the exponent,
-// re-rounds the codes that the block held where the exponent grew, and
-// writes the new codes: one pass over the input, no atomics on global memory.  A CTA looks at
-// `window` consecutive tokens and works for those that begin a run of tokens in one
-// block (a run may reach past the window); the launcher's window is 1 while
-// T tokens x heads x 2 fill the GPU few times over (a CTA then has one
-// short job) and 16 for prompts, where most tokens begin nothing.
+// 16 codes of a block whose exponent grew, rounded to the new one (f = 2^-growth);
+// the first `held` of them are the block's, the rest stays as it is.
+__device__ __forceinline__ uint4 recode(uint4 c, float f, int held) {
+    uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        uint32_t o = 0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t h2 = e4m3x2_to_f16x2((uint16_t)(w[q] >> (16 * e)));
+            const float2 f2 = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
+            o |= fp8_pair(f2.x, f2.y, f) << (16 * e);
+        }
+        const int n = held - 4 * q;
+        const uint32_t keep = n >= 4 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << (8 * n)) - 1;
+        w[q] = (o & keep) | (w[q] & ~keep);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The codes of a block's first off0 tokens, by threads `first` of `count`: 16
+// bytes are a token's 16 dims (keys) or a dim's 16 tokens (values).  kFlight
+// of them at a time: the stores may alias the loads, which otherwise wait.
+template <int D, int kFlight>
+__device__ __forceinline__ void recode_block(uint8_t *codes, bool is_v, int off0, float f, int first, int count) {
+    const int units = (off0 + 15) / 16 * D;
+    for (int u0 = first; u0 < units; u0 += kFlight * count) {
+        uint4 c[kFlight];
+        int held[kFlight];
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+            const int u = u0 + i * count, token = is_v ? u / D * 16 : u / (16 * (D / 16)) * 16 + u % 16;
+            held[i] = u >= units || token >= off0 ? 0 : is_v ? off0 - token : 16;
+            if (held[i])
+                c[i] = reinterpret_cast<const uint4 *>(codes)[u];
+        }
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i)
+            if (held[i])
+                reinterpret_cast<uint4 *>(codes)[u0 + i * count] = recode(c[i], f, held[i]);
+    }
+}
+
+// A CTA looks at `window` consecutive tokens, for one head of the keys
+// (blockIdx.z = 0) or values (1), and works for those that begin a run of
+// tokens in one block (a run may reach past the window).  Runs of up to
+// kShortRun tokens, the decode steps', are a warp's work each; a longer one is
+// the whole CTA's, which holds the block's new tokens in registers (at most
+// 128 x 128 bf16 = 8 x 16 bytes a thread).  Both take the run's largest magnitude,
+// settle the exponent, re-round the codes that the block held where the exponent grew, and
+// write the new codes: one pass over the input, no atomics on global memory.
+//
+// Bound: latency, of the chain slots -> input -> exponent -> codes.  64 requests of
+// one token (8 heads of 128) take 3.4 us, 256 take 6.6 and 400 take 8.6; with a CTA for
+// every run they took 5.8, 17.4 and 26.6, since few CTAs fit an SM.  5,000 prompt tokens in blocks of
+// 64 take 16 us (2.0 TB/s in and out); four CTAs an SM at 64 registers are ahead of three (22 us)
+// and of five that spill (20 us).
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendProblem p, int window) {
+__global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(AppendProblem p, int window) {
     constexpr int kLanes = D / 8;                       // threads per token (16 bytes each)
     constexpr int kTok = kAppendThreads / kLanes;       // tokens per step
     constexpr int kSteps = 128 / kTok;
     __shared__ __align__(16) uint8_t s_code[128 * D];   // values: codes [token][dim] before the transpose
-    __shared__ uint32_t s_max[kAppendThreads / 32];
-    __shared__ int s_len;
-    __shared__ uint32_t s_begins;
+    __shared__ uint32_t s_max[kAppendWarps];
+    __shared__ int64_t s_slot[kAppendWindow + 128];     // of the tokens from the one before the window on; < 0: none
     pdl_wait();
     pdl_trigger();
-    const int tid = threadIdx.x, h = blockIdx.y;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y;
     const bool is_v = blockIdx.z != 0;
     const int bs = p.cache.block_size, sh = 31 - __clz(bs);
     const uint16_t *src = (is_v ? p.v + h * p.v_sh : p.k + h * p.k_sh);
     const int64_t st = is_v ? p.v_st : p.k_st;
     const int64_t n_slots = (int64_t)p.cache.num_blocks << sh;
     const int t0 = blockIdx.x * window;
-    // which tokens of the window begin a run: their block is not that of the token before
-    if (tid < 32) {
-        const int t = t0 + tid;
-        const int64_t slot = tid < window && t < p.T ? p.slots[t] : -1;
-        const int64_t prev = slot >= 0 && t > 0 ? p.slots[t - 1] : -1;
-        if (slot >= n_slots)
+    for (int i = tid; i < window + bs; i += kAppendThreads) {
+        const int t = t0 - 1 + i;
+        int64_t slot = t >= 0 && t < p.T ? p.slots[t] : -1;
+        if (slot >= n_slots) {
             record_status(p.hdr, MOE_ERR_DEVICE_ASSERT);
-        const uint32_t begins = __ballot_sync(0xffffffffu, slot >= 0 && slot < n_slots && (prev < 0 || (prev >> sh) != (slot >> sh)));
-        if (tid == 0) {
-            s_begins = begins;
-            s_len = bs;
+            slot = -1;
         }
+        s_slot[i] = slot;
     }
     __syncthreads();
-    for (uint32_t begins = s_begins; begins; begins &= begins - 1) {
-        const int t = t0 + __ffs(begins) - 1;
-        const int64_t slot = p.slots[t], blk = slot >> sh;
-        // run length: the first of the next block_size tokens that lies elsewhere
-        if (tid < bs && (t + tid >= p.T || p.slots[t + tid] < 0 || (p.slots[t + tid] >> sh) != blk))
-            atomicMin(&s_len, tid);
-        __syncthreads();
-        const int off0 = (int)(slot & (bs - 1)), n = min(s_len, bs - off0);
+    // which tokens of the window begin a run (their block is not that of the token before), and which of
+    // these runs are short
+    const int64_t here = lane < window ? s_slot[1 + lane] : -1;
+    bool begins = false, brief = false;
+    if (here >= 0) {
+        const int64_t prev = s_slot[lane];
+        begins = prev < 0 || (prev >> sh) != (here >> sh);
+        brief = bs - (int)(here & (bs - 1)) <= kShortRun;
+#pragma unroll
+        for (int j = 1; j <= kShortRun; ++j)            // kShortRun < bs: within s_slot
+            brief = brief || (s_slot[1 + lane + j] >> sh) != (here >> sh);
+    }
+    const uint32_t all = __ballot_sync(0xffffffffu, begins), shorts = __ballot_sync(0xffffffffu, begins && brief);
+
+    uint8_t *scales = is_v ? p.cache.v_scale : p.cache.k_scale, *pool = is_v ? p.cache.v : p.cache.k;
+    int turn = 0;
+    for (uint32_t left = shorts; left; left &= left - 1, ++turn) {
+        if (turn % kAppendWarps != warp)
+            continue;
+        constexpr int kHold = kShortRun * kLanes / 32;  // 16-byte pieces a lane
+        const int w0 = __ffs(left), t = t0 + w0 - 1;
+        const int64_t slot = s_slot[w0], blk = slot >> sh;
+        const int off0 = (int)(slot & (bs - 1));
+        const int n = min(bs - off0,
+                          __ffs(__ballot_sync(0xffffffffu, lane >= kShortRun || (s_slot[w0 + lane] >> sh) != blk)) - 1);
+        uint8_t *scale = scales + blk * p.cache.kv_heads + h;
+        uint8_t *codes = pool + ((size_t)blk * p.cache.kv_heads + h) * bs * D;
+        const int was = off0 > 0 ? *scale : 0;
+        const int dim = lane % kLanes * 8;
+        uint4 x[kHold];
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+            const int r = (i * 32 + lane) / kLanes;
+            x[i] = r < n ? __ldg(reinterpret_cast<const uint4 *>(src + (t + r) * st + dim)) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kHold; ++i)
+            m = max(m, amax_bf16x8(x[i]));
+        m = __reduce_max_sync(0xffffffffu, m);
+        const int s = max(fp8_scale_byte(m), was);
+        if (off0 > 0 && was < s)
+            recode_block<D, 4>(codes, is_v, off0, exp2i(max(was - s, -126)), lane, 32);
+        __syncwarp();                                   // old scale read, old codes rewritten
+        if (lane == 0)
+            *scale = (uint8_t)s;
+        const float inv = exp2i(max(127 - s, -126));
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+            const int r = (i * 32 + lane) / kLanes, o = off0 + r;
+            if (r >= n)
+                continue;
+            const uint2 c = fp8_from_bf16x8(x[i], inv);
+            if (is_v) {
+                uint8_t *dst = codes + (size_t)((o >> 4) * D + dim) * 16 + (o & 15);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    dst[16 * j] = (uint8_t)((j < 4 ? c.x : c.y) >> (8 * (j & 3)));
+            } else {
+                *reinterpret_cast<uint2 *>(codes + (o >> 4) * 16 * D + (dim >> 4) * 256 + (o & 15) * 16 + (dim & 15)) = c;
+            }
+        }
+    }
+
+    for (uint32_t left = all & ~shorts; left; left &= left - 1) {
+        const int w0 = __ffs(left), t = t0 + w0 - 1;
+        const int64_t slot = s_slot[w0], blk = slot >> sh;
+        // run length: up to the first token that lies elsewhere, or the block's end
+        const int off0 = (int)(slot & (bs - 1));
+        int n = bs - off0;
+        for (int j = 0; j < n; j += 32) {
+            const uint32_t ends = __ballot_sync(0xffffffffu, j + lane >= n || (s_slot[w0 + j + lane] >> sh) != blk);
+            if (ends) {
+                n = min(n, j + __ffs(ends) - 1);
+                break;
+            }
+        }
+        uint8_t *scale = scales + blk * p.cache.kv_heads + h;
+        uint8_t *codes = pool + ((size_t)blk * p.cache.kv_heads + h) * bs * D;
+        const int was = off0 > 0 ? *scale : 0;
         // the new tokens, and their largest magnitude
-        const int lane8 = (tid % kLanes) * 8, row = tid / kLanes;
+        const int dim = (tid % kLanes) * 8, row = tid / kLanes;
         uint4 x[kSteps];
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < kSteps; ++i)
             if (i * kTok < n) {
                 const int r = i * kTok + row;
-                x[i] = r < n ? __ldg(reinterpret_cast<const uint4 *>(src + (t + r) * st + lane8)) : make_uint4(0, 0, 0, 0);
+                x[i] = r < n ? __ldg(reinterpret_cast<const uint4 *>(src + (t + r) * st + dim)) : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
         for (int i = 0; i < kSteps; ++i)
             if (i * kTok < n)
                 m = max(m, amax_bf16x8(x[i]));
         m = __reduce_max_sync(0xffffffffu, m);
-        if ((tid & 31) == 0)
-            s_max[tid >> 5] = m;
+        if (lane == 0)
+            s_max[warp] = m;
         __syncthreads();
-        m = max(max(s_max[0], s_max[1]), max(s_max[2], s_max[3]));
-        uint8_t *scale = (is_v ? p.cache.v_scale : p.cache.k_scale) + blk * p.cache.kv_heads + h;
-        uint8_t *codes = (is_v ? p.cache.v : p.cache.k) + ((size_t)blk * p.cache.kv_heads + h) * bs * D;
-        int s = fp8_scale_byte(m);
-        const int was = off0 > 0 ? *scale : 0;
-        if (was < s && off0 > 0) {
-            // the block's own exponent grew: its earlier tokens' codes, rounded to it.  16
-            // bytes are a token's 16 dims (keys) or a dim's 16 tokens (values, of
-            // which those before off0 are meant)
-            const float f = exp2i(max(was - s, -126));
-            for (int u = tid; u < bs / 16 * D; u += kAppendThreads) {
-                const int first = is_v ? u / D * 16 : u / D * 16 + u % 16;
-                if (first >= off0)
-                    continue;
-                uint4 c = reinterpret_cast<uint4 *>(codes)[u];
-                uint32_t *w = reinterpret_cast<uint32_t *>(&c);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t o = 0;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t h2 = e4m3x2_to_f16x2((uint16_t)(w[q] >> (16 * e)));
-                        const float2 f2 = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
-                        o |= fp8_pair(f2.x, f2.y, f) << (16 * e);
-                    }
-                    const int held = is_v ? off0 - first - 4 * q : 4;      // of the word's four codes
-                    const uint32_t keep = held >= 4 ? 0xFFFFFFFFu : held <= 0 ? 0u : (1u << (8 * held)) - 1;
-                    w[q] = (o & keep) | (w[q] & ~keep);
-                }
-                reinterpret_cast<uint4 *>(codes)[u] = c;
-            }
-        } else if (off0 > 0) {
-            s = was;
-        }
+        m = __reduce_max_sync(0xffffffffu, s_max[lane % kAppendWarps]);
+        const int s = max(fp8_scale_byte(m), was);
+        if (off0 > 0 && was < s)
+            recode_block<D, 1>(codes, is_v, off0, exp2i(max(was - s, -126)), tid, kAppendThreads);
         __syncthreads();                                // old scale read, old codes rewritten
         if (tid == 0)
             *scale = (uint8_t)s;
@@ -251,10 +338,10 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendProblem
             if (i * kTok < n && r < n) {
                 const uint2 c = fp8_from_bf16x8(x[i], inv);
                 if (is_v) {
-                    *reinterpret_cast<uint2 *>(s_code + r * D + lane8) = c;
+                    *reinterpret_cast<uint2 *>(s_code + r * D + dim) = c;
                 } else {
                     const int o = off0 + r;
-                    *reinterpret_cast<uint2 *>(codes + (o >> 4) * 16 * D + (lane8 >> 4) * 256 + (o & 15) * 16 + (lane8 & 15)) = c;
+                    *reinterpret_cast<uint2 *>(codes + (o >> 4) * 16 * D + (dim >> 4) * 256 + (o & 15) * 16 + (dim & 15)) = c;
                 }
             }
         }
@@ -279,8 +366,6 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendProblem
                 }
             }
         }
-        if (tid == 0)
-            s_len = bs;
         __syncthreads();                                // s_code, s_max free for the next run
     }
 }
@@ -302,11 +387,13 @@ cudaError_t launch_kv_tables(const TablesProblem &p, cudaStream_t stream) {
 }
 
 cudaError_t launch_kv_append(const AppendProblem &p, cudaStream_t stream) {
-    const int window = p.T <= 512 ? 1 : 16;
+    // few tokens: a run for each warp, were all of them short; many: fewer CTAs that find no run to begin
+    // (us with 8 and with 32 tokens a CTA: 5,000 prompt tokens 23.4 and 16.0, 600 prompt tokens 5.1 and 9.2,
+    // 600 tokens of as many requests 11.0 and 12.5)
+    const int window = p.T <= 1024 ? kAppendWarps : kAppendWindow;
     const dim3 grid((p.T + window - 1) / window, p.cache.kv_heads, 2);
-    if (p.cache.head_dim == 64)
-        return launch_pdl(kv_append_kernel<64>, grid, dim3(kAppendThreads), 0, stream, p, window);
-    return launch_pdl(kv_append_kernel<128>, grid, dim3(kAppendThreads), 0, stream, p, window);
+    return p.cache.head_dim == 64 ? launch_pdl(kv_append_kernel<64>, grid, dim3(kAppendThreads), 0, stream, p, window)
+                                  : launch_pdl(kv_append_kernel<128>, grid, dim3(kAppendThreads), 0, stream, p, window);
 }
 
 }  // namespace moe
