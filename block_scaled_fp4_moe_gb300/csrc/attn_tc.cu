@@ -112,6 +112,17 @@ __device__ __forceinline__ void tmem_ld32(float (&v)[32], uint32_t addr) {
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(float (&v)[16], uint32_t addr) {
+    uint32_t *u = reinterpret_cast<uint32_t *>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]), "=r"(u[9]),
+          "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(addr)
+        : "memory");
+}
+
 // Two fp32 values in one instruction each.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
     uint64_t r;
@@ -701,20 +712,32 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
 
         // ---- the rows' result: l is NaN where a score was, and then so is the row
         const float mz = m == -INFINITY ? 0.0f : m, bz = big == -INFINITY ? 0.0f : big;
-        const float scale = l == 0.0f ? 0.0f : exp2f(bz - mz) / l, lse2 = l == 0.0f ? -INFINITY : mz + log2f(l);
-        // workers of the unit: its CTAs, twice those with two tiles or more where the halves share rows
-        Workers w{1, 0, 0};
+        float scale = l == 0.0f ? 0.0f : exp2f(bz - mz) / l, lse2 = l == 0.0f ? -INFINITY : mz + log2f(l);
         const int ctas = pc.last - pc.first + 1;
+        // Halves that share the rows of an uncut unit join here: through the space of their queries, which nothing reads
+        // any more, each learns the other's sum, and makes half of the dims from both products.
+        const bool both = !pair && ctas == 1 && n > 1;
+        float other_scale = 0.0f;
+        if (both) {
+            *reinterpret_cast<float2 *>(q_at) = make_float2(scale, lse2);
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            named_barrier_sync(3, 256);
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const float2 other = *reinterpret_cast<const float2 *>(sm + (size_t)(1 - h) * S::kQBytes + tid * 128);
+            const float rm = fmaxf(lse2, other.y), z = rm == -INFINITY ? 0.0f : rm;
+            const float w0 = ex2(lse2 - z), w1 = ex2(other.y - z), rl = w0 + w1, wt = rl == 0.0f ? 0.0f : 1.0f / rl;
+            scale *= w0 * wt;
+            other_scale = other.x * w1 * wt;
+            lse2 = rl == 0.0f ? -INFINITY : rm + log2f(rl);
+        }
+        // workers of a cut unit: its CTAs, twice those with two tiles or more where the halves share rows
+        Workers w{1, 0, 0};
         {
             const int cta = (int)blockIdx.x;
             w.slot = (cta * 2 + (cta == pc.first)) * 2 + h;
             w.ticket = pc.first * 2 + (pair ? h : 0);
-            if (pair || n == 0) {
-                w.count = ctas;
-            } else {
-                // tiles of the unit in the first and the last of its CTAs; those between have pl.per of them
-                w.count = ctas == 1 ? min(2, n) : min(2, pc.first_tiles) + min(2, pc.last_tiles) + (int)min(2ll, pl.per) * (ctas - 2);
-            }
+            // tiles of the unit in the first and the last of its CTAs; those between have pl.per of them
+            w.count = pair || ctas == 1 ? ctas : min(2, pc.first_tiles) + min(2, pc.last_tiles) + (int)min(2ll, pl.per) * (ctas - 2);
         }
         const int rows_here = pair ? min(128, pc.rows - 128 * h) : pc.rows;
         const int cap = min(128, (int)min((long long)p.T * a.group, 128ll));       // rows of a part in the workspace
@@ -729,7 +752,7 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
         const size_t to = (size_t)(pc.q0 + row / a.group) * p.q_heads + pc.head * a.group + row % a.group;
         const NanEntry *nans = reinterpret_cast<const NanEntry *>(static_cast<const uint8_t *>(a.nans) + (size_t)blockIdx.x * kAttnNanBytes);
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = both ? h * (D / 64) : 0; c < (both ? (h + 1) * (D / 64) : D / 32); ++c) {
             float x[32];
             if (mine > 0) {
                 tmem_ld32(x, o_at + 32 * c);
@@ -741,15 +764,26 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
             uint32_t bad = 0;                      // dims whose values this row saw as NaN
             for (uint32_t k = 0; k < min(nan_seen, (uint32_t)kNanEntries); ++k) {
                 const int nu = __ldcg(&nans[k].unit), nt = __ldcg(&nans[k].token);
-                if (nu == unit && nt >= lo && nt < hi && (pair || (((nt / kTile - pc.tile0 - pc.t0) & 1) == h)))
+                if (nu == unit && nt >= lo && nt < hi && (pair || both || (((nt / kTile - pc.tile0 - pc.t0) & 1) == h)))
                     bad |= __ldcg(&nans[k].dims[c]);
             }
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < 32; ++e)
                 x[e] *= scale;
+            if (both) {
+#pragma unroll
+                for (int u = 0; u < 32; u += 16) {
+                    float y[16];
+                    tmem_ld16(y, lanes + 256 + D * (1 - h) + 32 * c + u);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        x[u + e] = fmaf(y[e], other_scale, x[u + e]);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
                 if (bad >> e & 1)
                     x[e] = __uint_as_float(0x7FFFFFFFu);
-            }
             if (live && w.count == 1) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 8) {
@@ -769,8 +803,12 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
                     __stcg(dst + (size_t)(e / 4) * cap, make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]));
             }
         }
+        if (both) {                                // the products may be made anew
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            named_barrier_sync(3, 256);
+        }
         if (live && w.count == 1) {
-            if (p.lse)
+            if (p.lse && (!both || h == 0))
                 p.lse[to] = lse2 * 0.69314718055994530942f;
         } else if (live) {
             __stcg(a.part_lse + (size_t)w.slot * cap + tid, lse2);

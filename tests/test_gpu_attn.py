@@ -666,3 +666,12 @@ def test_attention_many_rows_repeats_bit_for_bit():
     a, la = p.run()
     b, lb = p.run()
     assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+@pytest.mark.parametrize("dim,size,seed", [(64, 32, 39), (128, 16, 40), (128, 64, 41)])
+def test_attention_many_rows_whole_units_beside_cut_ones(dim, size, seed):
+    """A CTA's range holds whole units of two and more tiles (both halves work on the same rows) between parts of others."""
+    p = Problem([(8, 9000)] + [(8, 150 + 70 * i) for i in range(9)], 8, 4, dim, size, seed=seed)
+    a, la = p.check()
+    b, lb = p.run()
+    assert torch.equal(a, b) and torch.equal(la, lb)
