@@ -562,9 +562,9 @@ __device__ __forceinline__ void finish(const AttnArgs &a, const Piece &pc, uint8
                     if (d == 0 && p.lse)
                         p.lse[at] = lse2 * 0.69314718055994530942f;
                 } else {
-                    __stcg(reinterpret_cast<float4 *>(a.part + ((size_t)slot * kRows + row) * D + d), o);
+                    __stcg(reinterpret_cast<float4 *>(a.part + ((size_t)slot * a.part_rows + row) * D + d), o);
                     if (d == 0)
-                        __stcg(a.part_lse + slot * kRows + row, lse2);
+                        __stcg(a.part_lse + (size_t)slot * a.part_rows + row, lse2);
                 }
             }
         }
@@ -592,7 +592,7 @@ __device__ __forceinline__ void finish(const AttnArgs &a, const Piece &pc, uint8
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
                         const int k = k0 + u;
-                        const size_t at = ((size_t)(pc.first + k) * 2 + (k == 0)) * kRows + row;
+                        const size_t at = ((size_t)(pc.first + k) * 2 + (k == 0)) * a.part_rows + row;
                         e[u] = k < pieces ? __ldcg(a.part_lse + at) : -INFINITY;
                         v[u] = k < pieces ? __ldcg(reinterpret_cast<const float4 *>(a.part + at * D + d)) : make_float4(0, 0, 0, 0);
                     }
@@ -715,6 +715,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     }
 }
 
+// Rows of a part in the workspace.
+int part_rows(int T, int group, int rows) { return (int)((long long)T * group < rows ? (long long)T * group : rows); }
+
 int max_row_tiles(int T, int B, int group, int rows) { return (int)((long long)T * group / rows + B); }
 
 }  // namespace
@@ -728,7 +731,7 @@ AttnLayout AttnLayout::make(int T, int B, int q_heads, int kv_heads, int head_di
     L.plan = take(sizeof(Plan));
     L.recs = take((size_t)max_row_tiles(T, B, group, kRows) * sizeof(RowTile));
     // a CTA has parts of at most two units; in the tensor-memory form of up to two row halves or token halves each
-    const size_t cut = rows < kRows ? rows : kRows, tall = rows <= kAttnTcMinRows ? 0 : rows < 128 ? rows : 128;
+    const size_t cut = part_rows(T, group, kRows), tall = rows <= kAttnTcMinRows ? 0 : part_rows(T, group, 128);
     const size_t parts = (size_t)kMaxAttnCtas * (2 * cut > 4 * tall ? 2 * cut : 4 * tall);
     L.part = take(parts * head_dim * sizeof(float));
     L.part_lse = take(parts * sizeof(float));
@@ -743,7 +746,7 @@ cudaError_t launch_kv_attention(const AttnProblem &p, void *ws, int sms, cudaStr
     int shift = 4;
     while ((1 << shift) < p.cache.block_size)
         ++shift;
-    AttnArgs a{p, group, shift, kRows, sms < kMaxAttnCtas ? sms : kMaxAttnCtas, max_row_tiles(p.T, p.B, group, kRows),
+    AttnArgs a{p, group, shift, kRows, part_rows(p.T, group, kRows), sms < kMaxAttnCtas ? sms : kMaxAttnCtas, max_row_tiles(p.T, p.B, group, kRows),
                p.scale * 1.44269504088896340736f, ws_at<Plan>(ws, L.plan), ws_at<RowTile>(ws, L.recs),
                ws_at<uint32_t>(ws, kHeaderBytes), ws_at<float>(ws, L.part), ws_at<float>(ws, L.part_lse),
                ws_at<uint8_t>(ws, L.nans), ws_at<uint32_t>(ws, 0)};

@@ -31,7 +31,7 @@ struct Plan {
 struct AttnArgs {
     AttnProblem p;
     int group, shift;                    // query heads of a key/value head; log2(block_size)
-    int rows;                            // of a unit
+    int rows, part_rows;                 // of a unit; of a part in the workspace
     int ctas, max_tiles;
     float scale_log2;
     Plan *plan;

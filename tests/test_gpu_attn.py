@@ -675,3 +675,18 @@ def test_attention_many_rows_whole_units_beside_cut_ones(dim, size, seed):
     a, la = p.check()
     b, lb = p.run()
     assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+@pytest.mark.parametrize("kv_heads,group,dim,lens", [
+    (2, 1, 128, [(1, 2516), (1, 1623)]), (2, 3, 128, [(1, 18298)]), (2, 4, 64, [(1, 3609)]), (1, 1, 64, [(1, 9000)]), (1, 1, 128, [(1, 1)]),
+    (8, 5, 128, [(1, 1000)]), (4, 4, 64, [(14, 5000)]), (8, 1, 64, [(1, 900 * i + 1) for i in range(6)]), (2, 16, 128, [(3, 7000)]),
+    (8, 4, 128, [(8, 5000)] * 8), (8, 1, 64, [(26, 800 * i + 30) for i in range(9)])])
+def test_attention_few_rows_cut_into_many_parts(kv_heads, group, dim, lens):
+    """Fewer rows than a unit's: their parts lie close together in a workspace of just the size asked for, and none past its end."""
+    p = Problem(lens, kv_heads, group, dim, 32, seed=42)
+    n = attn.moe_kv_attention_workspace_size(p.T, len(lens), kv_heads * group, kv_heads, dim)
+    guarded = torch.full((n + (1 << 24),), 0xA5, dtype=torch.uint8, device="cuda")
+    guarded[:n] = 0
+    p.check(ws=guarded[:n])
+    p.check(causal=False, window=700, ws=guarded[:n])
+    assert bool((guarded[n:] == 0xA5).all())
