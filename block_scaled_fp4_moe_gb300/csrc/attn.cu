@@ -750,11 +750,13 @@ cudaError_t launch_kv_attention(const AttnProblem &p, void *ws, int sms, cudaStr
                p.scale * 1.44269504088896340736f, ws_at<Plan>(ws, L.plan), ws_at<RowTile>(ws, L.recs),
                ws_at<uint32_t>(ws, kHeaderBytes), ws_at<float>(ws, L.part), ws_at<float>(ws, L.part_lse),
                ws_at<uint8_t>(ws, L.nans), ws_at<uint32_t>(ws, 0)};
-    // The tensor-memory form where requests have more than 24 rows on average (16 requests of 1..4 tokens x 12 heads of
-    // a group: 148 us against 179; of 1..3 x 8: 174 against 129) and there are units enough that its longer way from
-    // a unit's start to its end does not show (one request of 4 x 8 rows over 30,000 tokens: 60 us against 42).
+    // The tensor-memory form where requests have more than 24 rows on average (us of it and of this one: 16 requests of
+    // 1..4 tokens x 12 heads of a group 143 and 173, 32 of 10 x 4 rows 157 and 188; of 1..3 x 8 154 and 120; requests of 32 rows
+    // each, 153 and 124, are the price of telling them from ragged ones by the average alone) and there are units enough
+    // that its longer way from a unit's start to its end does not show (16 x 8 rows of four requests over 20,000 tokens 93
+    // and 99, of two 89 and 77).
     const long long rows = (long long)p.T * group, units = ((rows + kAttnTcRows - 1) / kAttnTcRows + p.B - 1) * p.cache.kv_heads;
-    const bool tall = rows > (long long)kAttnTcMinRows * p.B && units >= 64;
+    const bool tall = rows > (long long)kAttnTcMinRows * p.B && units >= 32;
     auto go = [&](auto kernel, size_t smem) {
         cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         return r != cudaSuccess ? r : launch_pdl(kernel, dim3(a.ctas), dim3(kThreads), smem, stream, a);

@@ -15,17 +15,25 @@
 // product that they wait for; at D = 128 they lie over the scores just read.  One half's softmax runs
 // beside the other half's products.
 //
-// Warps: 0..7 softmax (warp % 4 = TMEM lane quarter, warp / 4 the half; a thread has a row), 8..13 convert, 14 streams the cache, 15 issues the
-// MMAs.  What bounds it is the issue of the softmax and of the conversion.  (Two threads to a row, 16 warps of at most 88 registers, took as long:
-// more latency hidden, more moves and exchanges.)  The operands pass in the order K0, K1, V0, K2, V1, ...: as codes into a ring of raw tiles
+// Warps: 0..7 softmax (warp % 4 = TMEM lane quarter, warp / 4 the half; a thread has a row), 8..13 convert, 14 streams the cache,
+// 15 issues the MMAs.  (Two threads to a row, 16 warps of at most 88 registers, took as long: more latency hidden, more moves
+// and exchanges.)
+//
+// Measured: three requests' chunks of 500 tokens over 9,000, 48 query heads of 64, 147 us (563 TFLOP/s), bound by the softmax's issue
+// (a quarter of its steps left out: 119 us; of the conversion's: 171); chunks of 600 over 16,000, 40 heads of 128, 478 us (905 TFLOP/s),
+// where shared memory, read and written for codes, operands and products, is busy three quarters of the time; 16 requests of up to 48 rows
+// over 10,000 tokens 143 us, bound by a tile's way through conversion, product, softmax and product with few rows.
+//
+// The operands pass in the order K0, K1, V0, K2, V1, ...: as codes into a ring of raw tiles
 // by bulk copies, then as f16 into a ring of operand tiles, rows (tokens of K, dims of V) of 64
 // elements in the 128-byte swizzle.  The cache's innermost 16 bytes run along the summed axis for both, so the two
 // conversions are the same code.
 //
-// The running maxima of a row are references that move only where a score has outgrown them (M by 2^8: w stays below
-// that, and f16's rounding is relative): then the half waits for its last product and rescales O in TMEM.  Where the
-// weights have columns of their own a tile is tried with the references as they are and made again if they move: its
-// scores are read once.
+// The running maxima of a row are references that move only where scores have outgrown them (16 weights sum to more than
+// 2^12: f16 holds up to 2^16, and its rounding is relative).  So a score is read once: 32 of a row at a time become weights,
+// whose sums say whether they fit.  Where they do not, the references move to the maxima (of the tile, which is then made
+// again, or of the 32 where the weights lie over the scores), the half waits for its last product and rescales O, and the
+// tile's weights so far, in TMEM.  Only a unit's first tile is read for its maxima first.
 #include "attn_plan.cuh"
 
 namespace moe {
@@ -34,7 +42,8 @@ namespace {
 constexpr int kSoftWarps = 8, kConvWarps = 6;
 constexpr int kTcThreads = (kSoftWarps + kConvWarps + 2) * 32;
 constexpr int kNanEntries = 2048;
-constexpr float kLazy = 8.0f;
+// What 16 weights may sum to before the references move; 2^-32: with that factor, what 16 terms of l may.
+constexpr float kMostWeight = 4096.0f, kLeastSum = 0x1p-32f;
 
 // A value's NaN codes in a tile that some rows see in part: the unit, the position, the dims.
 struct NanEntry {
@@ -603,17 +612,15 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
                     return fmaxf(max3(v0, v1, v2), v3) * fi;
                 };
                 auto factor = [&](int k) { return fmaxf(f * meta[k], 1.2e-38f); };
-                // whether a score with this exponent outgrows the references
-                auto outgrows = [&](float top, float b) {
-                    return m == -INFINITY || big == -INFINITY ? top > -INFINITY : fmaxf(top + b - big, top - m - 32.0f) > kLazy + 0.01f;
-                };
-                // moves the references to the tile's maxima (of x, and of x + b) where they lie above
-                auto move = [&](float nm, float nb) {
+                // moves the references to these maxima (of x, and of x + b) where they lie above; the tile's first `chunks` of
+                // 32 weights are stored already
+                auto move = [&](float nm, float nb, int chunks) {
                     if (nm > m) {
                         l *= m == -INFINITY ? 0.0f : ex2(m - nm);
                         m = nm;
                     }
-                    const float to = nb > big + kLazy || big == -INFINITY ? nb : big, r = big == -INFINITY ? 0.0f : ex2(big - to);
+                    const float to = fmaxf(nb, big), r = big == -INFINITY ? 0.0f : ex2(big - to);
+                    big = to;
                     if (i > 0) {                   // the half's last product is done
                         wait(b.o_done + h, (on - 1) & 1);
 #pragma unroll 1
@@ -626,77 +633,111 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
                             tmem_st32(o_at + 32 * c, x);
                         }
                     }
-                    big = to;
-                };
-                auto maxima = [&](float &nm, float &nb) {
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    const __half2 r2 = __float2half2_rn(r);
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        float x[32];
-                        tmem_ld32(x, s_at + 32 * c);
-                        if (edge)
-                            hide(x, tok0 + 32 * c, lo, hi);
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const float v = top_of(x + 16 * u, factor(2 * c + u));
-                            nm = fmaxf(nm, v);
-                            nb = fmaxf(nb, v + meta[kSubs + 2 * c + u]);
-                        }
-                    }
-                };
-                if (!S::kOwnW) {
-                    // the weights will lie over the scores: the references are settled first
-                    float nm = -INFINITY, nb = -INFINITY;
-                    maxima(nm, nb);
-                    if (__any_sync(0xffffffffu, outgrows(nm, nb - nm)))
-                        move(nm, nb);
-                } else if (i > 0) {
-                    // the last tile's product, issued after these scores, must have read its weights
-                    wait(b.o_done + h, (on - 1) & 1);
-                }
-                for (;;) {
-                    const float mz = m == -INFINITY ? 0.0f : m, bz = big == -INFINITY ? 0.0f : big;
-                    const uint64_t minus_m = pack2(-mz, -mz);
-                    uint64_t sum0 = 0, sum1 = 0;
-                    bool grew = false;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float x[32];
-                        tmem_ld32(x, s_at + 32 * c);
-                        if (edge)
-                            hide(x, tok0 + 32 * c, lo, hi);
+                    for (int c = 0; c < chunks; ++c) {
                         uint32_t w[16];
+                        tmem_ld16(reinterpret_cast<float(&)[16]>(w), lanes + S::w_col(h, 32 * c));
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const float fi = factor(2 * c + u), bb = meta[kSubs + 2 * c + u];
-                            const float *y = x + 16 * u;
-                            if (S::kOwnW)
-                                grew |= outgrows(top_of(y, fi), bb);
-                            const float r = ex2(fminf(bb + (mz - bz), 126.0f));
-                            const uint64_t fi2 = pack2(fi, fi), r2 = pack2(r, r);
-#pragma unroll
-                            for (int e = 0; e < 16; e += 2) {
-                                const float2 t2 = unpack2(fma2(pack2(y[e], y[e + 1]), fi2, minus_m));
-                                const uint64_t p2 = pack2(ex2(t2.x), ex2(t2.y));
-                                if (e & 2)
-                                    sum0 = add2(sum0, p2);
-                                else
-                                    sum1 = add2(sum1, p2);
-                                const float2 w2 = unpack2(mul2(p2, r2));
-                                const __half2 h2 = __floats2half2_rn(w2.x, w2.y);
-                                w[8 * u + e / 2] = *reinterpret_cast<const uint32_t *>(&h2);
-                            }
+                        for (int e = 0; e < 16; ++e) {
+                            const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(w + e), r2);
+                            w[e] = *reinterpret_cast<const uint32_t *>(&v);
                         }
                         tmem_st16(lanes + S::w_col(h, 32 * c), w);
                     }
-                    if (!S::kOwnW || !__any_sync(0xffffffffu, grew)) {
-                        const float2 s2 = unpack2(add2(sum0, sum1));
-                        l += s2.x + s2.y;
-                        break;
+                };
+                auto chunk_maxima = [&](const float *x, int c, float &nm, float &nb) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const float v = top_of(x + 16 * u, factor(2 * c + u));
+                        nm = fmaxf(nm, v);
+                        nb = fmaxf(nb, v + meta[kSubs + 2 * c + u]);
                     }
-                    // made again with the references moved (a unit's first tile, and rarely after that)
+                };
+                auto scores = [&](float (&x)[32], int c) {
+                    tmem_ld32(x, s_at + 32 * c);
+                    if (edge)
+                        hide(x, tok0 + 32 * c, lo, hi);
+                };
+                auto to_maxima = [&]() {           // of the tile
                     float nm = -INFINITY, nb = -INFINITY;
-                    maxima(nm, nb);
-                    move(nm, nb);
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        float x[32];
+                        scores(x, c);
+                        chunk_maxima(x, c, nm, nb);
+                    }
+                    move(nm, nb, 0);
+                };
+                // 32 scores to weights; their terms of l to sum; whether they outgrew the references
+                auto weigh = [&](const float (&x)[32], int c, uint32_t (&w)[16], float &sum) {
+                    const float mz = m == -INFINITY ? 0.0f : m, bz = big == -INFINITY ? 0.0f : big;
+                    const uint64_t minus_m = pack2(-mz, -mz);
+                    bool grew = false;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const float *y = x + 16 * u;
+                        const float fi = factor(2 * c + u), bb = meta[kSubs + 2 * c + u];
+                        const float r = ex2(fminf(bb + (mz - bz), 126.0f));
+                        const uint64_t fi2 = pack2(fi, fi), r2 = pack2(r, r);
+                        uint64_t s2[2];
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            const float2 t2 = unpack2(fma2(pack2(y[e], y[e + 1]), fi2, minus_m));
+                            const uint64_t p2 = pack2(ex2(t2.x), ex2(t2.y));
+                            s2[e >> 1 & 1] = e < 4 ? p2 : add2(s2[e >> 1 & 1], p2);
+                            const float2 w2 = unpack2(mul2(p2, r2));
+                            const __half2 h2 = __floats2half2_rn(w2.x, w2.y);
+                            w[8 * u + e / 2] = *reinterpret_cast<const uint32_t *>(&h2);
+                        }
+                        const float2 t = unpack2(add2(s2[0], s2[1]));
+                        const float s16 = t.x + t.y;
+                        sum += s16;
+                        grew |= fmaxf(s16 * r, s16 * kLeastSum) > kMostWeight;
+                    }
+                    return grew;
+                };
+                // where weights have columns of their own these scores came before the last product: it must have read its weights
+                if (S::kOwnW && i > 0)
+                    wait(b.o_done + h, (on - 1) & 1);
+                if (__any_sync(0xffffffffu, big == -INFINITY))           // no references yet
+                    to_maxima();
+                // The loops are rolled: unrolled, their instructions cost more to fetch than the steps they save (9 to 12 % of the kernel).
+                if (S::kOwnW) {
+                    // the scores outlive the weights: one vote a tile (four take 159 us for 147)
+                    for (;;) {
+                        float sum = 0.0f;
+                        bool grew = false;
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            float x[32];
+                            uint32_t w[16];
+                            scores(x, c);
+                            grew |= weigh(x, c, w, sum);
+                            tmem_st16(lanes + S::w_col(h, 32 * c), w);
+                        }
+                        if (!__any_sync(0xffffffffu, grew)) {
+                            l += sum;
+                            break;
+                        }
+                        to_maxima();
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        float x[32], sum = 0.0f;
+                        uint32_t w[16];
+                        scores(x, c);
+                        while (__any_sync(0xffffffffu, weigh(x, c, w, sum))) {
+                            float nm = -INFINITY, nb = -INFINITY;
+                            chunk_maxima(x, c, nm, nb);
+                            move(nm, nb, c);
+                            sum = 0.0f;
+                        }
+                        l += sum;
+                        tmem_st16(lanes + S::w_col(h, 32 * c), w);
+                    }
                 }
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             }

@@ -690,3 +690,15 @@ def test_attention_few_rows_cut_into_many_parts(kv_heads, group, dim, lens):
     p.check(ws=guarded[:n])
     p.check(causal=False, window=700, ws=guarded[:n])
     assert bool((guarded[n:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("step,q_scale", [(1, 1.0), (3, 4.0), (-2, 4.0)])
+def test_attention_many_rows_references_move_inside_a_tile(dim, step, q_scale):
+    """Key exponents that climb (or fall) from block to block of 16 tokens, eight to a tile, and values' exponents against them."""
+    p = Problem([(9, 700), (9, 130)] * 5, 8, 4, dim, 16, seed=43, q_scale=q_scale)
+    for row, kv in zip(p.table, p.kv):
+        for i in range(-(-kv // 16)):
+            p.cache.ke[row[i]] = -14 + step * (i % 11)
+            p.cache.ve[row[i]] = -3 * step * (i % 7)
+    p.check()
