@@ -91,11 +91,27 @@ class KVCache:
     k [num_blocks, kv_heads, block_size/16, head_dim/16, 16 tokens, 16 dims],
     v [num_blocks, kv_heads, block_size/16, head_dim, 16 tokens],
     k_scale, v_scale [num_blocks, kv_heads]."""
-    __slots__ = ("k", "v", "k_scale", "v_scale", "num_blocks", "kv_heads", "head_dim", "block_size")
+    __slots__ = ("k", "v", "k_scale", "v_scale")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        _native().check_cache(k, v, k_scale, v_scale)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.num_blocks, self.kv_heads, self.head_dim, self.block_size = _native().check_cache(k, v, k_scale, v_scale)
+
+    @property
+    def num_blocks(self) -> int:
+        return self.k.shape[0]
+
+    @property
+    def kv_heads(self) -> int:
+        return self.k.shape[1]
+
+    @property
+    def head_dim(self) -> int:
+        return 16 * self.k.shape[3]
+
+    @property
+    def block_size(self) -> int:
+        return 16 * self.k.shape[2]
 
     @staticmethod
     def empty(num_blocks: int, kv_heads: int, head_dim: int, block_size: int, device="cuda") -> "KVCache":
@@ -109,11 +125,19 @@ class KVCache:
 
 class FP8Weight:
     """codes uint8 [N, K] (E4M3) and scale uint8 [ceil(N/128), ceil(K/128)] (E8M0)."""
-    __slots__ = ("codes", "scale", "n", "k")
+    __slots__ = ("codes", "scale")
 
     def __init__(self, codes: torch.Tensor, scale: torch.Tensor):
+        _native().check_weight(codes, scale)
         self.codes, self.scale = codes, scale
-        self.n, self.k = _native().check_weight(codes, scale)
+
+    @property
+    def n(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def k(self) -> int:
+        return self.codes.shape[1]
 
     @staticmethod
     def from_dense(w: torch.Tensor, stream=None) -> "FP8Weight":

@@ -36,6 +36,11 @@
 // B operand of one MMA, or of two with 32 rows.  Thread (g, c) of a warp holds codes
 // 4c .. 4c+3, as K positions 2c, 2c+1, 2c+8, 2c+9: q's dims (and, for the
 // values, the weights' tokens) are taken in that order.
+//
+// Measured, key/value heads of 128: 64 requests of 31,000 tokens, 8 heads with 8 query heads each, 586 us (6.7 TB/s, the rate of a copy: bound by
+// memory); 48 ragged requests of 5,000 in blocks of 16, 102 us (5.2 TB/s: a request's first tiles and last join are a larger part);
+// one of 1,000, 10.7 us (launch, plan, block ids, tiles, join: latency).  24 rows a request run at 3.5 TB/s and 32
+// at 3.2, bound by the chain of products and powers in eight warps.
 #include "attn_plan.cuh"
 
 namespace moe {
@@ -282,8 +287,9 @@ struct Acc {
 };
 
 // One piece's tiles: RG groups of MT x 16 rows; the warps of a row group form SG sets that take tiles in turn, those of
-// a set sharing a tile's sub-blocks.  (SG = 2 at 16 rows: a warp's chain of products, maxima and powers is as long for 32
-// tokens as for 16.)
+// a set sharing a tile's sub-blocks.  (SG = 2 where all warps have the same rows: a warp's chain of products, maxima and powers
+// is as long for 32 tokens as for 16.  One set: 64 requests of 31,000 tokens and 8 rows take 694 us for 600, 32 of 8,000 tokens
+// and 24 rows 120 for 105.)
 template <int D, int MT, int RG, int SG>
 __device__ __forceinline__ void attend(const Piece &pc, uint8_t *sm, int qbuf, uint64_t *full, uint64_t *empty, uint32_t *hdr,
                                        long long &it, bool &dead, Acc<D, MT> &acc) {
@@ -645,7 +651,7 @@ __device__ __forceinline__ void consume_piece(const AttnArgs &a, const Piece &pc
             acc.l[mt][s] = 0.0f;
         }
     }
-    attend<D, MT, RG, MT == 1 ? 2 : 1>(pc, sm, qbuf, full, empty, a.hdr, it, dead, acc);
+    attend<D, MT, RG, RG == 1 ? 2 : 1>(pc, sm, qbuf, full, empty, a.hdr, it, dead, acc);
     __syncwarp();
     if ((threadIdx.x & 31) == 0)
         mbar_arrive(q_empty);
@@ -751,8 +757,8 @@ cudaError_t launch_kv_attention(const AttnProblem &p, void *ws, int sms, cudaStr
                ws_at<uint32_t>(ws, kHeaderBytes), ws_at<float>(ws, L.part), ws_at<float>(ws, L.part_lse),
                ws_at<uint8_t>(ws, L.nans), ws_at<uint32_t>(ws, 0)};
     // The tensor-memory form where requests have more than 24 rows on average (us of it and of this one: 16 requests of
-    // 1..4 tokens x 12 heads of a group 143 and 173, 32 of 10 x 4 rows 157 and 188; of 1..3 x 8 154 and 120; requests of 32 rows
-    // each, 153 and 124, are the price of telling them from ragged ones by the average alone) and there are units enough
+    // 1..4 tokens x 12 heads of a group 143 and 175, 32 of 10 x 4 rows 157 and 191; of 1..3 x 8 154 and 105; requests of 32 rows
+    // each, 153 and 112, are the price of telling them from ragged ones by the average alone) and there are units enough
     // that its longer way from a unit's start to its end does not show (16 x 8 rows of four requests over 20,000 tokens 93
     // and 99, of two 89 and 77).
     const long long rows = (long long)p.T * group, units = ((rows + kAttnTcRows - 1) / kAttnTcRows + p.B - 1) * p.cache.kv_heads;
