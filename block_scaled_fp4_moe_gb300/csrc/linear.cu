@@ -187,8 +187,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) fp8_gemm_kernel(const
     const Range r0(a);
 
     if (warp == 0) {
-        // ---- copies.  W does not depend on the quantisation of x: the first
-        // stages' W goes out before the wait for that kernel.
+        // ---- copies.  W does not depend on the quantisation of x: the first stages' W goes out before the wait for that
+        // kernel, which itself waited for all that came before.  Without one (fused) the kernel before may be the one that
+        // writes W: then it is only asked into L2 ahead of the wait.
         auto stage_w = [&](int st, int tile, int kb) {
             mbar_arrive_expect_tx(full + st, kABytes + (FUSED ? 0 : S::kB + 512 * S::kBlobs));
             tma_2d(smem_u32(sm + (size_t)st * kABytes), &wmap, kb * kStageK, tile % a.n_tiles * 128, full + st);
@@ -205,7 +206,15 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) fp8_gemm_kernel(const
                 : "memory");
         };
         long long it = 0;                   // stages issued
-        bool dead = false, waited = false;
+        bool dead = false, waited = FUSED;
+        if (FUSED) {
+            if (lane < kStages && r0.kb0 + lane < r0.kb1)
+                asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(&wmap)),
+                             "r"((r0.kb0 + lane) * kStageK), "r"(r0.tile % a.n_tiles * 128)
+                             : "memory");
+            pdl_wait();
+            pdl_trigger();
+        }
         for (int tile = r0.tile; tile < a.tiles && !dead; tile += r0.step) {
             for (int kb = r0.kb0; kb < r0.kb1; ++kb, ++it) {
                 const int st = (int)(it % kStages);
@@ -285,6 +294,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) fp8_gemm_kernel(const
         __syncwarp();
     } else if (warp >= 6) {
         // ---- W's scale, warps in turn: a stage's blob is one byte throughout
+        if (FUSED)
+            pdl_wait();
         long long it = 0;
         bool dead = false;
         for (int tile = r0.tile; tile < a.tiles && !dead; tile += r0.step) {

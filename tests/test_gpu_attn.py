@@ -702,3 +702,30 @@ def test_attention_many_rows_references_move_inside_a_tile(dim, step, q_scale):
             p.cache.ke[row[i]] = -14 + step * (i % 11)
             p.cache.ve[row[i]] = -3 * step * (i % 7)
     p.check()
+
+
+@pytest.mark.parametrize("T", [1, 8, 40])
+def test_linear_directly_after_its_weights(T):
+    """Weights written by the kernel just before, the library's own or another, are the ones that the product reads."""
+    N, K = 4096, 7168
+    rng = np.random.default_rng(44)
+    x = bf16(rng.standard_normal((T, K)))
+    dense = [torch.randn(N, K, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    w = [attn.FP8Weight.from_dense(d) for d in dense]
+    ws = workspace(attn.moe_linear_fp8_workspace_size(T, N, K))
+    want = [torch.empty(T, N, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for i in range(2):
+        attn.moe_linear_fp8(x, w[i], want[i], ws)
+    torch.cuda.synchronize()
+    one = attn.FP8Weight(w[0].codes.clone(), w[0].scale.clone())
+    got = [torch.empty_like(want[0]) for _ in range(40)]
+    torch.cuda.synchronize()
+    for i, y in enumerate(got):
+        if i % 4 < 2:
+            attn.moe_quantize_fp8_weight(dense[i % 2], one)
+        else:
+            one.codes.copy_(w[i % 2].codes)
+            one.scale.copy_(w[i % 2].scale)
+        attn.moe_linear_fp8(x, one, y, ws)
+    torch.cuda.synchronize()
+    assert [i for i, y in enumerate(got) if not torch.equal(y, want[i % 2])] == []
