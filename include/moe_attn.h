@@ -119,7 +119,7 @@ size_t moe_kv_attention_workspace_size(int T, int B, int q_heads, int kv_heads, 
  * Device-side errors (MOE_ERR_DEVICE_ASSERT): q_offsets that decrease or leave 0..T, a
  * kv_len outside 0..max_blocks * block_size (out stays untouched); a block id outside the
  * cache (that block is read as block 0).  B <= 8192, T <= 2^20,
- * q_heads / kv_heads <= 256.  Three
+ * q_heads / kv_heads <= 256.  Two
  * launches at most.
  */
 moe_status_t moe_kv_attention(const uint16_t *q, int64_t q_stride_t, int64_t q_stride_h, int T, int q_heads,
