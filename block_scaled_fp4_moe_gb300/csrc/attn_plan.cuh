@@ -45,7 +45,7 @@ struct AttnArgs {
 // The positions that a row of a request with n new of kv tokens sees: [lo, hi).
 __device__ __forceinline__ void row_range(const AttnProblem &p, int group, int kv, int n, int row, int &lo, int &hi) {
     const int pos = kv - n + row / group;
-    lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+    lo = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
     hi = p.causal ? max(0, min(kv, pos + 1)) : kv;
     if (lo > hi)
         lo = hi;

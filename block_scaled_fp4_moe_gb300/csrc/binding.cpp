@@ -72,6 +72,9 @@ const at::Tensor &heads(PyObject *o, const char *name) {
     return t;
 }
 
+// The stride of an axis; that of an axis of one element is never used, whatever it says.
+int64_t step(const at::Tensor &t, int axis) { return t.size(axis) > 1 ? t.stride(axis) : 0; }
+
 template <typename P>
 P *at_of(const at::Tensor &t) {
     return reinterpret_cast<P *>(t.data_ptr());
@@ -224,8 +227,8 @@ PyObject *kv_append(PyObject *, PyObject *const *o, Py_ssize_t n) {
         const int64_t T = slots.numel();
         want(k, {T, c.kv_heads, c.head_dim}, "k");
         want(v, {T, c.kv_heads, c.head_dim}, "v");
-        return PyLong_FromLong(lib.append(at_of<uint16_t>(k), k.stride(0), k.stride(1), at_of<uint16_t>(v), v.stride(0),
-                                          v.stride(1), at_of<int64_t>(slots), narrow(T, "slot_map"), &c, at_of<void>(ws),
+        return PyLong_FromLong(lib.append(at_of<uint16_t>(k), step(k, 0), step(k, 1), at_of<uint16_t>(v), step(v, 0),
+                                          step(v, 1), at_of<int64_t>(slots), narrow(T, "slot_map"), &c, at_of<void>(ws),
                                           (size_t)ws.numel(), stream_of(o[8])));
     });
 }
@@ -250,7 +253,7 @@ PyObject *kv_attention(PyObject *, PyObject *const *o, Py_ssize_t n) {
             lse = at_of<float>(l);
         }
         return PyLong_FromLong(lib.attention(
-            at_of<uint16_t>(q), q.stride(0), q.stride(1), narrow(T, "q"), narrow(H, "q"), &c, at_of<int32_t>(table),
+            at_of<uint16_t>(q), step(q, 0), step(q, 1), narrow(T, "q"), narrow(H, "q"), &c, at_of<int32_t>(table),
             narrow(table.size(1), "block_table"), at_of<int32_t>(qo), at_of<int32_t>(kv), narrow(B, "kv_lens"),
             (float)real(o[8]), truth(o[12]), integer(o[13], "window"), at_of<uint16_t>(out), lse, at_of<void>(ws),
             (size_t)ws.numel(), stream_of(o[14])));

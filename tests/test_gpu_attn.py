@@ -729,3 +729,25 @@ def test_linear_directly_after_its_weights(T):
         attn.moe_linear_fp8(x, one, y, ws)
     torch.cuda.synchronize()
     assert [i for i, y in enumerate(got) if not torch.equal(y, want[i % 2])] == []
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_widest_window(causal):
+    """The largest window a call can name, with requests that bring more tokens than the cache holds of them."""
+    Problem([(9, 3), (4, 200), (1, 1)], 2, 4, 64, 16, seed=45).check(causal, 2 ** 31 - 1)
+    Problem([(40, 30), (30, 200), (30, 3)] * 2, 8, 8, 128, 16, seed=46).check(causal, 2 ** 31 - 1)
+
+
+def test_single_token_strides_do_not_matter():
+    """A lone token's, or head's, stride is not used: whatever a view gives is taken."""
+    p = Problem([(1, 77)], 1, 1, 64, 16, seed=47)
+    want, want_lse = p.check()
+    p.q = p.q.contiguous().as_strided((1, 1, 64), (3, 5, 1))
+    got, lse = p.check()
+    assert torch.equal(got, want) and torch.equal(lse, want_lse)
+    x, w = bf16(np.random.default_rng(48).standard_normal((1, 64))), attn.FP8Weight.from_dense(bf16(np.eye(64)))
+    ws = workspace()
+    y = [torch.empty(1, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    attn.moe_linear_fp8(x, w, y[0], ws)
+    attn.moe_linear_fp8(x.as_strided((1, 64), (7, 1)), w, y[1], ws)
+    assert torch.equal(*y)
