@@ -39,7 +39,7 @@
 //
 // Measured, key/value heads of 128: 64 requests of 31,000 tokens, 8 heads with 8 query heads each, 586 us (6.7 TB/s, the rate of a copy: bound by
 // memory); 48 ragged requests of 5,000 in blocks of 16, 102 us (5.2 TB/s: a request's first tiles and last join are a larger part);
-// one of 1,000, 10.7 us (launch, plan, block ids, tiles, join: latency).  24 rows a request run at 3.5 TB/s and 32
+// one of 1,000, 9.8 us (launch, plan, block ids, tiles, join: latency).  24 rows a request run at 3.5 TB/s and 32
 // at 3.2, bound by the chain of products and powers in eight warps.
 #include "attn_plan.cuh"
 
@@ -465,6 +465,33 @@ __device__ __forceinline__ void attend(const Piece &pc, uint8_t *sm, int qbuf, u
                         mma_m16n8k16_f16(acc.o[mt][n + u], pw[mt][i][0], pw[mt][i][1], pw[mt][i][2], pw[mt][i][3], b0, b1, acc.o[mt][n + u]);
                 }
             }
+        if (edge && __any_sync(0xffffffffu, nan_seen != 0)) {
+            // looked at again, without the tokens that no row sees: in unused slots such codes are common
+            int some_lo = INT_MAX, some_hi = 0;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    some_lo = min(some_lo, info[mt * 16 + 8 * s].lo);
+                    some_hi = max(some_hi, info[mt * 16 + 8 * s].hi);
+                }
+            some_lo = __reduce_min_sync(0xffffffffu, some_lo);
+            some_hi = __reduce_max_sync(0xffffffffu, some_hi);
+            nan_seen = 0;
+#pragma unroll 1
+            for (int i = 0; i < NS; ++i) {
+                const int k = tok0 + (i * TG + tg) * 16 + 4 * c, from = min(max(some_lo - k, 0), 4), to = min(max(some_hi - k, 0), 4);
+                const uint32_t seen = (uint32_t)((1ull << (8 * to)) - 1) & ~(uint32_t)((1ull << (8 * from)) - 1);
+#pragma unroll 1
+                for (int n = 0; n < D / 8; n += 4) {
+                    uint32_t vc[4];
+                    ldmatrix4(vc, vs + (uint32_t)((i * TG + tg) * S::kSubBytes + n * 128) + v_off);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        nan_seen |= __vcmpeq4(vc[u] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) & seen;
+                }
+            }
+        }
         if (edge && __any_sync(0xffffffffu, nan_seen != 0)) {
             const uint8_t *vb = sm + (size_t)st * S::kStageBytes + S::kTileBytes;
 #pragma unroll
