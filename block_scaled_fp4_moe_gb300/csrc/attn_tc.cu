@@ -20,7 +20,7 @@
 // and exchanges.)
 //
 // Measured: three requests' chunks of 500 tokens over 9,000, 48 query heads of 64, 147 us (563 TFLOP/s), bound by the issue of the softmax (a
-// pass for the maxima before the weights: 165; four such tiles unrolled: 180); chunks of 600 over 16,000, 40 heads of 128, 478 us (905 TFLOP/s),
+// pass for the maxima before the weights: 165; four such tiles unrolled: 180); chunks of 600 over 16,000, 40 heads of 128, 490 us (880 TFLOP/s),
 // where shared memory, read and written for codes, operands and products, is busy three quarters of the time; 16 requests of up to 48 rows
 // over 10,000 tokens 143 us, bound by a tile's way through conversion, product, softmax and product with few rows.
 //
@@ -528,6 +528,35 @@ __device__ __forceinline__ void hide(float (&x)[32], int k, int lo, int hi) {
             x[e] = -INFINITY;
 }
 
+// Where more values were NaN than the list holds: a row looks through the cache itself, at tiles first, first + step .. before
+// last that some row of its piece sees in part, and writes NaN over its results' dims d0 .. d1 - 1.  (Not inlined, and by
+// value: the softmax's loop is the faster for it.)
+template <int D>
+__device__ __noinline__ void nan_rows(const AttnArgs &a, int request, int head, int kv, int n, int row0, int rows, int first, int last, int step,
+                                      int lo, int hi, int d0, int d1, uint16_t *out, float *part, int cap) {
+    int lo0, hi0, lo1, hi1;
+    row_range(a.p, a.group, kv, n, row0, lo0, hi0);
+    row_range(a.p, a.group, kv, n, row0 + rows - 1, lo1, hi1);
+    for (int t = first; t < last; t += step) {
+        if ((t + 1) * kTile <= hi0 && t * kTile >= lo1)
+            continue;                              // seen by all: the product has them
+        for (int j = max(t * kTile, lo); j < min((t + 1) * kTile, hi); ++j) {
+            int page = __ldg(a.p.table + (size_t)request * a.p.max_blocks + (j >> a.shift));
+            if (page < 0 || page >= a.p.cache.num_blocks)
+                page = 0;
+            const int off = j & ((1 << a.shift) - 1);
+            const uint8_t *v = a.p.cache.v + ((((size_t)page * a.p.cache.kv_heads + head) << a.shift) + (off & ~15)) * D + (off & 15);
+            for (int d = d0; d < d1; ++d)
+                if ((__ldg(v + 16 * d) & 0x7F) == 0x7F) {
+                    if (out)
+                        out[d] = 0x7FFF;
+                    else
+                        __stcg(part + (size_t)(d >> 2) * cap * 4 + (d & 3), __uint_as_float(0x7FFFFFFFu));
+                }
+        }
+    }
+}
+
 template <int D>
 __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, uint8_t *sm, const Bars &b, uint32_t tmem,
                                            uint32_t *nan_count, int *s_last) {
@@ -844,6 +873,13 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
                     __stcg(dst + (size_t)(e / 4) * cap, make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]));
             }
         }
+        if (live && nan_seen > (uint32_t)kNanEntries) {
+            const int at = pc.tile0 + pc.t0;
+            nan_rows<D>(a, pc.request, pc.head, pc.kv, pc.n, pc.row0, pc.rows, at + (pair || both ? 0 : h), at + n, pair || both ? 1 : 2, lo, hi,
+                        both ? h * (D / 2) : 0, both ? (h + 1) * (D / 2) : D, w.count == 1 ? p.out + to * D : nullptr,
+                        a.part + ((size_t)w.slot * cap * D + 4 * tid), cap);
+        }
+        __syncwarp();
         if (both) {                                // the products may be made anew
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             named_barrier_sync(3, 256);

@@ -751,3 +751,19 @@ def test_single_token_strides_do_not_matter():
     attn.moe_linear_fp8(x, w, y[0], ws)
     attn.moe_linear_fp8(x.as_strided((1, 64), (7, 1)), w, y[1], ws)
     assert torch.equal(*y)
+
+
+@pytest.mark.parametrize("dim,new,group", [(64, 60, 4), (64, 9, 4), (128, 40, 8), (128, 7, 4), (64, 120, 2), (128, 60, 4), (128, 30, 4)])
+def test_attention_many_rows_many_nan_values(dim, new, group):
+    """Every value of 45 consecutive tokens among the newest is NaN: all rows that see one of them are, and no other."""
+    kv, first = 400, 400 - new // 2 - 1                   # some new tokens come before them, and see none
+    p = Problem([(new, kv)] * 5, 8, group, dim, 32, seed=49)
+    clean_out, clean_lse = p.run()
+    for b in range(5):
+        for j in range(first, min(first + 45, kv)):
+            p.cache.v[p.table[b, j // 32], :, j % 32] = 0x7F
+    out, lse = p.run()
+    assert p.status == 0 and torch.equal(lse, clean_lse)
+    sees = torch.tensor([kv - new + i >= first for i in range(new)] * 5, device="cuda")
+    assert sees.any() and not sees.all()
+    assert torch.equal(out[~sees], clean_out[~sees]) and bool(torch.isnan(out[sees].float()).all())
