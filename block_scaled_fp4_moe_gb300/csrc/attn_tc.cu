@@ -19,7 +19,7 @@
 // 15 issues the MMAs.  (Two threads to a row, 16 warps of at most 88 registers, took as long: more latency hidden, more moves
 // and exchanges.)
 //
-// Measured: three requests' chunks of 500 tokens over 9,000, 48 query heads of 64, 147 us (563 TFLOP/s), bound by the issue of the softmax (a
+// Measured: three requests' chunks of 500 tokens over 9,000, 48 query heads of 64, 148 us (558 TFLOP/s), bound by the issue of the softmax (a
 // pass for the maxima before the weights: 165; four such tiles unrolled: 180); chunks of 600 over 16,000, 40 heads of 128, 490 us (880 TFLOP/s),
 // where shared memory, read and written for codes, operands and products, is busy three quarters of the time; 16 requests of up to 48 rows
 // over 10,000 tokens 143 us, bound by a tile's way through conversion, product, softmax and product with few rows.
