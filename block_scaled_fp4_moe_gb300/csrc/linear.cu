@@ -529,15 +529,22 @@ __global__ void __launch_bounds__(256) fp8_weight_kernel(const uint16_t *__restr
 }
 
 // Token tile and form for T tokens and the tiles of N.  The split form's tile is the least
-// width that holds the tokens, up to 128.
+// width that holds the tokens, up to 128, two CTAs to an SM; the persistent form's is 192, one CTA.
 struct Form {
     bool split_form;
     int tile, split;
     static Form make(int T, int N, int KB, int sms) {
         Form f{};
         const int n_tiles = (N + 127) / 128;
-        f.split_form = (long long)n_tiles * ((T + 191) / 192) < sms;
-        f.tile = !f.split_form ? 192 : T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+        f.tile = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+        // The split form for a token tile or less (us of it and of the persistent form: one token and W 45056 x 5120 45.5 and 84.0, 64 and
+        // 131072 x 4096 98.8 and 105.3, 100 110.1 and 108.0); for more while its tiles have an SM each, or share one where the persistent
+        // form would walk twice (7168 x 5120: 200 tokens, 112 tiles, 20.4 and 25.6; 384, 168 tiles against 112, 28.0 and 26.4; 576, 280
+        // against 168, 30.3 and 42.0; 700, 336 against 224, 49.7 and 42.1).
+        const long long split_tiles = (long long)n_tiles * ((T + f.tile - 1) / f.tile), wide_tiles = (long long)n_tiles * ((T + 191) / 192);
+        f.split_form = T <= 128 || split_tiles <= sms || (wide_tiles > sms && split_tiles <= 2 * sms);
+        if (!f.split_form)
+            f.tile = 192;
         f.split = 1;
         if (f.split_form) {
             const int tiles = n_tiles * ((T + f.tile - 1) / f.tile);
@@ -552,7 +559,8 @@ struct Form {
     }
 };
 
-// quantising x in the GEMM costs a stage about as much as its copies at 8 tokens; a kernel before it about 2 us
+// x quantised in the GEMM, each cluster for itself, or by a kernel before it (7168 x 5120, one token 8.9 and 9.6 us, 8 tokens 9.6
+// and 10.9; a second pass of 8 over x costs a stage more than its copies hide)
 constexpr int kFusedTokens = 8;
 
 struct Layout {

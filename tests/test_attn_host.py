@@ -174,3 +174,20 @@ def test_reference_cache_layout_round_trip():
     assert k[1, 0, 1, 2, 5, 7] == c.k[1, 0, 21, 39] and v[2, 1, 1, 40, 9] == c.v[2, 1, 25, 40]
     back = ref.Cache.from_layout(k, v, ks, vs)
     assert np.array_equal(back.k, c.k) and np.array_equal(back.v, c.v)
+
+
+def test_binding_refuses_what_is_not_on_the_gpu(L):
+    """The compiled checks name the tensor, before any address is passed on."""
+    torch = pytest.importorskip("torch")
+    u8 = torch.zeros(1, 1, 1, 4, 16, 16, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="k: expected a CUDA tensor"):
+        attn.KVCache(u8, u8, u8, u8)
+    with pytest.raises(ValueError, match="codes: expected a CUDA tensor"):
+        attn.FP8Weight(torch.zeros(16, 16, dtype=torch.uint8), torch.zeros(1, 1, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="k: expected a tensor"):
+        attn.KVCache(None, u8, u8, u8)
+    i32 = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="ctx_lens"):
+        attn.moe_kv_build_tables(i32, i32, 16, i32, i32, i32, i32, i32, i32, i32, i32, u8)
+    with pytest.raises(ValueError, match="expected 6 arguments"):
+        attn._native().linear_fp8(u8)

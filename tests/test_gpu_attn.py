@@ -767,3 +767,12 @@ def test_attention_many_rows_many_nan_values(dim, new, group):
     sees = torch.tensor([kv - new + i >= first for i in range(new)] * 5, device="cuda")
     assert sees.any() and not sees.all()
     assert torch.equal(out[~sees], clean_out[~sees]) and bool(torch.isnan(out[sees].float()).all())
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 40000, 144), (9, 40001, 128), (100, 40000, 16), (128, 21000, 272), (130, 16500, 128), (300, 7000, 256), (400, 7000, 256),
+                                   (650, 7000, 128)])
+def test_linear_forms_by_size(T, N, K):
+    """More tiles than SMs, with one token tile and with several; tiles that share an SM; a grid that walks."""
+    xt, _, weight, y = linear_case(T, N, K, seed=50)
+    want, bound = ref.linear(f64(xt), weight.codes.cpu().numpy(), weight.scale.cpu().numpy())
+    assert (np.abs(f64(y) - want) <= bound).all()
