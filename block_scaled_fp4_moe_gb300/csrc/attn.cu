@@ -597,7 +597,7 @@ __device__ __forceinline__ void finish(const AttnArgs &a, const Piece &pc, uint8
                 } else {
                     __stcg(reinterpret_cast<float4 *>(a.part + ((size_t)slot * a.part_rows + row) * D + d), o);
                     if (d == 0)
-                        __stcg(a.part_lse + (size_t)slot * a.part_rows + row, lse2);
+                        __stcg(a.part_sum + (size_t)slot * a.part_rows + row, make_float2(lse2, 1.0f));
                 }
             }
         }
@@ -626,7 +626,7 @@ __device__ __forceinline__ void finish(const AttnArgs &a, const Piece &pc, uint8
                     for (int u = 0; u < U; ++u) {
                         const int k = k0 + u;
                         const size_t at = ((size_t)(pc.first + k) * 2 + (k == 0)) * a.part_rows + row;
-                        e[u] = k < pieces ? __ldcg(a.part_lse + at) : -INFINITY;
+                        e[u] = k < pieces ? __ldcg(a.part_sum + at).x : -INFINITY;
                         v[u] = k < pieces ? __ldcg(reinterpret_cast<const float4 *>(a.part + at * D + d)) : make_float4(0, 0, 0, 0);
                     }
                     float nm = m;
@@ -767,7 +767,7 @@ AttnLayout AttnLayout::make(int T, int B, int q_heads, int kv_heads, int head_di
     const size_t cut = part_rows(T, group, kRows), tall = rows <= kAttnTcMinRows ? 0 : part_rows(T, group, 128);
     const size_t parts = (size_t)kMaxAttnCtas * (2 * cut > 4 * tall ? 2 * cut : 4 * tall);
     L.part = take(parts * head_dim * sizeof(float));
-    L.part_lse = take(parts * sizeof(float));
+    L.part_sum = take(parts * sizeof(float2));
     L.nans = take(tall ? (size_t)kMaxAttnCtas * kAttnNanBytes : 0);
     L.total = align_up(o, 256);
     return L;
@@ -781,7 +781,7 @@ cudaError_t launch_kv_attention(const AttnProblem &p, void *ws, int sms, cudaStr
         ++shift;
     AttnArgs a{p, group, shift, kRows, part_rows(p.T, group, kRows), sms < kMaxAttnCtas ? sms : kMaxAttnCtas, max_row_tiles(p.T, p.B, group, kRows),
                p.scale * 1.44269504088896340736f, ws_at<Plan>(ws, L.plan), ws_at<RowTile>(ws, L.recs),
-               ws_at<uint32_t>(ws, kHeaderBytes), ws_at<float>(ws, L.part), ws_at<float>(ws, L.part_lse),
+               ws_at<uint32_t>(ws, kHeaderBytes), ws_at<float>(ws, L.part), ws_at<float2>(ws, L.part_sum),
                ws_at<uint8_t>(ws, L.nans), ws_at<uint32_t>(ws, 0)};
     // The tensor-memory form where requests have more than 24 rows on average (us of it and of this one: 16 requests of
     // 1..4 tokens x 12 heads of a group 143 and 175, 32 of 10 x 4 rows 157 and 191; of 1..3 x 8 154 and 105; requests of 32 rows

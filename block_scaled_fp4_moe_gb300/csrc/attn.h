@@ -111,7 +111,7 @@ struct AttnProblem {
 };
 // Workspace regions of the attention.
 struct AttnLayout {
-    size_t plan, recs, part, part_lse, nans, total;
+    size_t plan, recs, part, part_sum, nans, total;
     static AttnLayout make(int T, int B, int q_heads, int kv_heads, int head_dim);
 };
 // The tensor-memory form (attn_tc.cu) for requests of more than this many rows on average, its units' rows, and the

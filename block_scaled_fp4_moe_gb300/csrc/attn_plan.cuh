@@ -38,7 +38,8 @@ struct AttnArgs {
     Plan *plan;
     RowTile *recs;
     uint32_t *tickets;
-    float *part, *part_lse;              // parts of cut units
+    float *part;                         // parts of cut units: their rows,
+    float2 *part_sum;                    // and their m and l
     void *nans;                          // lists of NaN values (attn_tc.cu)
     uint32_t *hdr;
 };

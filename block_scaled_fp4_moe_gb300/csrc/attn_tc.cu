@@ -31,9 +31,15 @@
 //
 // The running maxima of a row are references that move only where scores have outgrown them (16 weights sum to more than
 // 2^12: f16 holds up to 2^16, and its rounding is relative).  So a score is read once: 32 of a row at a time become weights,
-// whose sums say whether they fit.  Where they do not, the references move to the maxima (of the tile, which is then made
-// again, or of the 32 where the weights lie over the scores), the half waits for its last product and rescales O, and the
-// tile's weights so far, in TMEM.  Only a unit's first tile is read for its maxima first.
+// whose sums say whether they fit.  Where they do not, the references move to the maxima (of the tile, or of the 32 where the
+// weights lie over the scores), the half waits for its last product and rescales O, and the tile's weights so far, in TMEM; then
+// the weights are made, and not looked at again.  Only a unit's first tile is read for its maxima first.
+//
+// The reference of the weights is kept relative to that of l (rel = M - m) and moves by whole powers of two: weights stored already
+// lose nothing to it, and it has all its bits however large the scores are.  A weight's power is fma(y, fi, -m), the
+// product exact; m, rounded, may lie under it by half of its last place.  Past kFar that would matter (half a place of 2^28 is a
+// factor of 2^16).  There, and wherever the references have just moved, the product is rounded as m was before m is
+// taken from it, so that no power is above zero, and every tile is read for its maxima first.
 #include "attn_plan.cuh"
 
 namespace moe {
@@ -44,6 +50,7 @@ constexpr int kTcThreads = (kSoftWarps + kConvWarps + 2) * 32;
 constexpr int kNanEntries = 2048;
 // What 16 weights may sum to before the references move; 2^-32: with that factor, what 16 terms of l may.
 constexpr float kMostWeight = 4096.0f, kLeastSum = 0x1p-32f;
+constexpr float kFar = 0x1p20f;        // half of its last place: 2^-4
 
 // A value's NaN codes in a tile that some rows see in part: the unit, the position, the dims.
 struct NanEntry {
@@ -557,6 +564,147 @@ __device__ __noinline__ void nan_rows(const AttnArgs &a, int request, int head, 
     }
 }
 
+// A row's references, m and M - m, and its l with respect to m.
+struct Refs {
+    float m, rel, l;
+};
+
+// A tile as one row finds it.
+struct TileRow {
+    uint32_t lanes;          // the warp's rows in tensor memory
+    int h;                   // their half
+    const float *meta;       // the sub-blocks' exponents
+    float f;                 // factor of the row's products
+    int lo, hi, tok0;        // positions that it sees, the tile's first
+    int edge;                // some row of the warp does not see all of it
+    uint64_t *product;       // barrier of the half's last product, if there was one, and its parity
+    uint32_t parity;
+    uint32_t *hdr;
+};
+
+__device__ __forceinline__ float seen(float v) { return v == -INFINITY ? 0.0f : v; }
+
+__device__ __forceinline__ float factor(float f, const float *meta, int sub) { return fmaxf(f * meta[sub], 1.2e-38f); }
+
+// The tile's scores 32 c .. 32 c + 31.
+__device__ __forceinline__ void row_scores(float (&x)[32], const TileRow &t, int c) {
+    tmem_ld32(x, t.lanes + 128 * t.h + 32 * c);
+    if (t.edge)
+        hide(x, t.tok0 + 32 * c, t.lo, t.hi);
+}
+
+// 32 scores (LESS: less their reference already) to weights; their terms of l to sum; whether they outgrew the references.
+template <bool LESS>
+__device__ __forceinline__ bool weigh(const float (&x)[32], const float *meta, float f, int c, const Refs &refs, uint32_t (&w)[16], float &sum) {
+    const float mz = LESS ? 0.0f : seen(refs.m), below = seen(refs.rel);
+    const uint64_t minus_m = pack2(-mz, -mz);
+    bool grew = false;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const float *y = x + 16 * u;
+        const float fi = LESS ? 1.0f : factor(f, meta, 2 * c + u), bb = meta[kSubs + 2 * c + u];
+        const float r = ex2(fminf(bb - below, 126.0f));
+        const uint64_t fi2 = pack2(fi, fi), r2 = pack2(r, r);
+        uint64_t s2[2];
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+            const float2 t2 = unpack2(fma2(pack2(y[e], y[e + 1]), fi2, minus_m));
+            const uint64_t p2 = pack2(ex2(t2.x), ex2(t2.y));
+            s2[e >> 1 & 1] = e < 4 ? p2 : add2(s2[e >> 1 & 1], p2);
+            const float2 w2 = unpack2(mul2(p2, r2));
+            const __half2 h2 = __floats2half2_rn(w2.x, w2.y);
+            w[8 * u + e / 2] = *reinterpret_cast<const uint32_t *>(&h2);
+        }
+        const float2 t = unpack2(add2(s2[0], s2[1]));
+        const float s16 = t.x + t.y;
+        sum += s16;
+        grew |= fmaxf(s16 * r, s16 * kLeastSum) > kMostWeight;
+    }
+    return grew;
+}
+
+// The weights of a tile's chunks (of 32 scores) from c on, the references first moved to the maxima where those lie above, of the whole tile
+// or, behind weights that are stored already, of a chunk where it outgrows them.  With the references moves what was made with
+// them: l, the half's sums, the stored weights.
+template <int D>
+__device__ __forceinline__ Refs move_and_weigh(Refs r, const TileRow &t, int c) {
+    using S = TcSmem<D>;
+    int top = c;                                   // the references are no less than the scores of the chunks before
+    bool move = true;
+#pragma unroll 1
+    while (c < 4) {
+        if (move) {
+            top = c == 0 ? 4 : c + 1;
+            float nm = -INFINITY, nrel = -INFINITY;        // largest x, and x + b less that
+#pragma unroll 1
+            for (int k = c; k < top; ++k) {
+                float x[32];
+                row_scores(x, t, k);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const float *y = x + 16 * u;
+                    float v0 = max3(y[0], y[1], y[2]), v1 = max3(y[3], y[4], y[5]), v2 = max3(y[6], y[7], y[8]), v3 = max3(y[9], y[10], y[11]);
+                    v0 = max3(v0, y[12], y[13]);
+                    v1 = max3(v1, y[14], y[15]);
+                    const float v = fmaxf(max3(v0, v1, v2), v3) * factor(t.f, t.meta, 2 * k + u), to = fmaxf(nm, v), z = seen(to);
+                    nrel = fmaxf(nrel + (nm - z), (v - z) + t.meta[kSubs + 2 * k + u]);
+                    nm = to;
+                }
+            }
+            const float to = fmaxf(nm, r.m), z = seen(to);
+            const float was = r.rel + (r.m - z), want = fmaxf(nrel + (nm - z), -INFINITY);     // M from the new m, as it is and at least
+            // nothing is left of sums 150 binades down: their reference may be far off, and is not added to
+            const bool anew = !(want - was < 150.0f);
+            const float up = anew ? 0.0f : fmaxf(ceilf(want - was), 0.0f), by = anew ? 0.0f : ex2(-up);
+            r.l *= ex2(r.m - z);
+            r.m = to;
+            r.rel = anew ? want : was + up;
+            if (t.product) {
+                if (!__all_sync(0xffffffffu, wait_phase(t.product, t.parity)) && (threadIdx.x & 31) == 0)
+                    record_status(t.hdr, MOE_ERR_DEVICE_TIMEOUT);
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll 1
+                for (int k = 0; k < D / 32; ++k) {
+                    const uint32_t at = t.lanes + 256 + D * t.h + 32 * k;
+                    float x[32];
+                    tmem_ld32(x, at);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        x[e] *= by;
+                    tmem_st32(at, x);
+                }
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            const __half2 by2 = __float2half2_rn(by);
+#pragma unroll 1
+            for (int k = 0; k < c; ++k) {
+                uint32_t w[16];
+                tmem_ld16(reinterpret_cast<float(&)[16]>(w), t.lanes + S::w_col(t.h, 32 * k));
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(w + e), by2);
+                    w[e] = *reinterpret_cast<const uint32_t *>(&v);
+                }
+                tmem_st16(t.lanes + S::w_col(t.h, 32 * k), w);
+            }
+        }
+        float x[32], sum = 0.0f;
+        uint32_t w[16];
+        row_scores(x, t, c);                       // no weights lie over these yet
+        const float z = seen(r.m);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            x[e] = __fsub_rn(__fmul_rn(x[e], factor(t.f, t.meta, 2 * c + e / 16)), z);
+        move = __any_sync(0xffffffffu, weigh<true>(x, t.meta, t.f, c, r, w, sum)) && c >= top;
+        if (move)
+            continue;
+        r.l += sum;
+        tmem_st16(t.lanes + S::w_col(t.h, 32 * c), w);
+        ++c;
+    }
+    return r;
+}
+
 template <int D>
 __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, uint8_t *sm, const Bars &b, uint32_t tmem,
                                            uint32_t *nan_count, int *s_last) {
@@ -624,7 +772,7 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
             row_range(p, a.group, pc.kv, pc.n, row, lo, hi);
         const int min_hi = __reduce_min_sync(0xffffffffu, hi), max_lo = __reduce_max_sync(0xffffffffu, lo);
 
-        float m = -INFINITY, big = -INFINITY, l = 0.0f;     // references, and l with respect to m
+        Refs refs{-INFINITY, -INFINITY, 0.0f};
         for (int i = 0; i < mine; ++i) {
             const int t = pair ? i : 2 * i + h;
             const int tok0 = (pc.tile0 + pc.t0 + t) * kTile;
@@ -633,141 +781,51 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
             if (!idle) {
                 const bool edge = tok0 + kTile > min_hi || tok0 < max_lo;
                 const float *meta = reinterpret_cast<const float *>(sm + S::kOffMeta) + ((tile + t) % S::kMetaTiles) * 2 * kSubs;
-                // the largest score of 16, in x's units
-                auto top_of = [&](const float *y, float fi) {
-                    float v0 = max3(y[0], y[1], y[2]), v1 = max3(y[3], y[4], y[5]), v2 = max3(y[6], y[7], y[8]), v3 = max3(y[9], y[10], y[11]);
-                    v0 = max3(v0, y[12], y[13]);
-                    v1 = max3(v1, y[14], y[15]);
-                    return fmaxf(max3(v0, v1, v2), v3) * fi;
-                };
-                auto factor = [&](int k) { return fmaxf(f * meta[k], 1.2e-38f); };
-                // moves the references to these maxima (of x, and of x + b) where they lie above; the tile's first `chunks` of
-                // 32 weights are stored already
-                auto move = [&](float nm, float nb, int chunks) {
-                    if (nm > m) {
-                        l *= m == -INFINITY ? 0.0f : ex2(m - nm);
-                        m = nm;
-                    }
-                    const float to = fmaxf(nb, big), r = big == -INFINITY ? 0.0f : ex2(big - to);
-                    big = to;
-                    if (i > 0) {                   // the half's last product is done
-                        wait(b.o_done + h, (on - 1) & 1);
-#pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            float x[32];
-                            tmem_ld32(x, o_at + 32 * c);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                x[e] *= r;
-                            tmem_st32(o_at + 32 * c, x);
-                        }
-                    }
-                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                    const __half2 r2 = __float2half2_rn(r);
-#pragma unroll 1
-                    for (int c = 0; c < chunks; ++c) {
-                        uint32_t w[16];
-                        tmem_ld16(reinterpret_cast<float(&)[16]>(w), lanes + S::w_col(h, 32 * c));
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(w + e), r2);
-                            w[e] = *reinterpret_cast<const uint32_t *>(&v);
-                        }
-                        tmem_st16(lanes + S::w_col(h, 32 * c), w);
-                    }
-                };
-                auto chunk_maxima = [&](const float *x, int c, float &nm, float &nb) {
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const float v = top_of(x + 16 * u, factor(2 * c + u));
-                        nm = fmaxf(nm, v);
-                        nb = fmaxf(nb, v + meta[kSubs + 2 * c + u]);
-                    }
-                };
+                const TileRow tr{lanes, h, meta, f, lo, hi, tok0, edge, i > 0 && !dead ? b.o_done + h : nullptr, (on - 1) & 1, a.hdr};
                 auto scores = [&](float (&x)[32], int c) {
                     tmem_ld32(x, s_at + 32 * c);
                     if (edge)
                         hide(x, tok0 + 32 * c, lo, hi);
                 };
-                auto to_maxima = [&]() {           // of the tile
-                    float nm = -INFINITY, nb = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        float x[32];
-                        scores(x, c);
-                        chunk_maxima(x, c, nm, nb);
-                    }
-                    move(nm, nb, 0);
-                };
-                // 32 scores to weights; their terms of l to sum; whether they outgrew the references
-                auto weigh = [&](const float (&x)[32], int c, uint32_t (&w)[16], float &sum) {
-                    const float mz = m == -INFINITY ? 0.0f : m, bz = big == -INFINITY ? 0.0f : big;
-                    const uint64_t minus_m = pack2(-mz, -mz);
-                    bool grew = false;
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const float *y = x + 16 * u;
-                        const float fi = factor(2 * c + u), bb = meta[kSubs + 2 * c + u];
-                        const float r = ex2(fminf(bb + (mz - bz), 126.0f));
-                        const uint64_t fi2 = pack2(fi, fi), r2 = pack2(r, r);
-                        uint64_t s2[2];
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const float2 t2 = unpack2(fma2(pack2(y[e], y[e + 1]), fi2, minus_m));
-                            const uint64_t p2 = pack2(ex2(t2.x), ex2(t2.y));
-                            s2[e >> 1 & 1] = e < 4 ? p2 : add2(s2[e >> 1 & 1], p2);
-                            const float2 w2 = unpack2(mul2(p2, r2));
-                            const __half2 h2 = __floats2half2_rn(w2.x, w2.y);
-                            w[8 * u + e / 2] = *reinterpret_cast<const uint32_t *>(&h2);
-                        }
-                        const float2 t = unpack2(add2(s2[0], s2[1]));
-                        const float s16 = t.x + t.y;
-                        sum += s16;
-                        grew |= fmaxf(s16 * r, s16 * kLeastSum) > kMostWeight;
-                    }
-                    return grew;
-                };
                 // where weights have columns of their own these scores came before the last product: it must have read its weights
                 if (S::kOwnW && i > 0)
                     wait(b.o_done + h, (on - 1) & 1);
-                if (__any_sync(0xffffffffu, big == -INFINITY))           // no references yet
-                    to_maxima();
                 // The loops are rolled: unrolled, their instructions cost more to fetch than the steps they save (9 to 12 % of the kernel).
-                if (S::kOwnW) {
+                int made = 4;                      // chunks of 32 with their weights
+                if (__any_sync(0xffffffffu, !(fabsf(refs.m) <= kFar))) {            // no reference yet, or a far one
+                    made = 0;
+                } else if (S::kOwnW) {
                     // the scores outlive the weights: one vote a tile (four take 159 us for 147)
-                    for (;;) {
-                        float sum = 0.0f;
-                        bool grew = false;
+                    float sum = 0.0f;
+                    bool grew = false;
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            float x[32];
-                            uint32_t w[16];
-                            scores(x, c);
-                            grew |= weigh(x, c, w, sum);
-                            tmem_st16(lanes + S::w_col(h, 32 * c), w);
-                        }
-                        if (!__any_sync(0xffffffffu, grew)) {
-                            l += sum;
-                            break;
-                        }
-                        to_maxima();
+                    for (int c = 0; c < 4; ++c) {
+                        float x[32];
+                        uint32_t w[16];
+                        scores(x, c);
+                        grew |= weigh<false>(x, meta, f, c, refs, w, sum);
+                        tmem_st16(lanes + S::w_col(h, 32 * c), w);
                     }
+                    if (__any_sync(0xffffffffu, grew))
+                        made = 0;
+                    else
+                        refs.l += sum;
                 } else {
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         float x[32], sum = 0.0f;
                         uint32_t w[16];
                         scores(x, c);
-                        while (__any_sync(0xffffffffu, weigh(x, c, w, sum))) {
-                            float nm = -INFINITY, nb = -INFINITY;
-                            chunk_maxima(x, c, nm, nb);
-                            move(nm, nb, c);
-                            sum = 0.0f;
+                        if (__any_sync(0xffffffffu, weigh<false>(x, meta, f, c, refs, w, sum))) {
+                            made = c;
+                            break;
                         }
-                        l += sum;
+                        refs.l += sum;
                         tmem_st16(lanes + S::w_col(h, 32 * c), w);
                     }
                 }
+                if (made < 4)
+                    refs = move_and_weigh<D>(refs, tr, made);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -780,25 +838,25 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
             wait(b.o_done + h, (on - 1) & 1);
         tile += n;
 
-        // ---- the rows' result: l is NaN where a score was, and then so is the row
-        const float mz = m == -INFINITY ? 0.0f : m, bz = big == -INFINITY ? 0.0f : big;
-        float scale = l == 0.0f ? 0.0f : exp2f(bz - mz) / l, lse2 = l == 0.0f ? -INFINITY : mz + log2f(l);
+        // ---- the rows' result: l is NaN where a score was (or was infinite), and then so is the row
+        float m = refs.m, l = refs.l, scale = l == 0.0f ? 0.0f : exp2f(refs.rel) / l;
         const int ctas = pc.last - pc.first + 1;
         // Halves that share the rows of an uncut unit join here: through the space of their queries, which nothing reads
-        // any more, each learns the other's sum, and makes half of the dims from both products.
+        // any more, each learns the other's reference and sum, and makes half of the dims from both products.
         const bool both = !pair && ctas == 1 && n > 1;
         float other_scale = 0.0f;
         if (both) {
-            *reinterpret_cast<float2 *>(q_at) = make_float2(scale, lse2);
+            *reinterpret_cast<float4 *>(q_at) = make_float4(scale, m, l, 0.0f);
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             named_barrier_sync(3, 256);
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const float2 other = *reinterpret_cast<const float2 *>(sm + (size_t)(1 - h) * S::kQBytes + tid * 128);
-            const float rm = fmaxf(lse2, other.y), z = rm == -INFINITY ? 0.0f : rm;
-            const float w0 = ex2(lse2 - z), w1 = ex2(other.y - z), rl = w0 + w1, wt = rl == 0.0f ? 0.0f : 1.0f / rl;
+            const float4 other = *reinterpret_cast<const float4 *>(sm + (size_t)(1 - h) * S::kQBytes + tid * 128);
+            const float rm = fmaxf(m, other.y), z = rm == -INFINITY ? 0.0f : rm;
+            const float w0 = l * ex2(m - z), w1 = other.z * ex2(other.y - z), wt = w0 + w1 == 0.0f ? 0.0f : 1.0f / (w0 + w1);
             scale *= w0 * wt;
             other_scale = other.x * w1 * wt;
-            lse2 = rl == 0.0f ? -INFINITY : rm + log2f(rl);
+            m = rm;
+            l = w0 + w1;
         }
         // workers of a cut unit: its CTAs, twice those with two tiles or more where the halves share rows
         Workers w{1, 0, 0};
@@ -809,6 +867,8 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
             // tiles of the unit in the first and the last of its CTAs; those between have pl.per of them
             w.count = pair || ctas == 1 ? ctas : min(2, pc.first_tiles) + min(2, pc.last_tiles) + (int)min(2ll, pl.per) * (ctas - 2);
         }
+        if (w.count == 1 && l == 0.0f && lo < hi)  // it sees positions, and every score overflowed
+            scale = other_scale = l = __uint_as_float(0x7FFFFFFFu);
         const int rows_here = pair ? min(128, pc.rows - 128 * h) : pc.rows;
         const int cap = min(128, (int)min((long long)p.T * a.group, 128ll));       // rows of a part in the workspace
         // entries so far, once all of them are written (the converters may be in the next unit already)
@@ -886,9 +946,9 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
         }
         if (live && w.count == 1) {
             if (p.lse && (!both || h == 0))
-                p.lse[to] = lse2 * 0.69314718055994530942f;
+                p.lse[to] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
         } else if (live) {
-            __stcg(a.part_lse + (size_t)w.slot * cap + tid, lse2);
+            __stcg(a.part_sum + (size_t)w.slot * cap + tid, make_float2(m, l));
         }
         if (w.count > 1) {
             __threadfence();
@@ -916,37 +976,43 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
                     const int r = i % rows_here, d = i / rows_here * 4;
                     float rm = -INFINITY, rl = 0.0f;
                     for (int k0 = 0; k0 < parts; k0 += 2 * U) {
-                        float e[2 * U];
+                        float2 e[2 * U];           // m, l
 #pragma unroll
                         for (int u = 0; u < 2 * U; ++u) {
                             const int slot = slot_of(k0 + u);
-                            e[u] = slot >= 0 ? __ldcg(a.part_lse + (size_t)slot * cap + r) : -INFINITY;
+                            e[u] = slot >= 0 ? __ldcg(a.part_sum + (size_t)slot * cap + r) : make_float2(-INFINITY, 0.0f);
                         }
                         float nm = rm;
 #pragma unroll
                         for (int u = 0; u < 2 * U; ++u)
-                            nm = fmaxf(nm, e[u]);
+                            nm = fmaxf(nm, e[u].x);
                         const float z = nm == -INFINITY ? 0.0f : nm;
                         rl *= ex2(rm - z);
                         rm = nm;
 #pragma unroll
                         for (int u = 0; u < 2 * U; ++u)
-                            rl += ex2(e[u] - z);
+                            rl += e[u].y * ex2(e[u].x - z);
+                    }
+                    const int grow = pc.row0 + (pair ? 128 * h : 0) + r;
+                    if (rl == 0.0f) {              // it sees nothing, or every score overflowed
+                        int rlo, rhi;
+                        row_range(p, a.group, pc.kv, pc.n, grow, rlo, rhi);
+                        if (rlo < rhi)
+                            rl = __uint_as_float(0x7FFFFFFFu);
                     }
                     const float z = rm == -INFINITY ? 0.0f : rm, wt = rl == 0.0f ? 0.0f : 1.0f / rl;
-                    const int grow = pc.row0 + (pair ? 128 * h : 0) + r;
                     const size_t at = (size_t)(pc.q0 + grow / a.group) * p.q_heads + pc.head * a.group + grow % a.group;
                     float o[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
                         o[e] = 0.0f;
                     for (int k0 = 0; k0 < parts; k0 += U) {
-                        float e[U];
+                        float2 e[U];
                         float4 v[U][4];
 #pragma unroll
                         for (int u = 0; u < U; ++u) {
                             const int slot = slot_of(k0 + u);
-                            e[u] = slot >= 0 ? __ldcg(a.part_lse + (size_t)slot * cap + r) : -INFINITY;
+                            e[u] = slot >= 0 ? __ldcg(a.part_sum + (size_t)slot * cap + r) : make_float2(-INFINITY, 0.0f);
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
                                 v[u][q] = slot >= 0 ? __ldcg(reinterpret_cast<const float4 *>(a.part + (size_t)slot * cap * D) + (size_t)(d + q) * cap + r)
@@ -954,7 +1020,7 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
                         }
 #pragma unroll
                         for (int u = 0; u < U; ++u) {
-                            const float w = ex2(e[u] - z);
+                            const float w = e[u].y * ex2(e[u].x - z) * wt;
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
                                 o[4 * q] += v[u][q].x * w;
@@ -968,8 +1034,8 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         uint32_t x0, x1;
-                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x0) : "f"(o[4 * q + 1] * wt), "f"(o[4 * q] * wt));
-                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x1) : "f"(o[4 * q + 3] * wt), "f"(o[4 * q + 2] * wt));
+                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x0) : "f"(o[4 * q + 1]), "f"(o[4 * q]));
+                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x1) : "f"(o[4 * q + 3]), "f"(o[4 * q + 2]));
                         dst[q] = make_uint2(x0, x1);
                     }
                     if (d == 0 && p.lse)
