@@ -14,6 +14,9 @@
 // of itself, or 2^-25 of the row's largest) is relative to what the row's
 // largest contribution can be, however far the blocks' exponents lie apart.
 // l is summed from the unrounded fp32 p with its own maximum m.
+// The power of p is one FMA, x's product exact; m, rounded, may lie under it by half of its last place.  Where a warp's maxima pass
+// kFar (half a place of 2^28 is a factor of 2^16) a loop of its own takes over, in which the products are rounded first, as m was, so that
+// no power is above zero, and M is kept as M - m, which has all its bits however large the scores are.
 //
 // Work.  A unit is (request, up to 64 rows, key/value head), a row being a
 // (token, query head of the group) pair, so that a key is read once for the
@@ -279,24 +282,37 @@ __device__ __forceinline__ void load_queries(const AttnArgs &a, const Plan &pl, 
     }
 }
 
+// Rows g and g + 8 times r0 and r1.
+template <int N>
+__device__ __forceinline__ void scale_rows(float (&o)[N][4], float r0, float r1) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        o[n][0] *= r0;
+        o[n][1] *= r0;
+        o[n][2] *= r1;
+        o[n][3] *= r1;
+    }
+}
+
 // The state of a warp: MT x 16 rows, rows g and g + 8 of each for thread (g, c).
 template <int D, int MT>
 struct Acc {
     float o[MT][D / 8][4];
-    float m[MT][2], big[MT][2], l[MT][2];       // m_i, M_i, l_i (l: this thread's columns)
+    float m[MT][2], big[MT][2], l[MT][2];       // m_i, M_i (far, and when all tiles are done, M_i - m_i), l_i (l: this thread's columns)
 };
 
 // One piece's tiles: RG groups of MT x 16 rows; the warps of a row group form SG sets that take tiles in turn, those of
 // a set sharing a tile's sub-blocks.  (SG = 2 where all warps have the same rows: a warp's chain of products, maxima and powers
 // is as long for 32 tokens as for 16.  One set: 64 requests of 31,000 tokens and 8 rows take 694 us for 600, 32 of 8,000 tokens
 // and 24 rows 120 for 105.)
-template <int D, int MT, int RG, int SG>
-__device__ __forceinline__ void attend(const Piece &pc, uint8_t *sm, int qbuf, uint64_t *full, uint64_t *empty, uint32_t *hdr,
-                                       long long &it, bool &dead, Acc<D, MT> &acc) {
+// Returns the tile after the last one: not FAR stops at the tile where some row's maximum passes kFar, with nothing of it done.
+template <int D, int MT, int RG, int SG, bool FAR>
+__device__ __forceinline__ int attend_tiles(const Piece &pc, uint8_t *sm, int qbuf, uint64_t *full, uint64_t *empty, uint32_t *hdr,
+                                            long long it, int t, bool &dead, Acc<D, MT> &acc) {
     using S = Smem<D>;
     constexpr int TG = kConsumers / RG / SG, NS = kSubs / TG;    // warps of a set, sub-blocks of a warp in a tile
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int rg = warp % RG, tg = warp / RG % TG, sg = warp / RG / TG;
+    const int rg = warp % RG, tg = warp / RG % TG;
     const uint4 *q = reinterpret_cast<const uint4 *>(sm + S::kQ + (size_t)qbuf * S::kQBytes + (size_t)rg * MT * 32 * D) + lane;
     const RowInfo *info = reinterpret_cast<const RowInfo *>(sm + S::kInfo) + qbuf * kRows + rg * MT * 16 + g;
     float f[MT][2];
@@ -318,7 +334,7 @@ __device__ __forceinline__ void attend(const Piece &pc, uint8_t *sm, int qbuf, u
     const int mi = lane >> 3, ri = lane & 7;
     const uint32_t k_off = (uint32_t)((mi >> 1) * 256 + (4 * (ri >> 1) + (ri & 1) + 2 * (mi & 1)) * 16), v_off = (uint32_t)(lane * 16);
 
-    for (int t = pc.t0 + sg; t < pc.t1; t += SG) {
+    for (; t < pc.t1; t += SG) {
         const uint32_t at = (uint32_t)(it + (t - pc.t0)), st = at % S::kStages;
         if (!dead) {
             dead = !__all_sync(0xffffffffu, wait_phase(full + st, (at / S::kStages) & 1));
@@ -361,77 +377,129 @@ __device__ __forceinline__ void attend(const Piece &pc, uint8_t *sm, int qbuf, u
                     }
             }
         }
+        // maxima: m over x, M over x + b (products times fi are x; fi > 0, so that -infinity stays)
+        auto factor = [&](int mt, int s, int i) { return fmaxf(f[mt][s] * ex[i * TG + tg], 1.2e-38f); };
+        auto hide = [&](int mt) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int lo = info[mt * 16 + 8 * s].lo, hi = info[mt * 16 + 8 * s].hi;
+#pragma unroll
+                for (int i = 0; i < NS; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int k = tok0 + (i * TG + tg) * 16 + 4 * c + 2 * h + e;
+                            if (k < lo || k >= hi)
+                                x[mt][i][h][2 * s + e] = -INFINITY;
+                        }
+            }
+        };
+        float mz[MT][2], up[MT][2];                           // m to subtract (0 where nothing is seen yet), m - M
+        if constexpr (!FAR) {
+            float nm[MT][2], nb[MT][2];
+            bool grew = false, far = false;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                if (edge)
+                    hide(mt);
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    nm[mt][s] = acc.m[mt][s];
+                    nb[mt][s] = acc.big[mt][s];
+#pragma unroll
+                    for (int i = 0; i < NS; ++i) {
+                        const float v = factor(mt, s, i) * fmaxf(fmaxf(x[mt][i][0][2 * s], x[mt][i][0][2 * s + 1]),
+                                                                 fmaxf(x[mt][i][1][2 * s], x[mt][i][1][2 * s + 1]));
+                        nm[mt][s] = fmaxf(nm[mt][s], v);
+                        nb[mt][s] = fmaxf(nb[mt][s], v + ex[kSubs + i * TG + tg]);
+                    }
+                }
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    nm[mt][s] = fmaxf(nm[mt][s], __shfl_xor_sync(0xffffffffu, nm[mt][s], 1));
+                    nb[mt][s] = fmaxf(nb[mt][s], __shfl_xor_sync(0xffffffffu, nb[mt][s], 1));
+                    nm[mt][s] = fmaxf(nm[mt][s], __shfl_xor_sync(0xffffffffu, nm[mt][s], 2));
+                    nb[mt][s] = fmaxf(nb[mt][s], __shfl_xor_sync(0xffffffffu, nb[mt][s], 2));
+                    mz[mt][s] = seen(nm[mt][s]);
+                    grew |= nb[mt][s] > acc.big[mt][s];
+                    far |= fabsf(mz[mt][s]) > kFar;
+                }
+            }
+            if (__any_sync(0xffffffffu, far))
+                break;
+            if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    scale_rows(acc.o[mt], ex2(acc.big[mt][0] - seen(nb[mt][0])), ex2(acc.big[mt][1] - seen(nb[mt][1])));
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    acc.l[mt][s] *= ex2(acc.m[mt][s] - mz[mt][s]);
+                    acc.m[mt][s] = nm[mt][s];
+                    acc.big[mt][s] = nb[mt][s];
+                    up[mt][s] = mz[mt][s] - seen(nb[mt][s]);
+                }
+        } else {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                if (edge)
+                    hide(mt);
+                float r[2];
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    float v[NS], nm = acc.m[mt][s];
+#pragma unroll
+                    for (int i = 0; i < NS; ++i) {
+                        v[i] = -INFINITY;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float &y = x[mt][i][e >> 1][2 * s + (e & 1)];
+                            y = __fmul_rn(y, factor(mt, s, i));
+                            v[i] = fmaxf(v[i], y);
+                        }
+                        nm = fmaxf(nm, v[i]);
+                    }
+                    nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, 1));
+                    nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, 2));
+                    const float z = seen(nm), was = acc.big[mt][s] + (acc.m[mt][s] - z);       // M from the new m
+                    float nb = was;
+#pragma unroll
+                    for (int i = 0; i < NS; ++i) {
+                        nb = fmaxf(nb, (v[i] - z) + ex[kSubs + i * TG + tg]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float &y = x[mt][i][e >> 1][2 * s + (e & 1)];
+                            y = __fsub_rn(y, z);
+                        }
+                    }
+                    nb = fmaxf(nb, __shfl_xor_sync(0xffffffffu, nb, 1));
+                    nb = fmaxf(nb, __shfl_xor_sync(0xffffffffu, nb, 2));
+                    r[s] = was == -INFINITY ? 0.0f : ex2(was - nb);
+                    acc.l[mt][s] *= ex2(acc.m[mt][s] - z);
+                    acc.m[mt][s] = nm;
+                    acc.big[mt][s] = nb;
+                    mz[mt][s] = 0.0f;
+                    up[mt][s] = -seen(nb);
+                }
+                scale_rows(acc.o[mt], r[0], r[1]);
+            }
+        }
         uint32_t pw[MT][NS][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            if (edge) {
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const int lo = info[mt * 16 + 8 * s].lo, hi = info[mt * 16 + 8 * s].hi;
-#pragma unroll
-                    for (int i = 0; i < NS; ++i)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int k = tok0 + (i * TG + tg) * 16 + 4 * c + 2 * h + e;
-                                if (k < lo || k >= hi)
-                                    x[mt][i][h][2 * s + e] = -INFINITY;
-                            }
-                }
-            }
-            // maxima: m over x, M over x + b (products times fi are x; fi > 0, so that -infinity stays)
-            float fi[NS][2], nm[2] = {acc.m[mt][0], acc.m[mt][1]}, nb[2] = {acc.big[mt][0], acc.big[mt][1]};
-#pragma unroll
-            for (int i = 0; i < NS; ++i) {
-                const float kf = ex[i * TG + tg], b = ex[kSubs + i * TG + tg];
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    fi[i][s] = fmaxf(f[mt][s] * kf, 1.2e-38f);
-                    const float v = fi[i][s] * fmaxf(fmaxf(x[mt][i][0][2 * s], x[mt][i][0][2 * s + 1]),
-                                                     fmaxf(x[mt][i][1][2 * s], x[mt][i][1][2 * s + 1]));
-                    nm[s] = fmaxf(nm[s], v);
-                    nb[s] = fmaxf(nb[s], v + b);
-                }
-            }
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                nm[s] = fmaxf(nm[s], __shfl_xor_sync(0xffffffffu, nm[s], 1));
-                nb[s] = fmaxf(nb[s], __shfl_xor_sync(0xffffffffu, nb[s], 1));
-                nm[s] = fmaxf(nm[s], __shfl_xor_sync(0xffffffffu, nm[s], 2));
-                nb[s] = fmaxf(nb[s], __shfl_xor_sync(0xffffffffu, nb[s], 2));
-            }
-            float mz[2], bz[2];                               // maxima to subtract (0 where nothing is seen yet)
-            const bool grew = nb[0] > acc.big[mt][0] || nb[1] > acc.big[mt][1];
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                mz[s] = nm[s] == -INFINITY ? 0.0f : nm[s];
-                bz[s] = nb[s] == -INFINITY ? 0.0f : nb[s];
-                acc.l[mt][s] *= ex2(acc.m[mt][s] - mz[s]);
-                acc.m[mt][s] = nm[s];
-            }
-            if (__any_sync(0xffffffffu, grew)) {
-                const float r0 = ex2(acc.big[mt][0] - bz[0]), r1 = ex2(acc.big[mt][1] - bz[1]);
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n) {
-                    acc.o[mt][n][0] *= r0;
-                    acc.o[mt][n][1] *= r0;
-                    acc.o[mt][n][2] *= r1;
-                    acc.o[mt][n][3] *= r1;
-                }
-            }
-            acc.big[mt][0] = nb[0];
-            acc.big[mt][1] = nb[1];
             // weights: p 2^(b + m - M).  The power is at most 2^126: above it (M - m far below b) p is zero.
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
                 const float b = ex[kSubs + i * TG + tg];
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    const float r = ex2(fminf(b + (mz[s] - bz[s]), 126.0f));
+                    const float r = ex2(fminf(b + up[mt][s], 126.0f)), fi = FAR ? 1.0f : factor(mt, s, i);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float p0 = ex2(fmaf(x[mt][i][h][2 * s], fi[i][s], -mz[s])), p1 = ex2(fmaf(x[mt][i][h][2 * s + 1], fi[i][s], -mz[s]));
+                        const float p0 = ex2(fmaf(x[mt][i][h][2 * s], fi, -mz[mt][s])), p1 = ex2(fmaf(x[mt][i][h][2 * s + 1], fi, -mz[mt][s]));
                         acc.l[mt][s] += p0 + p1;
                         const __half2 u = __floats2half2_rn(p0 * r, p1 * r);
                         pw[mt][i][2 * h + s] = *reinterpret_cast<const uint32_t *>(&u);
@@ -514,7 +582,29 @@ __device__ __forceinline__ void attend(const Piece &pc, uint8_t *sm, int qbuf, u
         if (lane == 0)                  // for the warps of the other sets too
             asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(empty + st)), "r"(SG) : "memory");
     }
+    return t;
+}
+
+template <int D, int MT, int RG, int SG>
+__device__ __forceinline__ void attend(const Piece &pc, uint8_t *sm, int qbuf, uint64_t *full, uint64_t *empty, uint32_t *hdr,
+                                       long long &it, bool &dead, Acc<D, MT> &acc) {
+    const int sg = (threadIdx.x >> 5) * SG / kConsumers;
+    const int t = attend_tiles<D, MT, RG, SG, false>(pc, sm, qbuf, full, empty, hdr, it, pc.t0 + sg, dead, acc);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)                          // M from m from here on
+            acc.big[mt][s] = acc.m[mt][s] == -INFINITY ? -INFINITY : acc.big[mt][s] - acc.m[mt][s];
+    if (__builtin_expect(t < pc.t1, 0))
+        attend_tiles<D, MT, RG, SG, true>(pc, sm, qbuf, full, empty, hdr, it, t, dead, acc);
     it += pc.t1 - pc.t0;
+}
+
+// Whether a row of the piece sees a position: one that does and has no weights had scores past fp32's range only.
+__device__ __forceinline__ bool sees(const AttnArgs &a, const Piece &pc, int row) {
+    int lo, hi;
+    row_range(a.p, a.group, pc.kv, pc.n, pc.row0 + row, lo, hi);
+    return lo < hi;
 }
 
 // Joins the token groups of a piece and writes the rows: to the output, or,
@@ -564,26 +654,31 @@ __device__ __forceinline__ void finish(const AttnArgs &a, const Piece &pc, uint8
                 const int i = i0 + tid, r8 = i / Q % 8, wr = i / (8 * Q), d = i % Q * 4, row = wr * MT * 16 + mt * 16 + 8 * s + r8;
                 if (row >= pc.rows || (RG * 8 * Q < kConsumers * 32 && i >= RG * 8 * Q))
                     continue;
-                float m = -INFINITY, b = -INFINITY, l = 0.0f;
+                float m = -INFINITY, b = -INFINITY, l = 0.0f;        // b: M from m
 #pragma unroll
-                for (int t = 0; t < TG; ++t) {
+                for (int t = 0; t < TG; ++t)
                     m = fmaxf(m, s_m[t * R + row]);
-                    b = fmaxf(b, s_b[t * R + row]);
-                }
-                const float mz = m == -INFINITY ? 0.0f : m, bz = b == -INFINITY ? 0.0f : b;
+                const float mz = seen(m);
+#pragma unroll
+                for (int t = 0; t < TG; ++t)
+                    b = fmaxf(b, s_b[t * R + row] + (s_m[t * R + row] - mz));
+                const float bz = seen(b);
                 float4 o = make_float4(0, 0, 0, 0);
 #pragma unroll
                 for (int t = 0; t < TG; ++t) {
-                    l += s_l[t * R + row] * ex2(s_m[t * R + row] - mz);
-                    const float w = ex2(s_b[t * R + row] - bz);
+                    const float up = s_m[t * R + row] - mz;
+                    l += s_l[t * R + row] * ex2(up);
+                    const float w = ex2(s_b[t * R + row] + up - bz);
                     const float4 v = *reinterpret_cast<const float4 *>(join + (size_t)((t * RG + wr) * 8 + r8) * S::kPad + d);
                     o.x += v.x * w;
                     o.y += v.y * w;
                     o.z += v.z * w;
                     o.w += v.w * w;
                 }
-                // l is NaN where a score was: then so is the row
-                const float f = l == 0.0f ? 0.0f : exp2f(bz - mz) / l, lse2 = l == 0.0f ? -INFINITY : mz + log2f(l);
+                // l is NaN where a score was, or was infinite: then so is the row
+                if (l == 0.0f && pieces == 1 && sees(a, pc, row))
+                    l = __uint_as_float(0x7FFFFFFFu);
+                const float f = l == 0.0f ? 0.0f : exp2f(bz) / l;
                 o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
                 if (pieces == 1) {
                     const int r = pc.row0 + row;
@@ -593,11 +688,11 @@ __device__ __forceinline__ void finish(const AttnArgs &a, const Piece &pc, uint8
                     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(o.w), "f"(o.z));
                     *reinterpret_cast<uint2 *>(p.out + at * D + d) = make_uint2(x, y);
                     if (d == 0 && p.lse)
-                        p.lse[at] = lse2 * 0.69314718055994530942f;
+                        p.lse[at] = l == 0.0f ? -INFINITY : (mz + log2f(l)) * 0.69314718055994530942f;
                 } else {
                     __stcg(reinterpret_cast<float4 *>(a.part + ((size_t)slot * a.part_rows + row) * D + d), o);
                     if (d == 0)
-                        __stcg(a.part_sum + (size_t)slot * a.part_rows + row, make_float2(lse2, 1.0f));
+                        __stcg(a.part_sum + (size_t)slot * a.part_rows + row, make_float2(m, l * 0x1p-31f));   // no number of tokens brings that past 1
                 }
             }
         }
@@ -620,26 +715,26 @@ __device__ __forceinline__ void finish(const AttnArgs &a, const Piece &pc, uint8
                 float m = -INFINITY, l = 0.0f;
                 float4 o = make_float4(0, 0, 0, 0);
                 for (int k0 = 0; k0 < pieces; k0 += U) {
-                    float e[U];
+                    float2 e[U];                  // m, l 2^-31
                     float4 v[U];
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
                         const int k = k0 + u;
                         const size_t at = ((size_t)(pc.first + k) * 2 + (k == 0)) * a.part_rows + row;
-                        e[u] = k < pieces ? __ldcg(a.part_sum + at).x : -INFINITY;
+                        e[u] = k < pieces ? __ldcg(a.part_sum + at) : make_float2(-INFINITY, 0.0f);
                         v[u] = k < pieces ? __ldcg(reinterpret_cast<const float4 *>(a.part + at * D + d)) : make_float4(0, 0, 0, 0);
                     }
                     float nm = m;
 #pragma unroll
                     for (int u = 0; u < U; ++u)
-                        nm = fmaxf(nm, e[u]);
-                    const float mz = nm == -INFINITY ? 0.0f : nm, w0 = ex2(m - mz);
+                        nm = fmaxf(nm, e[u].x);
+                    const float mz = seen(nm), w0 = ex2(m - mz);
                     l *= w0;
                     o = make_float4(o.x * w0, o.y * w0, o.z * w0, o.w * w0);
                     m = nm;
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        const float w = ex2(e[u] - mz);
+                        const float w = e[u].y * ex2(e[u].x - mz);
                         l += w;
                         o.x += v[u].x * w;
                         o.y += v[u].y * w;
@@ -647,6 +742,8 @@ __device__ __forceinline__ void finish(const AttnArgs &a, const Piece &pc, uint8
                         o.w += v[u].w * w;
                     }
                 }
+                if (l == 0.0f && sees(a, pc, row))
+                    l = __uint_as_float(0x7FFFFFFFu);
                 const float w = l == 0.0f ? 0.0f : 1.0f / l;
                 const int r = pc.row0 + row;
                 const size_t to = (size_t)(pc.q0 + r / a.group) * p.q_heads + pc.head * a.group + r % a.group;
@@ -655,7 +752,7 @@ __device__ __forceinline__ void finish(const AttnArgs &a, const Piece &pc, uint8
                 asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(o.w * w), "f"(o.z * w));
                 *reinterpret_cast<uint2 *>(p.out + to * D + d) = make_uint2(lo, hi);
                 if (d == 0 && p.lse)
-                    p.lse[to] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+                    p.lse[to] = l == 0.0f ? -INFINITY : (m + (log2f(l) + 31.0f)) * 0.69314718055994530942f;
             }
         }
     }

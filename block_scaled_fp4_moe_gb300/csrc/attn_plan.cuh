@@ -39,7 +39,7 @@ struct AttnArgs {
     RowTile *recs;
     uint32_t *tickets;
     float *part;                         // parts of cut units: their rows,
-    float2 *part_sum;                    // and their m and l
+    float2 *part_sum;                    // and their m and l (attn.cu: l 2^-31)
     void *nans;                          // lists of NaN values (attn_tc.cu)
     uint32_t *hdr;
 };
@@ -211,6 +211,12 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity) {
             return false;
     return true;
 }
+
+// References of a softmax further from zero than this take the rounded form of their differences; half of its last place is 2^-4.
+constexpr float kFar = 0x1p20f;
+
+// A maximum as what is subtracted: 0 where nothing has been seen.
+__device__ __forceinline__ float seen(float v) { return v == -INFINITY ? 0.0f : v; }
 
 __device__ __forceinline__ float ex2(float x) {
     float y;

@@ -50,7 +50,6 @@ constexpr int kTcThreads = (kSoftWarps + kConvWarps + 2) * 32;
 constexpr int kNanEntries = 2048;
 // What 16 weights may sum to before the references move; 2^-32: with that factor, what 16 terms of l may.
 constexpr float kMostWeight = 4096.0f, kLeastSum = 0x1p-32f;
-constexpr float kFar = 0x1p20f;        // half of its last place: 2^-4
 
 // A value's NaN codes in a tile that some rows see in part: the unit, the position, the dims.
 struct NanEntry {
@@ -581,8 +580,6 @@ struct TileRow {
     uint32_t parity;
     uint32_t *hdr;
 };
-
-__device__ __forceinline__ float seen(float v) { return v == -INFINITY ? 0.0f : v; }
 
 __device__ __forceinline__ float factor(float f, const float *meta, int sub) { return fmaxf(f * meta[sub], 1.2e-38f); }
 

@@ -116,6 +116,7 @@ size_t moe_kv_attention_workspace_size(int T, int B, int q_heads, int kv_heads, 
  * influence, NaN included.  Rows of q past q_offsets[B] give no output.  Products of bf16 q and
  * E4M3 codes are exact, sums and softmax statistics fp32, the softmax weights are rounded to f16
  * relative to the row's largest contribution.  The same arguments give the same bits on the same device.
+ * Scores may be of any size that fp32 holds; a row whose largest score leaves that range is NaN.
  * Device-side errors (MOE_ERR_DEVICE_ASSERT): q_offsets that decrease or leave 0..T, a
  * kv_len outside 0..max_blocks * block_size (out stays untouched); a block id outside the
  * cache (that block is read as block 0).  B <= 8192, T <= 2^20,

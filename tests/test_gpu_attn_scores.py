@@ -79,7 +79,12 @@ def check(p, causal=True, window=0):
 MANY = {"64": ([(30, 300), (17, 140), (40, 40), (9, 3)], 8, 4, 64, 32), "128": ([(30, 300), (17, 140), (40, 40), (9, 3)], 8, 4, 128, 16),
         "64 cut": ([(8, 2000), (9, 700), (8, 400), (30, 130)], 8, 4, 64, 16), "128 cut": ([(8, 2000), (9, 700), (8, 400), (30, 130)], 8, 4, 128, 64),
         "128 two halves": ([(40, 900), (70, 300), (9, 100), (33, 64)], 8, 8, 128, 32), "64 two halves": ([(40, 900), (70, 300), (9, 100), (33, 64)], 8, 8, 64, 64)}
-FORMS = {f"many rows {k}": v for k, v in MANY.items()}
+# units of up to 16, 32 and 64 rows, one that many CTAs share, and a plan that is made by a kernel before (more than 256 requests)
+FEW = {"16 of 64": ([(1, 700), (2, 140), (4, 4), (1, 33), (3, 2)], 2, 4, 64, 32), "16 of 128": ([(1, 700), (2, 140), (4, 4), (1, 33), (3, 2)], 2, 4, 128, 16),
+       "32 of 64": ([(3, 500), (4, 200), (3, 90)], 2, 8, 64, 64), "32 of 128": ([(3, 500), (4, 200), (3, 90)], 2, 8, 128, 16),
+       "64 of 64": ([(8, 500), (5, 90)], 2, 8, 64, 32), "64 of 128": ([(8, 500), (5, 90)], 2, 8, 128, 128), "one of 64": ([(1, 9000)], 1, 2, 64, 32),
+       "one of 128": ([(2, 7000)], 2, 8, 128, 64), "300 requests": ([(1, 1 + i % 140) for i in range(300)], 1, 2, 64, 16)}
+FORMS = {**{f"many rows {k}": v for k, v in MANY.items()}, **{f"few rows {k}": v for k, v in FEW.items()}}
 
 
 @pytest.mark.parametrize("sign", [1, -1])
