@@ -51,7 +51,9 @@ constexpr int kNanEntries = 2048;
 // What 16 weights may sum to before the references move; 2^-32: with that factor, what 16 terms of l may.
 constexpr float kMostWeight = 4096.0f, kLeastSum = 0x1p-32f;
 
-// A value's NaN codes in a tile that some rows see in part: the unit, the position, the dims.
+// A value's NaN codes in a tile that some rows see in part: the unit, the position, the dims.  A CTA's list of them is
+// never written over: past its end values are only counted (and found in the cache, nan_rows).  A unit's are in it before its
+// last product ends; those of the next unit may be on their way then, so that an entry counts from its mark on.
 struct NanEntry {
     int unit, token;
     uint32_t dims[4];
@@ -74,7 +76,8 @@ struct TcSmem {
     static constexpr bool kOwnW = D == 64;                   // weights in columns of their own
     __host__ __device__ static constexpr int w_col(int h, int tok) { return kOwnW ? 384 + 64 * h + tok / 2 : 128 * h + (tok >= 64 ? 64 : 0) + (tok % 64) / 2; }
     static constexpr int kBarCount = 2 * kRaw + 2 * kOps + 8 + 1;
-    static constexpr size_t kBytes = kOffBars + kBarCount * 8 + 32 + 1024;     // + alignment to 1024
+    static constexpr size_t kOffMarks = kOffBars + kBarCount * 8 + 32;         // a bit for each entry of the list of NaN values
+    static constexpr size_t kBytes = kOffMarks + kNanEntries / 8 + 1024;       // + alignment to 1024
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -303,6 +306,7 @@ __device__ __forceinline__ void tc_convert(const AttnArgs &a, const Plan &pl, ui
     using S = TcSmem<D>;
     const int tid = threadIdx.x - kSoftWarps * 32, lane = tid & 31;
     NanEntry *nans = reinterpret_cast<NanEntry *>(static_cast<uint8_t *>(a.nans) + (size_t)blockIdx.x * kAttnNanBytes);
+    uint32_t *marks = reinterpret_cast<uint32_t *>(sm + S::kOffMarks);
     Walk walk(a, pl, a.recs);
     Piece pc;
     uint32_t op = 0;
@@ -384,12 +388,16 @@ __device__ __forceinline__ void tc_convert(const AttnArgs &a, const Plan &pl, ui
                         while (nan) {
                             const int e = (__ffs(nan) - 1) >> 3;
                             nan &= ~(0xFFu << (8 * e));
-                            const uint32_t at = atomicAdd(nan_count, 1u) % kNanEntries;
+                            if (*reinterpret_cast<volatile uint32_t *>(nan_count) > kNanEntries)
+                                continue;                    // counted far enough
+                            const uint32_t at = atomicAdd(nan_count, 1u);
+                            if (at >= kNanEntries)
+                                continue;
                             NanEntry x{unit, tok0 + chunk * 16 + 4 * q + e, {0, 0, 0, 0}, {0, 0}};
                             x.dims[row >> 5] = 1u << (row & 31);
                             nans[at] = x;
                             __threadfence();
-                            atomicAdd(nan_count + 1, 1u);
+                            atomicOr(marks + at / 32, 1u << (at & 31));
                         }
                     }
                     store(c, row, chunk);
@@ -868,14 +876,9 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
             scale = other_scale = l = __uint_as_float(0x7FFFFFFFu);
         const int rows_here = pair ? min(128, pc.rows - 128 * h) : pc.rows;
         const int cap = min(128, (int)min((long long)p.T * a.group, 128ll));       // rows of a part in the workspace
-        // entries so far, once all of them are written (the converters may be in the next unit already)
+        // values so far, this unit's all among them
         const uint32_t nan_seen = *reinterpret_cast<volatile uint32_t *>(nan_count);
-        if (nan_seen) {
-            const uint64_t t0 = globaltimer_ns();
-            while ((int)(*reinterpret_cast<volatile uint32_t *>(nan_count + 1) - nan_seen) < 0 && globaltimer_ns() - t0 < kWaitLimitNs) {
-            }
-            __threadfence();
-        }
+        const volatile uint32_t *marks = reinterpret_cast<const volatile uint32_t *>(sm + S::kOffMarks);
         const size_t to = (size_t)(pc.q0 + row / a.group) * p.q_heads + pc.head * a.group + row % a.group;
         const NanEntry *nans = reinterpret_cast<const NanEntry *>(static_cast<const uint8_t *>(a.nans) + (size_t)blockIdx.x * kAttnNanBytes);
 #pragma unroll 1
@@ -890,6 +893,9 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
             }
             uint32_t bad = 0;                      // dims whose values this row saw as NaN
             for (uint32_t k = 0; k < min(nan_seen, (uint32_t)kNanEntries); ++k) {
+                if (!(marks[k / 32] >> (k & 31) & 1))
+                    continue;
+                __threadfence();
                 const int nu = __ldcg(&nans[k].unit), nt = __ldcg(&nans[k].token);
                 if (nu == unit && nt >= lo && nt < hi && (pair || both || (((nt / kTile - pc.tile0 - pc.t0) & 1) == h)))
                     bad |= __ldcg(&nans[k].dims[c]);
@@ -1079,9 +1085,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             mbar_init(b.q_ready + i, 4);
         }
         mbar_init(b.spare, 1);
-        nan_count[0] = nan_count[1] = 0;            // entries begun, entries written
+        *nan_count = 0;
         fence_barrier_init();
     }
+    if (threadIdx.x < kNanEntries / 32)
+        reinterpret_cast<uint32_t *>(sm + S::kOffMarks)[threadIdx.x] = 0;
     if (warp == kSoftWarps + kConvWarps + 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(s_taddr)));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");

@@ -776,3 +776,26 @@ def test_linear_forms_by_size(T, N, K):
     xt, _, weight, y = linear_case(T, N, K, seed=50)
     want, bound = ref.linear(f64(xt), weight.codes.cpu().numpy(), weight.scale.cpu().numpy())
     assert (np.abs(f64(y) - want) <= bound).all()
+
+
+@pytest.mark.parametrize("dim,new,group,kv,nans", [(128, 20, 4, 100, 15), (128, 20, 4, 230, 15), (64, 20, 4, 120, 15), (64, 30, 2, 250, 24),
+                                                   (128, 8, 8, 60, 6), (128, 100, 4, 128, 40)])
+def test_attention_many_rows_nan_values_of_unit_after_unit(dim, new, group, kv, nans):
+    """More units than CTAs, of one or two tiles each and of one request or another: the NaN values of every head and request are found
+    by their own rows alone, also where the next unit's are met meanwhile and where there are more than a CTA's list holds."""
+    B, first = 60, kv - new // 2 - 1                      # some new tokens come before the NaN ones, and see none
+    p = Problem([(new, kv - b % 3) for b in range(B)], 8, group, dim, 32, seed=51)
+    clean_out, clean_lse = p.run()
+    sees = []
+    for b in range(B):
+        end = min(first + nans, p.kv[b])
+        has = b % 4 != 3                                   # some requests have none
+        for j in range(first, end if has else first):
+            p.cache.v[p.table[b, j // 32], :, j % 32] = 0x7F
+        sees += [has and p.kv[b] - new + i >= first for i in range(new)]
+    out, lse = p.run()
+    sees = torch.tensor(sees, device="cuda")
+    assert p.status == 0 and torch.equal(lse, clean_lse) and sees.any() and not sees.all()
+    assert torch.equal(out[~sees], clean_out[~sees]) and bool(torch.isnan(out[sees].float()).all())
+    again, _ = p.run()
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16))
