@@ -118,7 +118,7 @@ __device__ __forceinline__ bool barrier_any(int id, int threads, bool v) {
 // Up to four tiles of a piece: a lane for each of their sub-blocks.
 struct Batch {
     int tiles;                    // 0: there is none
-    int head, hi, page, scale;
+    int head, page, scale;
     long long tok;                // the lane's first token
     bool live;
 };
@@ -133,25 +133,28 @@ __device__ __forceinline__ void stream_cache(const AttnArgs &a, const Plan &pl, 
     const uint8_t *codes = is_v ? p.cache.v : p.cache.k, *scale = is_v ? p.cache.v_scale : p.cache.k_scale;
     Walk walk(a, pl, recs);
     Piece pc;
-    int t = 0;
-    bool more = walk.next(pc);
-    if (more)
+    int t = 0, lo = 0, hi = 0;                  // the piece's next tile; the positions that its rows see: from the first row's first
+    bool more = true;
+    auto next_piece = [&] {
+        more = walk.next(pc);
+        if (!more)
+            return;
         t = pc.t0;
+        row_range(p, a.group, pc.kv, pc.n, pc.row0, lo, hi);        // blocks before may be gone from the table
+        hi = p.causal ? min(pc.kv, pc.kv - pc.n + (pc.row0 + pc.rows - 1) / a.group + 1) : pc.kv;
+    };
+    next_piece();
     // the next batch, its block ids asked for
     auto pages = [&](Batch &b) {
         b.tiles = 0;
-        while (more && t == pc.t1) {
-            more = walk.next(pc);
-            if (more)
-                t = pc.t0;
-        }
+        while (more && t == pc.t1)
+            next_piece();
         if (!more)
             return;
         b.tiles = min(4, pc.t1 - t);
         b.head = pc.head;
-        b.hi = p.causal ? min(pc.kv, pc.kv - pc.n + (pc.row0 + pc.rows - 1) / a.group + 1) : pc.kv;
         b.tok = (long long)(pc.tile0 + t) * kTile + lane * 16;
-        b.live = lane < kSubs * b.tiles && b.tok < b.hi;
+        b.live = lane < kSubs * b.tiles && b.tok < hi && b.tok + 16 > lo;
         b.page = b.live ? __ldg(p.table + (size_t)pc.request * p.max_blocks + (b.tok >> a.shift)) : 0;
         t += b.tiles;
     };
@@ -177,8 +180,9 @@ __device__ __forceinline__ void stream_cache(const AttnArgs &a, const Plan &pl, 
         // sub-blocks of one block that lie in one tile are one copy, issued by the first one's lane
         const uint32_t live = __ballot_sync(0xffffffffu, b0.live);
         const int in_block = (int)(b0.tok & ((1 << a.shift) - 1)) >> 4, block_subs = 1 << (a.shift - 4);
-        const int left = __popc((live >> (lane & ~(kSubs - 1))) & ((1u << kSubs) - 1)) - sub;
-        const bool leads = b0.live && (sub == 0 || in_block == 0);
+        const uint32_t here = (live >> (lane & ~(kSubs - 1))) & ((1u << kSubs) - 1);         // one run of the tile's sub-blocks
+        const int left = 32 - __clz(here) - sub;
+        const bool leads = b0.live && (sub == __ffs(here) - 1 || in_block == 0);
         const uint32_t bytes = (uint32_t)min(block_subs - in_block, left) * S::kSubBytes;
         const size_t src = ((((size_t)b0.page * p.cache.kv_heads + b0.head) << a.shift) + in_block * 16) * D;
         for (int i = 0; i < b0.tiles; ++i, ++it) {
@@ -270,8 +274,9 @@ __device__ __forceinline__ void load_queries(const AttnArgs &a, const Plan &pl, 
                 }
                 if (c == 0) {
                     RowInfo r{a.scale_log2 * exp2i(-sh), 0, pc.kv};
-                    if (live)
-                        row_range(p, a.group, pc.kv, pc.n, row, r.lo, r.hi);
+                    row_range(p, a.group, pc.kv, pc.n, row, r.lo, r.hi);
+                    if (!live)                  // from the first row's first position, so that nothing unread is looked at for it
+                        r.hi = pc.kv;
                     info[rr] = r;
                 }
             }

@@ -219,12 +219,14 @@ __device__ __forceinline__ void tc_stream(const AttnArgs &a, const Plan &pl, uin
     while (walk.next(pc)) {
         const int n = pc.t1 - pc.t0;
         const int hi = p.causal ? min(pc.kv, pc.kv - pc.n + (pc.row0 + pc.rows - 1) / a.group + 1) : pc.kv;
+        int lo, unused;                    // the first row sees furthest back: blocks before may be gone from the table
+        row_range(p, a.group, pc.kv, pc.n, pc.row0, lo, unused);
         const int32_t *row = p.table + (size_t)pc.request * p.max_blocks;
         // a batch of four tiles' blocks and scales at a time, a lane for each sub-block; the next batch's on their way
         int page, ks, vs;
         auto fetch = [&](int t0, int &pg) {
             const long long tok = (long long)(pc.tile0 + pc.t0 + t0) * kTile + lane * 16;
-            pg = t0 < n && tok < hi && t0 + lane / kSubs < n ? __ldg(row + (tok >> a.shift)) : -1;
+            pg = t0 < n && tok < hi && tok + 16 > lo && t0 + lane / kSubs < n ? __ldg(row + (tok >> a.shift)) : -1;
         };
         int next;
         fetch(0, next);
@@ -234,7 +236,7 @@ __device__ __forceinline__ void tc_stream(const AttnArgs &a, const Plan &pl, uin
             page = next;
             fetch(t0 + 4, next);
             const long long tok = (long long)(pc.tile0 + pc.t0 + t0) * kTile + lane * 16;
-            const bool live = t0 + lane / kSubs < n && tok < hi;
+            const bool live = t0 + lane / kSubs < n && tok < hi && tok + 16 > lo;
             if (live && (page < 0 || page >= p.cache.num_blocks)) {
                 record_status(a.hdr, MOE_ERR_DEVICE_ASSERT);
                 page = 0;
@@ -278,8 +280,8 @@ __device__ __forceinline__ void tc_stream(const AttnArgs &a, const Plan &pl, uin
                     __syncwarp();
                     const long long tk = (long long)(pc.tile0 + pc.t0 + (is_v ? vt : t)) * kTile + sub * 16;
                     const int in_block = (int)(tk & ((1 << a.shift) - 1)) >> 4, block_subs = 1 << (a.shift - 4);
-                    if (mine && (here >> sub & 1) && (sub == 0 || in_block == 0)) {
-                        const uint32_t bytes = (uint32_t)min(block_subs - in_block, __popc(here) - sub) * (16 * D);
+                    if (mine && (here >> sub & 1) && (sub == __ffs(here) - 1 || in_block == 0)) {    // one run of sub-blocks
+                        const uint32_t bytes = (uint32_t)min(block_subs - in_block, 32 - __clz(here) - sub) * (16 * D);
                         const size_t src = ((((size_t)pg * p.cache.kv_heads + pc.head) << a.shift) + in_block * 16) * D;
                         asm volatile(
                             "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -376,12 +378,14 @@ __device__ __forceinline__ void tc_convert(const AttnArgs &a, const Plan &pl, ui
                     uint32_t *w = reinterpret_cast<uint32_t *>(&c);
                     int row, chunk;
                     place(u, row, chunk);
-                    const int left = hi1 - (tok0 + chunk * 16);     // tokens of the chunk that some row sees
+                    const int left = hi1 - (tok0 + chunk * 16), skip = lo0 - (tok0 + chunk * 16);    // some row sees tokens skip .. left - 1 of the chunk
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const int k = left - 4 * q;
                         if (k < 4)
                             w[q] &= k <= 0 ? 0u : (1u << (8 * k)) - 1;
+                        if (skip > 4 * q)
+                            w[q] &= skip >= 4 * q + 4 ? 0u : 0xFFFFFFFFu << (8 * (skip - 4 * q));
                         uint32_t nan = __vcmpeq4(w[q] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
                         w[q] &= ~nan;
 #pragma unroll 1

@@ -113,7 +113,8 @@ size_t moe_kv_attention_workspace_size(int T, int B, int q_heads, int kv_heads, 
  *   out [T, q_heads, head_dim] bf16 = sum_j softmax_j(softmax_scale q.k_j) v_j
  *   lse [T, q_heads] fp32 or NULL   = log sum_j exp(softmax_scale q.k_j)
  * A row that sees nothing gives zeros and -infinity.  What it does not see has no
- * influence, NaN included.  Rows of q past q_offsets[B] give no output.  Products of bf16 q and
+ * influence, NaN included, and table entries of blocks that no row sees (past the request's
+ * end, before its window) are not read.  Rows of q past q_offsets[B] give no output.  Products of bf16 q and
  * E4M3 codes are exact, sums and softmax statistics fp32, the softmax weights are rounded to f16
  * relative to the row's largest contribution.  The same arguments give the same bits on the same device.
  * Scores may be of any size that fp32 holds; a row whose largest score leaves that range is NaN.

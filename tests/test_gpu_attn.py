@@ -799,3 +799,25 @@ def test_attention_many_rows_nan_values_of_unit_after_unit(dim, new, group, kv, 
     assert torch.equal(out[~sees], clean_out[~sees]) and bool(torch.isnan(out[sees].float()).all())
     again, _ = p.run()
     assert torch.equal(out.view(torch.int16), again.view(torch.int16))
+
+
+@pytest.mark.parametrize("size", [16, 32, 64, 128])
+@pytest.mark.parametrize("dim,kv_heads,group,lens", [
+    (64, 2, 4, [(1, 700), (2, 300), (1, 90), (3, 129)]), (128, 1, 8, [(1, 700), (2, 300), (1, 90), (4, 257)]), (128, 2, 8, [(8, 500), (7, 200)]),
+    (64, 8, 4, [(9, 700), (20, 300), (40, 200), (8, 90)]), (128, 8, 8, [(40, 700), (9, 300), (30, 260), (12, 130)])])
+def test_attention_blocks_before_the_window_are_not_looked_at(size, dim, kv_heads, group, lens):
+    """Entries of blocks that no row sees any more may be anything, and so may what lies before the window in a block that is seen."""
+    for window in (1, 20, 100, 150):
+        p = Problem(lens, kv_heads, group, dim, size, seed=52)
+        want, want_lse = p.check(window=window)
+        table = p.table.copy()
+        for b, (n, kv) in enumerate(lens):
+            first = max(0, kv - n - window + 1)            # the first new token's first position
+            table[b, : first // size] = -1
+            if first % size:
+                block = p.table[b, first // size]
+                p.cache.k[block, :, : first % size] = 0x7F
+                p.cache.v[block, :, : first % size] = 0xFF
+        got, lse = p.run(window=window, table=table)
+        assert p.status == 0
+        assert torch.equal(got, want) and torch.equal(lse, want_lse)
