@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(AppendProb
 
 cudaError_t launch_kv_tables(const TablesProblem &p, cudaStream_t stream) {
     const size_t smem = (size_t)(3 * p.B + 1) * sizeof(int32_t);
-    if (smem > 48 * 1024) {
+    if (smem > 40 * 1024) {             // 48 KB without asking, of which the kernel's static memory takes its part
         const cudaError_t e = cudaFuncSetAttribute(kv_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess)
             return e;

@@ -1,6 +1,10 @@
 """The attention half on the GPU against its definitions in 64 bits
 (attn_reference): tables and cache contents exactly, attention and projection
 within bounds derived from the kernels' arithmetic (stated in the reference)."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -821,3 +825,13 @@ def test_attention_blocks_before_the_window_are_not_looked_at(size, dim, kv_head
         got, lse = p.run(window=window, table=table)
         assert p.status == 0
         assert torch.equal(got, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("B", [4053, 4054, 4095, 4096])
+def test_tables_of_the_batches_around_48_kb_of_shared_memory(B):
+    """In a process of their own: a larger batch before them would have raised the kernel's limit for them."""
+    code = f"import test_gpu_attn as t; t.test_tables_match_the_definition({B}, 16, 40, 2, 5)"
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", code], cwd=here, env={**os.environ, "PYTHONPATH": os.path.dirname(here)}, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
