@@ -260,7 +260,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) fp8_gemm_kernel(const
         for (long long i = max(0ll, it - kStages); i < it && !dead; ++i)
             wait_phase(full + i % kStages, (uint32_t)((i / kStages) & 1));
     } else if (warp == 1) {
-        // ---- MMAs
+        // ---- MMAs.  Fused: the kernel before may run for long yet, and its time is none of the waits' limit.
+        if (FUSED)
+            pdl_wait();
         bool dead = false;
         int it = 0, piece = 0;
         for (int tile = r0.tile; tile < a.tiles && !dead; tile += r0.step, ++piece) {

@@ -1,6 +1,7 @@
 """The attention half on the GPU against its definitions in 64 bits
 (attn_reference): tables and cache contents exactly, attention and projection
 within bounds derived from the kernels' arithmetic (stated in the reference)."""
+import ctypes
 import os
 import subprocess
 import sys
@@ -835,3 +836,41 @@ def test_tables_of_the_batches_around_48_kb_of_shared_memory(B):
     r = subprocess.run([sys.executable, "-c", code], cwd=here, env={**os.environ, "PYTHONPATH": os.path.dirname(here)}, capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+LONG_KERNEL = r"""
+#include <cstdint>
+// Lets the next kernel start at once, and runs for `ms` more on one SM.
+__global__ void long_kernel(unsigned ms) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    uint64_t t0, t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
+    for (unsigned i = 0; i < 1000u * ms; ++i) {            // at most 1 us each: ends by itself whatever the timer says
+        __nanosleep(1000);
+        asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+        if (t - t0 > ms * 1000000ull)
+            break;
+    }
+}
+extern "C" int run_long_kernel(unsigned ms, void *stream) {
+    long_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(ms);
+    return cudaGetLastError();
+}
+"""
+
+
+@pytest.mark.parametrize("T", [1, 8, 40, 300])
+def test_linear_behind_a_kernel_that_runs_for_long(T, tmp_path):
+    """The limits of a call's waits do not count what the kernel before it still has to do."""
+    src, lib = tmp_path / "long.cu", tmp_path / "long.so"
+    src.write_text(LONG_KERNEL)
+    subprocess.run([_build.nvcc_path(), *_build.ARCH_FLAGS, "-shared", "-Xcompiler", "-fPIC", "-o", str(lib), str(src)], check=True)
+    run = ctypes.CDLL(str(lib)).run_long_kernel
+    run.argtypes = [ctypes.c_uint, ctypes.c_void_p]
+    ws = workspace(attn.moe_linear_fp8_workspace_size(T, 333, 1040))
+    xt, _, weight, want = linear_case(T, 333, 1040, seed=53, ws=ws)
+    y = torch.zeros_like(want)
+    assert run(400, torch.cuda.current_stream().cuda_stream) == 0
+    attn.moe_linear_fp8(xt, weight, y, ws)
+    torch.cuda.synchronize()
+    assert status(ws) == 0 and torch.equal(y, want)
