@@ -576,6 +576,9 @@ __global__ void selftest_decode_kernel(const uint8_t *codes, uint16_t *out, int 
 
 // ---------------------------------------------------------------- host side
 
+// Dynamic shared memory that a launch may have without asking: 48 KB less, generously, the kernels' static memory.
+constexpr size_t kSmemUnasked = 40 * 1024;
+
 bool ffn_shape_supported(int H, int I) { return H > 0 && I > 0 && H % 64 == 0 && I % 64 == 0 && I <= 16384; }
 
 template <int MODE, bool WIN, bool ALIGNED>
@@ -586,7 +589,7 @@ static cudaError_t launch_one(const FfnArgs &a, int grid, size_t smem, cudaStrea
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess)
         return err;
-    if (smem > 48 * 1024 && set_bytes[dev & 63].load() < (int)smem) {
+    if (smem > kSmemUnasked && set_bytes[dev & 63].load() < (int)smem) {
         err = cudaFuncSetAttribute(ffn_kernel<MODE, NW, D, WIN, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    (int)smem);
         if (err != cudaSuccess)
@@ -651,7 +654,7 @@ cudaError_t launch_ffn(const FfnProblem &pr, void *ws, const WsLayout &L, int nu
         return err;
 
     const size_t hsmem = 2 * (size_t)I * sizeof(float);
-    if (hsmem > 48 * 1024 &&
+    if (hsmem > kSmemUnasked &&
         (err = cudaFuncSetAttribute(hfin_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)hsmem)) !=
             cudaSuccess)
         return err;
@@ -702,7 +705,7 @@ cudaError_t launch_combine(const float *yent, int entries, const int32_t *inv_po
 cudaError_t launch_hfin(void *ws, const WsLayout &L, int T, int entries, int I, bool tc_order, cudaStream_t stream) {
     const size_t hsmem = 2 * (size_t)I * sizeof(float);
     cudaError_t err;
-    if (hsmem > 48 * 1024 &&
+    if (hsmem > kSmemUnasked &&
         (err = cudaFuncSetAttribute(hfin_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)hsmem)) !=
             cudaSuccess)
         return err;
