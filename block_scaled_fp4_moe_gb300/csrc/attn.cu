@@ -9,10 +9,12 @@
 // Numbers.  A row of q is scaled by a power of two into f16's range (bf16's 8
 // significant bits fit f16's 11) and a code is exact in f16, so the products
 // q.c are exact and summed in fp32 by f16 MMAs; 2^a multiplies the sum.
-// The weight of d_j is w_ij = 2^(x_ij + b_j - M_i), M_i = max_j (x_ij + b_j): the
+// The weight of d_j is w_ij = 2^(x_ij + b_j - M_i + 15), M_i = max_j (x_ij + b_j): the
 // block's exponent is inside the power, so that the f16 rounding of w (2^-12
-// of itself, or 2^-25 of the row's largest) is relative to what the row's
-// largest contribution can be, however far the blocks' exponents lie apart.
+// of itself, or 2^-40 of the row's largest) is relative to what the row's
+// largest contribution can be.  The largest weight is 2^15, f16's last whole binade: a block whose exponent lies far
+// above the others' leaves them their bits, in the dims where it has nothing itself, down to 29 binades below it (with a largest
+// weight of 1, 14: those dims were off by 5e-3 at 16 binades and 0.67 at 24).
 // l is summed from the unrounded fp32 p with its own maximum m.
 // The power of p is one FMA, x's product exact; m, rounded, may lie under it by half of its last place.  Where a warp's maxima pass
 // kFar (half a place of 2^28 is a factor of 2^16) a loop of its own takes over, in which the products are rounded first, as m was, so that
@@ -55,6 +57,7 @@ constexpr int kThreads = 384;          // three warpgroups: two of consumers, on
 constexpr int kQWarps = 2;
 constexpr int kSmallRequests = 256;    // most requests and row tiles of a plan in shared memory
 constexpr int kSmallTiles = 288;
+constexpr float kLift = 15.0f;         // the largest weight's power
 
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnArgs a) {
     extern __shared__ int s_first[];
@@ -400,7 +403,7 @@ __device__ __forceinline__ int attend_tiles(const Piece &pc, uint8_t *sm, int qb
                         }
             }
         };
-        float mz[MT][2], up[MT][2];                           // m to subtract (0 where nothing is seen yet), m - M
+        float mz[MT][2], up[MT][2];                           // m to subtract (0 where nothing is seen yet), m - M + 15
         if constexpr (!FAR) {
             float nm[MT][2], nb[MT][2];
             bool grew = false, far = false;
@@ -445,7 +448,7 @@ __device__ __forceinline__ int attend_tiles(const Piece &pc, uint8_t *sm, int qb
                     acc.l[mt][s] *= ex2(acc.m[mt][s] - mz[mt][s]);
                     acc.m[mt][s] = nm[mt][s];
                     acc.big[mt][s] = nb[mt][s];
-                    up[mt][s] = mz[mt][s] - seen(nb[mt][s]);
+                    up[mt][s] = mz[mt][s] - seen(nb[mt][s]) + kLift;
                 }
         } else {
 #pragma unroll
@@ -487,7 +490,7 @@ __device__ __forceinline__ int attend_tiles(const Piece &pc, uint8_t *sm, int qb
                     acc.m[mt][s] = nm;
                     acc.big[mt][s] = nb;
                     mz[mt][s] = 0.0f;
-                    up[mt][s] = -seen(nb);
+                    up[mt][s] = kLift - seen(nb);
                 }
                 scale_rows(acc.o[mt], r[0], r[1]);
             }
@@ -495,7 +498,7 @@ __device__ __forceinline__ int attend_tiles(const Piece &pc, uint8_t *sm, int qb
         uint32_t pw[MT][NS][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            // weights: p 2^(b + m - M).  The power is at most 2^126: above it (M - m far below b) p is zero.
+            // weights: p 2^(b + m - M + 15).  The power is at most 2^126: above it (M - m far below b) p is zero.
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
                 const float b = ex[kSubs + i * TG + tg];
@@ -673,7 +676,7 @@ __device__ __forceinline__ void finish(const AttnArgs &a, const Piece &pc, uint8
                 for (int t = 0; t < TG; ++t) {
                     const float up = s_m[t * R + row] - mz;
                     l += s_l[t * R + row] * ex2(up);
-                    const float w = ex2(s_b[t * R + row] + up - bz);
+                    const float w = ex2(s_b[t * R + row] + up - bz - kLift);
                     const float4 v = *reinterpret_cast<const float4 *>(join + (size_t)((t * RG + wr) * 8 + r8) * S::kPad + d);
                     o.x += v.x * w;
                     o.y += v.y * w;

@@ -30,7 +30,8 @@
 // conversions are the same code.
 //
 // The running maxima of a row are references that move only where scores have outgrown them (16 weights sum to more than
-// 2^12: f16 holds up to 2^16, and its rounding is relative).  So a score is read once: 32 of a row at a time become weights,
+// f16 holds; its rounding is relative).  A largest weight is 2^6 when they have moved, so that 20 binades below it keep their bits
+// (2^8, with less room to grow, takes 161 us for 152 on the first case below; 2^0 to 2^6 the same).  So a score is read once: 32 of a row at a time become weights,
 // whose sums say whether they fit.  Where they do not, the references move to the maxima (of the tile, or of the 32 where the
 // weights lie over the scores), the half waits for its last product and rescales O, and the tile's weights so far, in TMEM; then
 // the weights are made, and not looked at again.  Only a unit's first tile is read for its maxima first.
@@ -48,8 +49,9 @@ namespace {
 constexpr int kSoftWarps = 8, kConvWarps = 6;
 constexpr int kTcThreads = (kSoftWarps + kConvWarps + 2) * 32;
 constexpr int kNanEntries = 2048;
-// What 16 weights may sum to before the references move; 2^-32: with that factor, what 16 terms of l may.
-constexpr float kMostWeight = 4096.0f, kLeastSum = 0x1p-32f;
+// What 16 weights may sum to before the references move: f16's largest number; 2^-32: with that factor, what 16 terms of l may.  The
+// power of a largest weight when they have: 16 of them sum to 2^10, the rest is room to grow.
+constexpr float kMostWeight = 65504.0f, kLeastSum = 0x1p-32f, kLift = 6.0f;
 
 // A value's NaN codes in a tile that some rows see in part: the unit, the position, the dims.  A CTA's list of them is
 // never written over: past its end values are only counted (and found in the cache, nan_rows).  A unit's are in it before its
@@ -575,7 +577,7 @@ __device__ __noinline__ void nan_rows(const AttnArgs &a, int request, int head, 
     }
 }
 
-// A row's references, m and M - m, and its l with respect to m.
+// A row's references, m and M - m (less kLift), and its l with respect to m.
 struct Refs {
     float m, rel, l;
 };
@@ -661,7 +663,7 @@ __device__ __forceinline__ Refs move_and_weigh(Refs r, const TileRow &t, int c) 
                 }
             }
             const float to = fmaxf(nm, r.m), z = seen(to);
-            const float was = r.rel + (r.m - z), want = fmaxf(nrel + (nm - z), -INFINITY);     // M from the new m, as it is and at least
+            const float was = r.rel + (r.m - z), want = fmaxf(nrel + (nm - z) - kLift, -INFINITY);     // M from the new m, as it is and at least
             // nothing is left of sums 150 binades down: their reference may be far off, and is not added to
             const bool anew = !(want - was < 150.0f);
             const float up = anew ? 0.0f : fmaxf(ceilf(want - was), 0.0f), by = anew ? 0.0f : ex2(-up);
@@ -684,14 +686,14 @@ __device__ __forceinline__ Refs move_and_weigh(Refs r, const TileRow &t, int c) 
                 }
             }
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-            const __half2 by2 = __float2half2_rn(by);
 #pragma unroll 1
             for (int k = 0; k < c; ++k) {
                 uint32_t w[16];
                 tmem_ld16(reinterpret_cast<float(&)[16]>(w), t.lanes + S::w_col(t.h, 32 * k));
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(w + e), by2);
+                    const float2 f2 = __half22float2(*reinterpret_cast<const __half2 *>(w + e));      // f16 holds no factor below 2^-24
+                    const __half2 v = __floats2half2_rn(f2.x * by, f2.y * by);
                     w[e] = *reinterpret_cast<const uint32_t *>(&v);
                 }
                 tmem_st16(t.lanes + S::w_col(t.h, 32 * k), w);

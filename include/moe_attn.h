@@ -115,8 +115,10 @@ size_t moe_kv_attention_workspace_size(int T, int B, int q_heads, int kv_heads, 
  * A row that sees nothing gives zeros and -infinity.  What it does not see has no
  * influence, NaN included, and table entries of blocks that no row sees (past the request's
  * end, before its window) are not read.  Rows of q past q_offsets[B] give no output.  Products of bf16 q and
- * E4M3 codes are exact, sums and softmax statistics fp32, the softmax weights are rounded to f16
- * relative to the row's largest contribution.  The same arguments give the same bits on the same device.
+ * E4M3 codes are exact (of q down to 2^-39 of its row's largest element), sums and softmax statistics fp32.  The softmax weights
+ * are rounded to f16: a weight times its block's 2^exponent to 2^-11 of itself or 2^-29 of the row's largest such product, which is one for
+ * all dims.  So a block whose exponent lies more than about 20 binades above the others' costs those precision in every dim, also
+ * where it is small itself.  The same arguments give the same bits on the same device.
  * Scores may be of any size that fp32 holds; a row whose largest score leaves that range is NaN.
  * Device-side errors (MOE_ERR_DEVICE_ASSERT): q_offsets that decrease or leave 0..T, a
  * kv_len outside 0..max_blocks * block_size (out stays untouched); a block id outside the

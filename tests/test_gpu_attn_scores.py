@@ -173,3 +173,30 @@ def test_attention_scores_past_fp32(form):
         bound = 2.0 ** -8 * np.abs(o) + 2.0 ** -10 * ((w / l) @ np.abs(v)) + len(v) * 448 * 2.0 ** -25 * (w / l * 2.0 ** ve).max(1, keepdims=True)
         assert (np.abs(got[t, h] - o) <= bound)[ok].all() and (np.abs(got_lse[t, h] - want) <= 2.0 ** -20 * np.abs(want))[ok].all()
         assert np.isnan(got[t, h][~ok]).all()
+
+
+@pytest.mark.parametrize("above", [12, 16, 20, 24])
+@pytest.mark.parametrize("form", [f for f in FORMS if "300" not in f])
+def test_attention_one_block_of_far_larger_values_leaves_the_others_their_bits(form, above):
+    """A visible block with an exponent far above the others', and values in the first half of the dims only: the other half is made of the
+    other blocks, whose weights are small beside that block's contribution."""
+    lens, kv_heads, group, dim, size = FORMS[form]
+    p = base.Problem(lens, kv_heads, group, dim, size, seed=6, exps=(-7, -7), q_scale=0.3)
+    for b, kv in enumerate(p.kv):
+        block = p.table[b, (kv - p.n[b]) // size // 2]     # seen by every row
+        p.cache.ve[block] = -7 + above
+        p.cache.v[block, :, :, dim // 2:] = 0
+    out, _ = p.run()
+    assert p.status == 0
+    got, half = base.f64(out), dim // 2
+    for t, h, x, v, ve, _ in units(p):
+        x = x * p.scale * math.log2(math.e)
+        w = np.exp2(x - x.max(1, keepdims=True))
+        w /= w.sum(1, keepdims=True)
+        o, top = w @ v, (w * 2.0 ** ve).max(1, keepdims=True)
+        # a weight (times 2^exponent) is off by 2^-11 of itself or up to 2^-30 of the row's largest, evenly: 2^-30.8 in the mean square, times
+        # codes of 90 in the mean square (448 x 2^-2.3); six times that, summed over the row, is below half of the last term;
+        # scores in fp32 by less than 2^-14
+        bound = 2.0 ** -8 * np.abs(o) + (2.0 ** -11 + 2.0 ** -13) * (w @ np.abs(v)) + 6 * math.sqrt(len(v)) * 2.0 ** -32 * top * 448
+        err = np.abs(got[t, h] - o)[:, half:]
+        assert (err <= bound[:, half:] + 1e-30).all(), (t[0], h, float((err / (bound[:, half:] + 1e-30)).max()))
