@@ -2,7 +2,7 @@
 under the same names.
 
 Argument marshalling only, as in ``moe``: tensors are passed as device
-pointers, the stream is torch's current stream unless one is given, a nonzero
+pointers, all of a call's on one device, the stream is torch's current stream of that device unless one is given, a nonzero
 status raises ``moe.MoEError``, and the workspace is a uint8 CUDA tensor that is
 zero-filled or passed through ``moe.moe_workspace_init`` once.  The tensors are checked (type, device,
 layout, shape: ``ValueError``) in ``_attn_native.so`` (csrc/binding.cpp), which passes their addresses

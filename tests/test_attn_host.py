@@ -191,3 +191,41 @@ def test_binding_refuses_what_is_not_on_the_gpu(L):
         attn.moe_kv_build_tables(i32, i32, 16, i32, i32, i32, i32, i32, i32, i32, i32, u8)
     with pytest.raises(ValueError, match="expected 6 arguments"):
         attn._native().linear_fp8(u8)
+
+
+def test_binding_refuses_tensors_of_two_devices(L):
+    """All of a call's tensors are on one device (stand-ins without memory: nothing is launched)."""
+    torch = pytest.importorskip("torch")
+    fake = pytest.importorskip("torch._subclasses.fake_tensor")
+    if torch.cuda.is_available():
+        pytest.skip("stand-ins for a second device need a machine without the first")
+    with fake.FakeTensorMode():
+        def u8(*shape, device="cuda:0"):
+            return torch.empty(shape, dtype=torch.uint8, device=device)
+        k, v, scale = (2, 1, 1, 4, 16, 16), (2, 1, 1, 64, 16), (2, 1)
+        cache = attn.KVCache(u8(*k), u8(*v), u8(*scale), u8(*scale))
+        for i in range(1, 4):
+            parts = [u8(*shape, device="cuda:1" if j == i else "cuda:0") for j, shape in enumerate((k, v, scale, scale))]
+            with pytest.raises(ValueError, match=f"{('k', 'v', 'k_scale', 'v_scale')[i]}: expected a tensor on cuda:0 as k, got cuda:1"):
+                attn.KVCache(*parts)
+        weight = attn.FP8Weight(u8(16, 16), u8(1, 1))
+        with pytest.raises(ValueError, match="scale: expected a tensor on cuda:0 as codes"):
+            attn.FP8Weight(u8(16, 16), u8(1, 1, device="cuda:1"))
+
+        def bf16(*shape, device="cuda:0"):
+            return torch.empty(shape, dtype=torch.bfloat16, device=device)
+        i32 = [torch.empty(1, dtype=torch.int32, device=d) for d in ("cuda:0", "cuda:1")]
+        i64 = [torch.empty(1, dtype=torch.int64, device=d) for d in ("cuda:0", "cuda:1")]
+        calls = [("ws", lambda: attn.moe_linear_fp8(bf16(1, 16), weight, bf16(1, 16), u8(512, device="cuda:1"))),
+                 ("y", lambda: attn.moe_linear_fp8(bf16(1, 16), weight, bf16(1, 16, device="cuda:1"), u8(512))),
+                 ("codes", lambda: attn.moe_quantize_fp8_weight(bf16(16, 16, device="cuda:1"), weight)),
+                 ("slot_map", lambda: attn.moe_kv_append(bf16(1, 1, 64), bf16(1, 1, 64), i64[1], cache, u8(512))),
+                 ("q", lambda: attn.moe_kv_attention(bf16(1, 1, 64, device="cuda:1"), cache, i32[0].view(1, 1), i32[0], i32[0], 1.0, bf16(1, 1, 64),
+                                                     None, u8(512))),
+                 ("kv_lens", lambda: attn.moe_kv_attention(bf16(1, 1, 64), cache, i32[0].view(1, 1), i32[0], i32[1], 1.0, bf16(1, 1, 64), None,
+                                                           u8(512))),
+                 ("new_lens", lambda: attn.moe_kv_build_tables(i32[0], i32[1], 16, i32[0], i32[0], i32[0].view(1, 1), i32[0], i32[0], i64[0], i32[0],
+                                                               i32[0], u8(512)))]
+        for name, call in calls:
+            with pytest.raises(ValueError, match=f"{name}: expected a tensor on cuda:"):
+                call()
