@@ -690,6 +690,8 @@ __device__ __forceinline__ void finish(const AttnArgs &a, const Piece &pc, uint8
                 o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
                 if (pieces == 1) {
                     const int r = pc.row0 + row;
+                    if (!MOE_DBG_IN_RANGE(pc.q0 + r / a.group, p.T, a.hdr))
+                        continue;
                     const size_t at = (size_t)(pc.q0 + r / a.group) * p.q_heads + pc.head * a.group + r % a.group;
                     uint32_t x, y;
                     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(o.y), "f"(o.x));
@@ -697,7 +699,7 @@ __device__ __forceinline__ void finish(const AttnArgs &a, const Piece &pc, uint8
                     *reinterpret_cast<uint2 *>(p.out + at * D + d) = make_uint2(x, y);
                     if (d == 0 && p.lse)
                         p.lse[at] = l == 0.0f ? -INFINITY : (mz + log2f(l)) * 0.69314718055994530942f;
-                } else {
+                } else if (MOE_DBG_IN_RANGE(slot, 2 * a.ctas, a.hdr) && MOE_DBG_IN_RANGE(row, a.part_rows, a.hdr)) {
                     __stcg(reinterpret_cast<float4 *>(a.part + ((size_t)slot * a.part_rows + row) * D + d), o);
                     if (d == 0)
                         __stcg(a.part_sum + (size_t)slot * a.part_rows + row, make_float2(m, l * 0x1p-31f));   // no number of tokens brings that past 1
@@ -709,7 +711,7 @@ __device__ __forceinline__ void finish(const AttnArgs &a, const Piece &pc, uint8
         named_barrier_sync(1, kConsumers * 32);
         if (tid == 0) {
             __threadfence();
-            const bool last = atomicAdd(a.tickets + pc.first, 1u) == (uint32_t)(pieces - 1);
+            const bool last = MOE_DBG_IN_RANGE(pc.first, a.ctas, a.hdr) && atomicAdd(a.tickets + pc.first, 1u) == (uint32_t)(pieces - 1);
             if (last)
                 a.tickets[pc.first] = 0;              // for the next call
             *s_last = last;
@@ -729,8 +731,9 @@ __device__ __forceinline__ void finish(const AttnArgs &a, const Piece &pc, uint8
                     for (int u = 0; u < U; ++u) {
                         const int k = k0 + u;
                         const size_t at = ((size_t)(pc.first + k) * 2 + (k == 0)) * a.part_rows + row;
-                        e[u] = k < pieces ? __ldcg(a.part_sum + at) : make_float2(-INFINITY, 0.0f);
-                        v[u] = k < pieces ? __ldcg(reinterpret_cast<const float4 *>(a.part + at * D + d)) : make_float4(0, 0, 0, 0);
+                        const bool is = k < pieces && MOE_DBG_IN_RANGE(at, 2ll * a.ctas * a.part_rows, a.hdr);
+                        e[u] = is ? __ldcg(a.part_sum + at) : make_float2(-INFINITY, 0.0f);
+                        v[u] = is ? __ldcg(reinterpret_cast<const float4 *>(a.part + at * D + d)) : make_float4(0, 0, 0, 0);
                     }
                     float nm = m;
 #pragma unroll

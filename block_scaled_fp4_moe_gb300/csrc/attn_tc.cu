@@ -924,6 +924,8 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
                 if (bad >> e & 1)
                     x[e] = __uint_as_float(0x7FFFFFFFu);
             if (live && w.count == 1) {
+                if (!MOE_DBG_IN_RANGE(pc.q0 + row / a.group, p.T, a.hdr))
+                    continue;
 #pragma unroll
                 for (int e = 0; e < 32; e += 8) {
                     uint32_t v[4];
@@ -934,7 +936,7 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
                     dst[0] = make_uint2(v[0], v[1]);
                     dst[1] = make_uint2(v[2], v[3]);
                 }
-            } else if (live) {
+            } else if (live && MOE_DBG_IN_RANGE(w.slot, 4 * a.ctas, a.hdr) && MOE_DBG_IN_RANGE(tid, cap, a.hdr)) {
                 // [dim / 4][row][4]: a warp's stores lie together
                 float4 *dst = reinterpret_cast<float4 *>(a.part + (size_t)w.slot * cap * D) + (size_t)8 * c * cap + tid;
 #pragma unroll
@@ -956,7 +958,7 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
         if (live && w.count == 1) {
             if (p.lse && (!both || h == 0))
                 p.lse[to] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
-        } else if (live) {
+        } else if (live && MOE_DBG_IN_RANGE(w.slot, 4 * a.ctas, a.hdr) && MOE_DBG_IN_RANGE(tid, cap, a.hdr)) {
             __stcg(a.part_sum + (size_t)w.slot * cap + tid, make_float2(m, l));
         }
         if (w.count > 1) {
@@ -964,7 +966,7 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
             named_barrier_sync(1 + h, 128);
             if (tid == 0) {
                 __threadfence();
-                const bool last = atomicAdd(a.tickets + w.ticket, 1u) == (uint32_t)(w.count - 1);
+                const bool last = MOE_DBG_IN_RANGE(w.ticket, 2 * a.ctas, a.hdr) && atomicAdd(a.tickets + w.ticket, 1u) == (uint32_t)(w.count - 1);
                 if (last)
                     a.tickets[w.ticket] = 0;       // for the next call
                 s_last[h] = last;
@@ -978,7 +980,8 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
                 const int parts = pair ? ctas : 2 * ctas;
                 auto slot_of = [&](int k) {        // -1: the part does not exist
                     const int c = pair ? k : k >> 1, g = pair ? h : k & 1;
-                    return k < parts && (pair || g == 0 || has_two(c)) ? ((pc.first + c) * 2 + (c == 0)) * 2 + g : -1;
+                    const int slot = ((pc.first + c) * 2 + (c == 0)) * 2 + g;
+                    return k < parts && (pair || g == 0 || has_two(c)) && MOE_DBG_IN_RANGE(slot, 4 * a.ctas, a.hdr) ? slot : -1;
                 };
                 constexpr int U = 4;
                 for (int i = tid; i < rows_here * (D / 16); i += 128) {

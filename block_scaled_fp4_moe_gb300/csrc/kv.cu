@@ -122,12 +122,15 @@ __global__ void __launch_bounds__(kTablesThreads) kv_tables_kernel(TablesProblem
                 hi = mid;
         }
         const int c = s_ctx[lo], pos = c + t - s_off[lo], idx = pos >> sh, held = before(c);
+        const int taken = head + s_blk[lo] + idx - held;        // place in the free list of a block that is new
+        if (!MOE_DBG_IN_RANGE(idx, p.max_blocks, p.hdr) || (idx >= held && !MOE_DBG_IN_RANGE(taken, p.num_free, p.hdr)))
+            continue;
         int32_t *entry = p.table + (size_t)lo * p.max_blocks + idx;
         int id;
         if (idx < held) {
             id = *entry;
         } else {
-            id = p.free_blocks[head + s_blk[lo] + idx - held];
+            id = p.free_blocks[taken];
             if ((pos & (bs - 1)) == 0)
                 *entry = id;
         }
@@ -141,6 +144,9 @@ __global__ void __launch_bounds__(kTablesThreads) kv_tables_kernel(TablesProblem
 constexpr int kAppendThreads = 256, kAppendWarps = kAppendThreads / 32;
 constexpr int kAppendWindow = 32;       // tokens a CTA looks at, at most
 constexpr int kShortRun = 4;            // tokens of a run that one warp appends
+#ifdef MOE_DEBUG_BOUNDS
+constexpr int kLookBack = 128;          // skipped tokens over which a run's predecessor is looked for
+#endif
 
 // 16 codes of a block whose exponent grew, rounded to the new one (f = 2^-growth);
 // the first `held` of them are the block's, the rest stays as it is.
@@ -233,6 +239,25 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(AppendProb
     if (here >= 0) {
         const int64_t prev = s_slot[lane];
         begins = prev < 0 || (prev >> sh) != (here >> sh);
+#ifdef MOE_DEBUG_BOUNDS
+        // What the caller must not do (a look at it costs a decode step's append a tenth of its time): a block's tokens that do not follow one
+        // another in it, or go on behind skipped ones, where another warp settles the block's scale already.
+        bool apart = !begins && here != prev + 1;
+        if (prev < 0) {
+            int64_t last = -1;
+            for (int t = t0 + lane - 1, left = kLookBack; last < 0 && t > 0 && left > 0; --left) {
+                last = p.slots[--t];
+                if (last >= n_slots)
+                    last = -1;
+            }
+            if (last >= 0 && (last >> sh) == (here >> sh)) {
+                begins = false;
+                apart = true;
+            }
+        }
+        if (apart)
+            record_status(p.hdr, MOE_ERR_DEVICE_ASSERT);
+#endif
         brief = bs - (int)(here & (bs - 1)) <= kShortRun;
 #pragma unroll
         for (int j = 1; j <= kShortRun; ++j)            // kShortRun < bs: within s_slot

@@ -86,7 +86,7 @@ moe_status_t moe_kv_build_tables(const int32_t *ctx_lens, const int32_t *new_len
  * t * stride_t + h * stride_h + i, strides in elements and multiples of 8,
  * pointers 16-byte aligned) into the cache at slot_map [T] (as moe_kv_build_tables makes
  * it: the tokens of a block follow one another in slot_map, with no other slot
- * between them, and in the block; a negative slot is skipped).  Each (block, head) has one exponent for its keys
+ * between them, and in the block; a negative slot is skipped; the range-checked build reports slots that break this).  Each (block, head) has one exponent for its keys
  * and one for its values.  A token at offset 0 starts the block anew.  Where
  * the block holds earlier tokens, its exponent becomes the larger of its own and
  * what the new tokens need, and if it grew the earlier tokens' codes are

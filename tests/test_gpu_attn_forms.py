@@ -9,7 +9,7 @@ import torch
 
 import attn_reference as ref
 import test_gpu_attn as base
-from block_scaled_fp4_moe_gb300 import attn
+from block_scaled_fp4_moe_gb300 import _build, attn, moe
 
 pytestmark = pytest.mark.gpu
 built = base.built
@@ -160,3 +160,58 @@ def test_linear_persistent_form_goes_round_its_ring_and_accumulators(T, N, K, tm
 @pytest.mark.parametrize("N,K", [(1001, 4112), (7003, 1040)])
 def test_linear_split_forms_go_round_their_rings(T, tile, fused, N, K, tmp_path):
     check_linear(T, N, K, T, tmp_path, tile, True, fused)
+
+
+# ------------------------------------------- the build with range checks
+
+@pytest.fixture
+def debug():
+    _build.build(debug=True)
+    with moe.debug_bounds():
+        yield
+
+
+@pytest.mark.parametrize("kv_heads,group,dim,lens", [
+    (2, 4, 64, [(1, 700), (3, 200), (0, 5), (1, 1)]), (1, 8, 128, [(1, 9000)]), (2, 8, 128, [(4, 900), (3, 40)]), (2, 8, 64, [(8, 5000), (7, 30)]),
+    (1, 2, 64, [(1, 1 + i % 140) for i in range(300)]), (8, 4, 64, [(9, 700), (20, 300), (40, 200), (8, 90)]),
+    (8, 8, 128, [(40, 5000), (9, 300), (70, 260), (12, 130)]), (8, 4, 128, [(8, 9000)] + [(8, 150 + 70 * i) for i in range(9)])])
+def test_attention_under_range_checks(kv_heads, group, dim, lens, debug):
+    """Rows, parts of cut units and their tickets stay in their ranges, in every form."""
+    base.Problem(lens, kv_heads, group, dim, 32, seed=67).check()
+    base.Problem(lens, kv_heads, group, dim, 16, seed=68).check(window=150)
+
+
+def test_a_step_under_range_checks(debug):
+    base.test_step_against_the_reference()
+    base.test_tables_match_the_definition(65, 32, 300, 40, 0)
+    for T in (1, 40, 300):
+        base.test_linear_token_counts(T)
+
+
+@pytest.mark.parametrize("T,gap", [(40, 1), (40, 3), (40, 40), (40, 127), (1500, 1), (1500, 100)])
+def test_append_that_goes_on_with_a_block_behind_skipped_tokens(T, gap, debug):
+    """Two runs of one block would settle its scale beside one another, which slot_map must not ask for: the range-checked build leaves the
+    second out, and reports it."""
+    cache, g, mirror, k, v, slots = append_case([T + gap + 300], [0], 2, 64, 64, seed=65)
+    k, v, slots = k[:len(slots)], v[:len(slots)], slots.copy()
+    at = T // 64 * 64 + 7                                  # inside a block
+    slots[at:at + gap] = -1
+    end = (at // 64 + 1) * 64
+    ws = base.workspace(512)
+    attn.moe_kv_append(k, v, torch.from_numpy(slots).cuda(), cache, ws)
+    late = at + gap < end                                  # something of the block is left behind the gap
+    assert base.status(ws) == (moe.MOE_ERR_DEVICE_ASSERT if late else 0)
+    if late:
+        slots[at + gap:end] = -1
+    mirror.append(base.f64(k), base.f64(v), slots)
+    base.check_cache(g, mirror)
+
+
+def test_append_that_jumps_inside_a_block_is_reported(debug):
+    for slots in ([0, 2], [5, 4], [7, 7]):
+        cache, g, mirror, k, v, _ = append_case([2], [0], 1, 64, 64, seed=66)
+        ws = base.workspace(512)
+        attn.moe_kv_append(k[:2], v[:2], torch.tensor(slots).cuda(), cache, ws)
+        assert base.status(ws) == moe.MOE_ERR_DEVICE_ASSERT
+        for x in g:
+            x.check()
