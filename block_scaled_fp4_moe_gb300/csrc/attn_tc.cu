@@ -778,9 +778,11 @@ __device__ __forceinline__ void tc_softmax(const AttnArgs &a, const Plan &pl, ui
         __syncwarp();
         if (lane == 0 && mine > 0)
             mbar_arrive(b.q_ready + h);
-        int lo = 0, hi = pc.kv;
-        if (live)
-            row_range(p, a.group, pc.kv, pc.n, row, lo, hi);
+        // a lane without a row sees from the first row's first position on: what lies before is not read, and it has a vote in its warp
+        int lo, hi;
+        row_range(p, a.group, pc.kv, pc.n, row, lo, hi);
+        if (!live)
+            hi = pc.kv;
         const int min_hi = __reduce_min_sync(0xffffffffu, hi), max_lo = __reduce_max_sync(0xffffffffu, lo);
 
         Refs refs{-INFINITY, -INFINITY, 0.0f};

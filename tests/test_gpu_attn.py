@@ -874,3 +874,23 @@ def test_linear_behind_a_kernel_that_runs_for_long(T, tmp_path):
     attn.moe_linear_fp8(xt, weight, y, ws)
     torch.cuda.synchronize()
     assert status(ws) == 0 and torch.equal(y, want)
+
+
+@pytest.mark.parametrize("dim,group,new", [(64, 4, 9), (128, 4, 9), (128, 20, 13), (64, 5, 1), (128, 8, 3)])
+def test_attention_with_a_window_does_not_depend_on_other_requests(dim, group, new):
+    """Every other request's keys are NaN, or not: where a tile begins with blocks that are not read, what the CTA read before lies there, and has no
+    part in the bits.  (A window's first tile has larger keys and smaller values than the others: the references of rows with tokens stay, those of
+    the unit's rows without, whose scores are zero, would not.)"""
+    window, lens = 425, [(new, 600 + 37 * (i % 12)) for i in range(300)]
+    p = Problem(lens, 1, group, dim, 16, seed=69, exps=(-7, -7))
+    p.cache.ve[:] = 2
+    for row, (n, kv) in zip(p.table, lens):
+        first = row[: ((kv - n - window + 1) // 128 + 1) * 8]
+        p.cache.ke[first], p.cache.ve[first] = -5, -8
+    want, want_lse = p.run(window=window)
+    assert p.status == 0
+    p.cache.k[p.table[::2, : 600 // 16]] = 0x7F
+    out, lse = p.run(window=window)
+    assert p.status == 0
+    t = torch.arange(p.T, device="cuda") // new % 2 == 1
+    assert bool(torch.isnan(lse[~t]).all()) and torch.equal(out[t], want[t]) and torch.equal(lse[t], want_lse[t])
