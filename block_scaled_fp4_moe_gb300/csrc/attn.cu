@@ -42,10 +42,10 @@
 // 4c .. 4c+3, as K positions 2c, 2c+1, 2c+8, 2c+9: q's dims (and, for the
 // values, the weights' tokens) are taken in that order.
 //
-// Measured, key/value heads of 128: 64 requests of 31,000 tokens, 8 heads with 8 query heads each, 586 us (6.7 TB/s, the rate of a copy: bound by
+// Measured, key/value heads of 128: 64 requests of 31,000 tokens, 8 heads with 8 query heads each, 592 us (6.67 TB/s of the 6.78 of a copy: bound by
 // memory); 48 ragged requests of 5,000 in blocks of 16, 102 us (5.2 TB/s: a request's first tiles and last join are a larger part);
-// one of 1,000, 9.8 us (launch, plan, block ids, tiles, join: latency).  24 rows a request run at 3.5 TB/s and 32
-// at 3.2, bound by the chain of products and powers in eight warps.
+// one of 1,000, 9.8 us (launch, plan, block ids, tiles, join: latency).  24 rows a request run at 3.6 TB/s and 32
+// at 3.5, bound by the chain of products and powers in eight warps.
 #include "attn_plan.cuh"
 
 namespace moe {
@@ -892,10 +892,10 @@ cudaError_t launch_kv_attention(const AttnProblem &p, void *ws, int sms, cudaStr
                ws_at<uint32_t>(ws, kHeaderBytes), ws_at<float>(ws, L.part), ws_at<float2>(ws, L.part_sum),
                ws_at<uint8_t>(ws, L.nans), ws_at<uint32_t>(ws, 0)};
     // The tensor-memory form where requests have more than 24 rows on average (us of it and of this one: 16 requests of
-    // 1..4 tokens x 12 heads of a group 143 and 175, 32 of 10 x 4 rows 157 and 191; of 1..3 x 8 154 and 105; requests of 32 rows
-    // each, 153 and 112, are the price of telling them from ragged ones by the average alone) and there are units enough
-    // that its longer way from a unit's start to its end does not show (16 x 8 rows of four requests over 20,000 tokens 93
-    // and 99, of two 89 and 77).
+    // 1..4 tokens x 12 heads of a group 144 and 177, 32 of 1..10 x 4 rows 158 and 196; of 1..3 x 8 141 and 97; requests of 32 rows
+    // each, 143 and 99, are the price of telling them from ragged ones by the average alone) and there are units enough
+    // that its longer way from a unit's start to its end does not show (16 x 8 rows of four requests over 20,000 tokens 106
+    // and 110, of two 114 and 74).
     const long long rows = (long long)p.T * group, units = ((rows + kAttnTcRows - 1) / kAttnTcRows + p.B - 1) * p.cache.kv_heads;
     const bool tall = rows > (long long)kAttnTcMinRows * p.B && units >= 32;
     auto go = [&](auto kernel, size_t smem) {

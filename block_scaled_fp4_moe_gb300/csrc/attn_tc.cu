@@ -19,10 +19,11 @@
 // 15 issues the MMAs.  (Two threads to a row, 16 warps of at most 88 registers, took as long: more latency hidden, more moves
 // and exchanges.)
 //
-// Measured: three requests' chunks of 500 tokens over 9,000, 48 query heads of 64, 148 us (558 TFLOP/s), bound by the issue of the softmax (a
-// pass for the maxima before the weights: 165; four such tiles unrolled: 180); chunks of 600 over 16,000, 40 heads of 128, 490 us (880 TFLOP/s),
+// Measured: three requests' chunks of 500 tokens over 9,000, 48 query heads of 64, 151 us (548 TFLOP/s): nine instructions a score, all roles together,
+// in half of the issue slots (a pass for the maxima before the weights: 165; four such tiles unrolled: 180); the special-function pipe is
+// busy a quarter of the time, the tensor pipe too.  Chunks of up to 600 over up to 16,000, 40 heads of 128, 341 us (857 TFLOP/s),
 // where shared memory, read and written for codes, operands and products, is busy three quarters of the time; 16 requests of up to 48 rows
-// over 10,000 tokens 143 us, bound by a tile's way through conversion, product, softmax and product with few rows.
+// over 10,000 tokens 145 us, bound by a tile's way through conversion, product, softmax and product with few rows.
 //
 // The operands pass in the order K0, K1, V0, K2, V1, ...: as codes into a ring of raw tiles
 // by bulk copies, then as f16 into a ring of operand tiles, rows (tokens of K, dims of V) of 64

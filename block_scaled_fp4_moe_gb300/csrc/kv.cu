@@ -203,7 +203,7 @@ __device__ __forceinline__ void recode_block(uint8_t *codes, bool is_v, int off0
 // Bound: latency, of the chain slots -> input -> exponent -> codes.  64 requests of
 // one token (8 heads of 128) take 3.4 us, 256 take 6.6 and 400 take 8.6; with a CTA for
 // every run they took 5.8, 17.4 and 26.6, since few CTAs fit an SM.  5,000 prompt tokens in blocks of
-// 64 take 16 us (2.0 TB/s in and out); four CTAs an SM at 64 registers are ahead of three (22 us)
+// 64 take 15.1 us (2.1 TB/s in and out); four CTAs an SM at 64 registers are ahead of three (22 us)
 // and of five that spill (20 us).
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(AppendProblem p, int window) {

@@ -22,7 +22,7 @@
 //
 // Measured (W in memory, not in L2): 7168 x 5120 with one token 8.9 us (4.1 TB/s: starting the stream, and the cluster's join, are a
 // third of it), 7168 x 8192 with 61 tokens 17.2 us, of which 2.7 quantise x (3.5 TB/s); 7168 x 5120 with 4,000 tokens 148 us, of which
-// 10 quantise x (1.98 PFLOP/s).  Many tokens are bound by shared memory: a stage of 128 x 192 x 128 is written to it and read from it in
+// 10 quantise x (1.99 PFLOP/s).  Weights are quantised at 4.8 TB/s (7168 x 5120 in 23 us; 16 at the rate of a copy).  Many tokens are bound by shared memory: a stage of 128 x 192 x 128 is written to it and read from it in
 // about 640 cycles and multiplied in 408, and no more than four fit.
 #include <cuda.h>
 
