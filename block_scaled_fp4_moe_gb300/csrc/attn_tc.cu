@@ -32,13 +32,13 @@
 //
 // The running maxima of a row are references that move only where scores have outgrown them (16 weights sum to more than
 // f16 holds; its rounding is relative).  A largest weight is 2^6 when they have moved, so that 20 binades below it keep their bits
-// (2^8, with less room to grow, takes 161 us for 152 on the first case below; 2^0 to 2^6 the same).  So a score is read once: 32 of a row at a time become weights,
+// (2^8, with less room to grow, takes 161 us for 152 on the first case above; 2^0 to 2^6 the same).  So a score is read once: 32 of a row at a time become weights,
 // whose sums say whether they fit.  Where they do not, the references move to the maxima (of the tile, or of the 32 where the
 // weights lie over the scores), the half waits for its last product and rescales O, and the tile's weights so far, in TMEM; then
 // the weights are made, and not looked at again.  Only a unit's first tile is read for its maxima first.
 //
 // The reference of the weights is kept relative to that of l (rel = M - m) and moves by whole powers of two: weights stored already
-// lose nothing to it, and it has all its bits however large the scores are.  A weight's power is fma(y, fi, -m), the
+// lose nothing to it but what falls below f16, and it has all its bits however large the scores are.  A weight's power is fma(y, fi, -m), the
 // product exact; m, rounded, may lie under it by half of its last place.  Past kFar that would matter (half a place of 2^28 is a
 // factor of 2^16).  There, and wherever the references have just moved, the product is rounded as m was before m is
 // taken from it, so that no power is above zero, and every tile is read for its maxima first.
