@@ -238,7 +238,8 @@ def describe(cfg):
 PER_CONFIG = ("glm_verify_t4", "glm_verify_t16", "1t_t1", "1t_t4")
 
 
-ATTENTION_SOURCES = {"attn.cu", "attn.h", "attn_capi.cu", "attn_plan.cuh", "attn_tc.cu", "kv.cu", "linear.cu"}
+ATTENTION_SOURCES = {"attn.cu", "attn.h", "attn_capi.cu", "attn_plan.cuh", "attn_tc.cu", "kv.cu", "latent.cu", "linear.cu", "norm.cu",
+                     "rotary.cu"}
 
 
 def kernel_source_digest() -> str:

@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes as C
 import importlib.util
+import math
 import os
 
 import torch
@@ -29,6 +30,10 @@ class _Cache(C.Structure):
                 ("num_blocks", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32), ("block_size", C.c_int32)]
 
 
+class _LatentCache(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("num_blocks", C.c_int32), ("latent_dim", C.c_int32), ("block_size", C.c_int32)]
+
+
 _p, _i, _l, _s, _f = C.c_void_p, C.c_int, C.c_int64, C.c_size_t, C.c_float
 _SIG = {
     "moe_kv_build_tables": (_i, [_p, _p, _i, _i, _i, _p, _i, _p, _p, _i, _p, _p, _p, _p, _p, _p, _s, _p]),
@@ -38,6 +43,11 @@ _SIG = {
     "moe_quantize_fp8_weight": (_i, [_p, _i, _i, _p, _p, _p]),
     "moe_linear_fp8_workspace_size": (_s, [_i, _i, _i]),
     "moe_linear_fp8": (_i, [_p, _l, _i, _p, _p, _i, _i, _p, _p, _s, _p]),
+    "moe_rms_norm": (_i, [_p, _l, _i, _i, _p, _p, _l, _f, _p, _p, _i, _p, _f, _p, _p]),
+    "moe_rotary": (_i, [_p, _l, _l, _p, _l, _l, _i, _p, _l, _l, _p, _l, _l, _i, _i, _i, _p, _p, _i, _f, _i, _i, _p, _p, _f, _p]),
+    "moe_latent_append": (_i, [_p, _l, _p, _l, _p, _i, _p, _p, _f, _i, _p, _f, C.POINTER(_LatentCache), _p, _s, _p]),
+    "moe_latent_attention_workspace_size": (_s, [_i, _i, _i, _i]),
+    "moe_latent_attention": (_i, [_p, _l, _l, _p, _l, _l, _i, _i, C.POINTER(_LatentCache), _p, _i, _p, _p, _i, _f, _i, _p, _p, _p, _s, _p]),
 }
 _ready: dict[int, C.CDLL] = {}
 
@@ -76,7 +86,7 @@ def _native():
         lib()
         _native_module.set_library(*[C.cast(getattr(L, name), C.c_void_p).value for name in
                                      ("moe_kv_build_tables", "moe_kv_append", "moe_kv_attention", "moe_quantize_fp8_weight",
-                                      "moe_linear_fp8")])
+                                      "moe_linear_fp8", "moe_rms_norm", "moe_rotary", "moe_latent_append", "moe_latent_attention")])
         _bound = id(L)
     return _native_module
 
@@ -149,12 +159,83 @@ class FP8Weight:
         return out
 
 
-def alloc_workspace(max_tokens: int, max_requests: int, q_heads: int, cache: KVCache, weights=()) -> torch.Tensor:
-    """A workspace for steps of up to these sizes: the attention's and, for
+class LatentCache:
+    """The paged cache of latent vectors: data bf16 [num_blocks, block_size, latent_dim + 64], a token's latent vector and
+    rotary key side by side."""
+    __slots__ = ("data",)
+
+    def __init__(self, data: torch.Tensor):
+        _native().check_latent_cache(data)
+        self.data = data
+
+    @property
+    def num_blocks(self) -> int:
+        return self.data.shape[0]
+
+    @property
+    def block_size(self) -> int:
+        return self.data.shape[1]
+
+    @property
+    def latent_dim(self) -> int:
+        return self.data.shape[2] - 64
+
+    @staticmethod
+    def empty(num_blocks: int, latent_dim: int, block_size: int, device="cuda") -> "LatentCache":
+        """A cache whose blocks hold nothing yet (its memory is not cleared)."""
+        return LatentCache(torch.empty((num_blocks, block_size, latent_dim + 64), dtype=torch.bfloat16, device=device))
+
+
+class RotaryTable:
+    """Frequencies of the rotated pairs: turns int64 [pairs], in units of 2^-64 turns a position (the bits of the unsigned
+    number), and the factor of cosines and sines."""
+    __slots__ = ("turns", "amplitude")
+
+    def __init__(self, turns: torch.Tensor, amplitude: float = 1.0):
+        self.turns, self.amplitude = turns, amplitude
+
+    @staticmethod
+    def make(dims: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0, original_len: int = 0, fast: float = 32.0,
+             slow: float = 1.0, amplitude: float | None = None, device="cuda") -> "RotaryTable":
+        """A table for ``dims`` rotated dims: pair i turns by base^(-2 i / dims) radians a position.  For contexts ``factor`` times
+        as long as a model was trained on, ``scaling`` is "linear" (all frequencies divided by it), "base" (the base enlarged so that the
+        slowest pair's is), or "parts" (pairs that turn ``fast`` times or more in ``original_len`` positions as they are, those that
+        turn ``slow`` times or fewer divided, linearly in the turns between; the amplitude is 0.1 ln(factor) + 1 unless one is given)."""
+        if dims <= 0 or dims % 2 or not base > 0 or not (factor > 0 and math.isfinite(factor)):
+            raise ValueError(f"dims {dims}, base {base}, factor {factor}: expected an even number and positive ones")
+        if scaling not in (None, "linear", "base", "parts"):
+            raise ValueError(f"scaling: expected linear, base or parts, got {scaling!r}")
+        if scaling is None and factor != 1.0:
+            raise ValueError("factor: expected with a scaling only")
+        if scaling == "parts" and not (original_len > 0 and fast > slow >= 0):
+            raise ValueError("scaling by parts: expected original_len > 0 and fast > slow >= 0")
+        if scaling == "base":
+            if dims < 4:
+                raise ValueError("scaling of the base: expected two pairs or more")
+            base *= factor ** (dims / (dims - 2))
+        turns = []
+        for i in range(dims // 2):
+            f = base ** (-2 * i / dims)
+            if scaling == "linear":
+                f /= factor
+            elif scaling == "parts":
+                keep = min(max((original_len * f / (2 * math.pi) - slow) / (fast - slow), 0.0), 1.0)
+                f = f * keep + f / factor * (1 - keep)
+            whole = round(f / (2 * math.pi) * 2.0 ** 64) % (1 << 64)
+            turns.append(whole - (1 << 64) if whole >> 63 else whole)
+        if amplitude is None:
+            amplitude = 0.1 * math.log(factor) + 1 if scaling == "parts" and factor > 1 else 1.0
+        return RotaryTable(torch.tensor(turns, dtype=torch.int64, device=device), amplitude)
+
+
+def alloc_workspace(max_tokens: int, max_requests: int, q_heads: int, cache: KVCache | LatentCache, weights=()) -> torch.Tensor:
+    """A workspace for steps of up to these sizes: the attention's over this cache and, for
     ``weights`` (FP8Weight), the projections'."""
-    n = max([512, moe_kv_attention_workspace_size(max_tokens, max_requests, q_heads, cache.kv_heads, cache.head_dim)] +
+    latent = isinstance(cache, LatentCache)
+    n = max([512, moe_latent_attention_workspace_size(max_tokens, max_requests, q_heads, cache.latent_dim) if latent else
+             moe_kv_attention_workspace_size(max_tokens, max_requests, q_heads, cache.kv_heads, cache.head_dim)] +
             [moe_linear_fp8_workspace_size(max_tokens, *w.codes.shape) for w in weights])
-    ws = torch.empty(n, dtype=torch.uint8, device=cache.k.device)
+    ws = torch.empty(n, dtype=torch.uint8, device=cache.data.device if latent else cache.k.device)
     with torch.cuda.device(ws.device):
         moe.moe_workspace_init(ws)
     return ws
@@ -204,3 +285,44 @@ def moe_linear_fp8(x, w: FP8Weight, y, ws, stream=None):
     st = _native().linear_fp8(x, w.codes, w.scale, y, ws, _stream(stream))
     if st:
         raise moe.MoEError(st, "moe_linear_fp8")
+
+
+def moe_rms_norm(x, weight, eps, y, residual=None, residual_out=None, post_weight=None, gate=None, scale=1.0, stream=None):
+    """x bf16 [T, H], rows may lie further apart than H; residual and residual_out bf16 or fp32 [T, H]; gate bf16 [H] or [T, H];
+    weight and y may be None where residual_out is given."""
+    st = _native().rms_norm(x, weight, eps, y, residual, residual_out, post_weight, gate, scale, _stream(stream))
+    if st:
+        raise moe.MoEError(st, "moe_rms_norm")
+
+
+def moe_rotary(q, positions, table: RotaryTable, q_out, k=None, k_out=None, interleaved=False, offset=0, q_norm=None, k_norm=None,
+               eps=1e-6, stream=None):
+    """q, k bf16 [T, heads, head_dim] (strided views are taken as they are); q_out and k_out may be q and k."""
+    st = _native().rotary(q, positions, table.turns, table.amplitude, q_out, k, k_out, interleaved, offset, q_norm, k_norm, eps,
+                          _stream(stream))
+    if st:
+        raise moe.MoEError(st, "moe_rotary")
+
+
+def moe_latent_append(c, k, slot_map, cache: LatentCache, ws, positions=None, table: RotaryTable | None = None, interleaved=False,
+                      norm=None, eps=1e-6, stream=None):
+    """c bf16 [T, latent_dim] and k bf16 [T, 64], rows may lie further apart; k is rotated where positions and a table are given,
+    c normed where norm is."""
+    turns, amplitude = (None, 1.0) if table is None else (table.turns, table.amplitude)
+    st = _native().latent_append(c, k, slot_map, cache.data, ws, positions, turns, amplitude, interleaved, norm, eps, _stream(stream))
+    if st:
+        raise moe.MoEError(st, "moe_latent_append")
+
+
+def moe_latent_attention_workspace_size(T: int, B: int, heads: int, latent_dim: int) -> int:
+    return int(lib().moe_latent_attention_workspace_size(T, B, heads, latent_dim))
+
+
+def moe_latent_attention(q_latent, q_rope, cache: LatentCache, block_table, q_offsets, kv_lens, softmax_scale, out, lse, ws, causal=True,
+                         stream=None):
+    """q_latent bf16 [T, heads, latent_dim] and q_rope bf16 [T, heads, 64] (strided views are taken as they are), out bf16
+    [T, heads, latent_dim], contiguous; lse fp32 [T, heads] or None."""
+    st = _native().latent_attention(q_latent, q_rope, cache.data, block_table, q_offsets, kv_lens, softmax_scale, out, lse, ws, causal,
+                                    _stream(stream))
+    if st:
+        raise moe.MoEError(st, "moe_latent_attention")

@@ -134,4 +134,80 @@ cudaError_t launch_linear_fp8(const LinearProblem &p, void *ws, int sms, cudaStr
 cudaError_t launch_quantize_fp8_weight(const uint16_t *w, int N, int K, uint8_t *codes, uint8_t *scale,
                                        cudaStream_t stream);
 
+constexpr int kRopeDims = 64;           // of the rotary key beside a latent vector
+constexpr int kMaxNormDims = 32768;
+
+struct NormProblem {
+    const uint16_t *x;
+    int64_t ldx;
+    int T, H;
+    const uint16_t *post, *gate;
+    int64_t ld_gate;
+    float scale;
+    const void *residual;
+    void *residual_out;
+    int wide;                            // the residual in fp32
+    const uint16_t *weight;
+    float eps;
+    uint16_t *y;
+};
+cudaError_t launch_rms_norm(const NormProblem &p, int sms, cudaStream_t stream);
+
+struct HeadSet {
+    const uint16_t *in;
+    int64_t st, sh;
+    uint16_t *out;
+    int64_t ost, osh;
+    int heads;
+    const uint16_t *norm;
+};
+struct RotaryProblem {
+    HeadSet q, k;
+    int T, D;
+    const int32_t *positions;
+    const uint64_t *turns;
+    int pairs;
+    float amplitude;
+    int interleaved, offset;
+    float eps;
+};
+cudaError_t launch_rotary(const RotaryProblem &p, int sms, cudaStream_t stream);
+
+struct LatentAppendProblem {
+    const uint16_t *c;
+    int64_t ldc;
+    const uint16_t *k;
+    int64_t ldk;
+    const int64_t *slots;
+    int T;
+    const int32_t *positions;
+    const uint64_t *turns;
+    float amplitude;
+    int interleaved;
+    const uint16_t *norm;
+    float eps;
+    moe_latent_cache_t cache;
+    uint32_t *hdr;
+};
+cudaError_t launch_latent_append(const LatentAppendProblem &p, int sms, cudaStream_t stream);
+
+struct LatentProblem {
+    const uint16_t *ql;
+    int64_t ql_st, ql_sh;
+    const uint16_t *qr;
+    int64_t qr_st, qr_sh;
+    int T, heads;
+    moe_latent_cache_t cache;
+    const int32_t *table;
+    int max_blocks;
+    const int32_t *q_offsets, *kv_lens;
+    int B;
+    float scale;
+    int causal;
+    uint16_t *out;
+    float *lse;
+};
+size_t latent_attention_workspace(int T, int B, int heads, int latent_dim);
+cudaError_t launch_latent_attention(const LatentProblem &p, void *ws, int sms, cudaStream_t stream);
+
 }  // namespace moe

@@ -23,6 +23,10 @@ struct Library {
     decltype(&moe_kv_attention) attention;
     decltype(&moe_quantize_fp8_weight) quantize;
     decltype(&moe_linear_fp8) linear;
+    decltype(&moe_rms_norm) norm;
+    decltype(&moe_rotary) rotary;
+    decltype(&moe_latent_append) latent_append;
+    decltype(&moe_latent_attention) latent_attention;
 } lib;
 
 std::string show(at::IntArrayRef s) {
@@ -159,13 +163,38 @@ void weight_of(const at::Tensor &codes, const at::Tensor &scale) {
     want(scale, {(codes.size(0) + 127) / 128, (codes.size(1) + 127) / 128}, "scale");
 }
 
+// A bf16 vector of n values, or nothing.
+const uint16_t *vector_of(Device &dev, PyObject *o, int64_t n, const char *name) {
+    if (o == Py_None)
+        return nullptr;
+    const at::Tensor &t = whole(dev, o, at::kBFloat16, name);
+    want(t, {n}, name);
+    return at_of<uint16_t>(t);
+}
+
+// A bf16 matrix with contiguous rows.
+const at::Tensor &matrix(Device &dev, PyObject *o, const char *name) {
+    const at::Tensor &t = cuda(dev, o, at::kBFloat16, name);
+    if (t.dim() != 2 || (t.stride(1) != 1 && t.size(1) > 1))
+        fail(name, "expected a matrix with contiguous rows");
+    return t;
+}
+
+// The dims of one latent vector's cache at o.
+moe_latent_cache_t latent_cache_of(Device &dev, PyObject *o) {
+    const at::Tensor &t = whole(dev, o, at::kBFloat16, "cache");
+    if (t.dim() != 3 || t.size(2) <= 64)
+        fail("cache", "expected [blocks, block_size, latent_dim + 64], got " + show(t.sizes()));
+    return moe_latent_cache_t{at_of<uint16_t>(t), narrow(t.size(0), "cache"), narrow(t.size(2) - 64, "cache"), narrow(t.size(1), "cache")};
+}
+
 // The body of a call: counts its arguments and turns what it throws into Python's errors.
 template <typename F>
 PyObject *guarded(Py_ssize_t n, Py_ssize_t expected, const F &body) {
     try {
         if (n != expected)
             throw std::invalid_argument("expected " + std::to_string(expected) + " arguments, got " + std::to_string(n));
-        if (!lib.linear)
+        if (!lib.latent_attention)
             throw std::invalid_argument("set_library() comes first");
         return body();
     } catch (const std::invalid_argument &e) {
@@ -178,12 +207,12 @@ PyObject *guarded(Py_ssize_t n, Py_ssize_t expected, const F &body) {
 }
 
 PyObject *set_library(PyObject *, PyObject *const *o, Py_ssize_t n) {
-    if (n != 5) {
-        PyErr_SetString(PyExc_ValueError, "expected five addresses");
+    if (n != 9) {
+        PyErr_SetString(PyExc_ValueError, "expected nine addresses");
         return nullptr;
     }
-    void *p[5];
-    for (int i = 0; i < 5; ++i) {
+    void *p[9];
+    for (int i = 0; i < 9; ++i) {
         p[i] = PyLong_AsVoidPtr(o[i]);
         if (!p[i]) {
             if (!PyErr_Occurred())
@@ -193,7 +222,9 @@ PyObject *set_library(PyObject *, PyObject *const *o, Py_ssize_t n) {
     }
     lib = Library{reinterpret_cast<decltype(lib.build_tables)>(p[0]), reinterpret_cast<decltype(lib.append)>(p[1]),
                   reinterpret_cast<decltype(lib.attention)>(p[2]), reinterpret_cast<decltype(lib.quantize)>(p[3]),
-                  reinterpret_cast<decltype(lib.linear)>(p[4])};
+                  reinterpret_cast<decltype(lib.linear)>(p[4]), reinterpret_cast<decltype(lib.norm)>(p[5]),
+                  reinterpret_cast<decltype(lib.rotary)>(p[6]), reinterpret_cast<decltype(lib.latent_append)>(p[7]),
+                  reinterpret_cast<decltype(lib.latent_attention)>(p[8])};
     Py_RETURN_NONE;
 }
 
@@ -325,9 +356,156 @@ PyObject *linear_fp8(PyObject *, PyObject *const *o, Py_ssize_t n) {
     });
 }
 
+// (x, weight, eps, y, residual, residual_out, post_weight, gate, scale, stream)
+PyObject *rms_norm(PyObject *, PyObject *const *o, Py_ssize_t n) {
+    return guarded(n, 10, [&] {
+        Device dev;
+        const at::Tensor &x = matrix(dev, o[0], "x");
+        const int64_t T = x.size(0), H = x.size(1);
+        const uint16_t *weight = vector_of(dev, o[1], H, "weight"), *post = vector_of(dev, o[6], H, "post_weight");
+        uint16_t *y = nullptr;
+        if (o[3] != Py_None) {
+            const at::Tensor &t = whole(dev, o[3], at::kBFloat16, "y");
+            want(t, {T, H}, "y");
+            y = at_of<uint16_t>(t);
+        }
+        const at::Tensor *res[2] = {nullptr, nullptr};
+        for (int i = 0; i < 2; ++i) {
+            const char *name = i ? "residual_out" : "residual";
+            if (o[4 + i] == Py_None)
+                continue;
+            const at::ScalarType type = res[0] ? res[0]->scalar_type() : tensor(o[4 + i], name).scalar_type() == at::kFloat ? at::kFloat : at::kBFloat16;
+            res[i] = &whole(dev, o[4 + i], type, name);
+            want(*res[i], {T, H}, name);
+        }
+        const at::Tensor *first = res[0] ? res[0] : res[1];
+        const uint16_t *gate = nullptr;
+        int64_t ld_gate = 0;
+        if (o[7] != Py_None) {
+            const at::Tensor &g = cuda(dev, o[7], at::kBFloat16, "gate");
+            if (g.dim() == 1) {
+                want(g, {H}, "gate");
+                if (g.stride(0) != 1 && H > 1)
+                    fail("gate", "expected contiguous values");
+            } else {
+                matrix(dev, o[7], "gate");
+                want(g, {T, H}, "gate");
+                ld_gate = T > 1 ? g.stride(0) : H;
+            }
+            gate = at_of<uint16_t>(g);
+        }
+        const c10::cuda::CUDAGuard guard(dev.index());
+        return PyLong_FromLong(lib.norm(at_of<uint16_t>(x), T > 1 ? x.stride(0) : H, narrow(T, "x"), narrow(H, "x"), post, gate, ld_gate,
+                                        (float)real(o[8]), res[0] ? at_of<void>(*res[0]) : nullptr, res[1] ? at_of<void>(*res[1]) : nullptr,
+                                        first && first->scalar_type() == at::kFloat, weight, (float)real(o[2]), y, stream_of(dev, o[9])));
+    });
+}
+
+// (q, positions, turns, amplitude, q_out, k, k_out, interleaved, offset, q_norm, k_norm, eps, stream)
+PyObject *rotary(PyObject *, PyObject *const *o, Py_ssize_t n) {
+    return guarded(n, 13, [&] {
+        Device dev;
+        const at::Tensor &q = heads(dev, o[0], "q"), &q_out = heads(dev, o[4], "q_out");
+        const at::Tensor &pos = whole(dev, o[1], at::kInt, "positions"), &turns = whole(dev, o[2], at::kLong, "turns");
+        const int64_t T = q.size(0), D = q.size(2);
+        want(pos, {T}, "positions");
+        want(q_out, {T, q.size(1), D}, "q_out");
+        if (turns.dim() != 1)
+            fail("turns", "expected a vector, got " + show(turns.sizes()));
+        const at::Tensor *k = nullptr, *k_out = nullptr;
+        if ((o[5] == Py_None) != (o[6] == Py_None))
+            fail("k_out", "expected with k, and only then");
+        if (o[5] != Py_None) {
+            k = &heads(dev, o[5], "k");
+            k_out = &heads(dev, o[6], "k_out");
+            want(*k, {T, k->size(1), D}, "k");
+            want(*k_out, {T, k->size(1), D}, "k_out");
+        } else if (o[10] != Py_None) {
+            fail("k_norm", "expected with k only");
+        }
+        const uint16_t *q_norm = vector_of(dev, o[9], D, "q_norm"), *k_norm = vector_of(dev, o[10], D, "k_norm");
+        const c10::cuda::CUDAGuard guard(dev.index());
+        return PyLong_FromLong(lib.rotary(
+            at_of<uint16_t>(q), step(q, 0), step(q, 1), at_of<uint16_t>(q_out), step(q_out, 0), step(q_out, 1), narrow(q.size(1), "q"),
+            k ? at_of<uint16_t>(*k) : nullptr, k ? step(*k, 0) : 0, k ? step(*k, 1) : 0, k ? at_of<uint16_t>(*k_out) : nullptr,
+            k ? step(*k_out, 0) : 0, k ? step(*k_out, 1) : 0, k ? narrow(k->size(1), "k") : 0, narrow(T, "q"), narrow(D, "q"),
+            at_of<int32_t>(pos), at_of<uint64_t>(turns), narrow(turns.size(0), "turns"), (float)real(o[3]), truth(o[7]),
+            integer(o[8], "offset"), q_norm, k_norm, (float)real(o[11]), stream_of(dev, o[12])));
+    });
+}
+
+// (cache)
+PyObject *check_latent_cache(PyObject *, PyObject *const *o, Py_ssize_t n) {
+    return guarded(n, 1, [&] {
+        Device dev;
+        latent_cache_of(dev, o[0]);
+        Py_RETURN_NONE;
+    });
+}
+
+// (c, k, slot_map, cache, ws, positions, turns, amplitude, interleaved, norm, eps, stream)
+PyObject *latent_append(PyObject *, PyObject *const *o, Py_ssize_t n) {
+    return guarded(n, 12, [&] {
+        Device dev;
+        const moe_latent_cache_t cache = latent_cache_of(dev, o[3]);
+        const at::Tensor &c = matrix(dev, o[0], "c"), &k = matrix(dev, o[1], "k"), &slots = whole(dev, o[2], at::kLong, "slot_map");
+        const at::Tensor &ws = whole(dev, o[4], at::kByte, "ws");
+        const int64_t T = slots.numel();
+        want(c, {T, cache.latent_dim}, "c");
+        want(k, {T, 64}, "k");
+        if ((o[5] == Py_None) != (o[6] == Py_None))
+            fail("positions", "expected with a table, and only then");
+        const int32_t *pos = nullptr;
+        const uint64_t *turns = nullptr;
+        if (o[5] != Py_None) {
+            const at::Tensor &p = whole(dev, o[5], at::kInt, "positions"), &t = whole(dev, o[6], at::kLong, "turns");
+            want(p, {T}, "positions");
+            want(t, {32}, "turns");
+            pos = at_of<int32_t>(p);
+            turns = at_of<uint64_t>(t);
+        }
+        const uint16_t *norm = vector_of(dev, o[9], cache.latent_dim, "norm");
+        const c10::cuda::CUDAGuard guard(dev.index());
+        return PyLong_FromLong(lib.latent_append(at_of<uint16_t>(c), step(c, 0), at_of<uint16_t>(k), step(k, 0), at_of<int64_t>(slots),
+                                                 narrow(T, "slot_map"), pos, turns, (float)real(o[7]), truth(o[8]), norm, (float)real(o[10]),
+                                                 &cache, at_of<void>(ws), (size_t)ws.numel(), stream_of(dev, o[11])));
+    });
+}
+
+// (q_latent, q_rope, cache, block_table, q_offsets, kv_lens, softmax_scale, out, lse, ws, causal, stream)
+PyObject *latent_attention(PyObject *, PyObject *const *o, Py_ssize_t n) {
+    return guarded(n, 12, [&] {
+        Device dev;
+        const moe_latent_cache_t cache = latent_cache_of(dev, o[2]);
+        const at::Tensor &ql = heads(dev, o[0], "q_latent"), &qr = heads(dev, o[1], "q_rope"), &table = whole(dev, o[3], at::kInt, "block_table");
+        const at::Tensor &qo = whole(dev, o[4], at::kInt, "q_offsets"), &kv = whole(dev, o[5], at::kInt, "kv_lens");
+        const at::Tensor &out = whole(dev, o[7], at::kBFloat16, "out"), &ws = whole(dev, o[9], at::kByte, "ws");
+        const int64_t B = kv.numel(), T = ql.size(0), H = ql.size(1);
+        want(ql, {T, H, cache.latent_dim}, "q_latent");
+        want(qr, {T, H, 64}, "q_rope");
+        want(out, {T, H, cache.latent_dim}, "out");
+        want(qo, {B + 1}, "q_offsets");
+        if (table.dim() != 2 || table.size(0) != B)
+            fail("block_table", "expected " + std::to_string(B) + " rows, got " + show(table.sizes()));
+        float *lse = nullptr;
+        if (o[8] != Py_None) {
+            const at::Tensor &l = whole(dev, o[8], at::kFloat, "lse");
+            want(l, {T, H}, "lse");
+            lse = at_of<float>(l);
+        }
+        const c10::cuda::CUDAGuard guard(dev.index());
+        return PyLong_FromLong(lib.latent_attention(
+            at_of<uint16_t>(ql), step(ql, 0), step(ql, 1), at_of<uint16_t>(qr), step(qr, 0), step(qr, 1), narrow(T, "q_latent"),
+            narrow(H, "q_latent"), &cache, at_of<int32_t>(table), narrow(table.size(1), "block_table"), at_of<int32_t>(qo), at_of<int32_t>(kv),
+            narrow(B, "kv_lens"), (float)real(o[6]), truth(o[10]), at_of<uint16_t>(out), lse, at_of<void>(ws), (size_t)ws.numel(),
+            stream_of(dev, o[11])));
+    });
+}
+
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(set_library), FAST(check_cache), FAST(check_weight), FAST(kv_build_tables), FAST(kv_append),
-                         FAST(kv_attention), FAST(quantize_fp8_weight), FAST(linear_fp8), {nullptr, nullptr, 0, nullptr}};
+                         FAST(kv_attention), FAST(quantize_fp8_weight), FAST(linear_fp8), FAST(rms_norm), FAST(rotary),
+                         FAST(check_latent_cache), FAST(latent_append), FAST(latent_attention), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

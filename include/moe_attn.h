@@ -7,6 +7,10 @@
  *   b2  append         new keys and values into the E4M3 cache
  *   b3  attention      of the new tokens over the cache
  *   b4  projection     y = x W^T with E4M3 operands, block-scaled
+ *   b5  norm           residual sum and root-mean-square norm before and after a block
+ *   b6  rotary         rotary positions on query and key heads
+ *   b7  latent append  a latent vector and a rotary key for each new token into a paged cache
+ *   b8  latent attention  of the new tokens over that cache, in its absorbed form
  *
  * Conventions are those of moe_fp4.h: row-major tensors, DEVICE pointers owned
  * by the caller, calls that enqueue kernels on `stream` and return without
@@ -152,6 +156,86 @@ size_t moe_linear_fp8_workspace_size(int T, int N, int K);
  */
 moe_status_t moe_linear_fp8(const uint16_t *x, int64_t ldx, int T, const uint8_t *codes, const uint8_t *scale, int N,
                             int K, uint16_t *y, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * b5: rows of H, for each of T tokens
+ *   u = x, or x * rms(x) * post_weight if post_weight is given   (the norm after a block)
+ *   h = residual + scale * gate * u                              (residual, gate: none is 0, 1)
+ *   residual_out = h,  y = h * rms(h) * weight                   (the norm before the next block)
+ * with rms(v) = 1 / sqrt(mean of v^2 + eps).  All in fp32, h for y not rounded first.  x bf16, rows ldx elements apart;
+ * post_weight, weight bf16 [H]; gate bf16, rows ld_gate elements apart, or 0 for one row for all tokens; residual and residual_out [T, H]
+ * bf16, or fp32 if residual_f32; y bf16 [T, H].  residual, residual_out, gate and post_weight may be NULL; y and weight may
+ * be NULL together, if residual_out is given.  residual_out may be residual, y may be x (rows of H).  A row with a value that is not
+ * finite, or whose squares overflow, is as the formulas give it in fp32; no other row is touched by it.
+ * H a multiple of 8 up to 32768, T <= 2^20; pointers 16-byte aligned, ldx and ld_gate multiples of 8.
+ */
+moe_status_t moe_rms_norm(const uint16_t *x, int64_t ldx, int T, int H, const uint16_t *post_weight, const uint16_t *gate,
+                          int64_t ld_gate, float scale, const void *residual, void *residual_out, int residual_f32,
+                          const uint16_t *weight, float eps, uint16_t *y, cudaStream_t stream);
+
+/*
+ * b6: rotary positions.  A head's dims offset .. offset + 2 pairs - 1 are `pairs` pairs (a_i, b_i): halves (a_i = dim i, b_i = dim
+ * pairs + i of them) or, if interleaved, neighbours (dims 2i, 2i + 1).  At position p
+ *   a' = amplitude (a cos t - b sin t),  b' = amplitude (b cos t + a sin t),  t = 2 pi p turns[i] 2^-64
+ * turns[i] being the pair's frequency in units of 2^-64 turns a position: p turns[i] modulo 2^64 is the exact angle, at any position.
+ * With q_norm (k_norm), bf16 [head_dim], a head v is v * rms(v) * norm first, all of its dims; other dims are as they were.
+ * fp32, rounded once.  q, q_out bf16, element (t, h, i) at t * stride_t + h * stride_h + i; k the same with k_heads heads (0: none).
+ * q_out may be q and k_out k, with the same strides; otherwise outputs overlap no input.  A token whose position is negative (as
+ * moe_kv_build_tables marks those behind the last) is left out: nothing is written.
+ * head_dim a multiple of 8 up to 256; pairs and offset multiples of 8, offset + 2 pairs <= head_dim; up to 1024 heads each; T <= 2^20;
+ * pointers 16-byte aligned (positions 4, turns 8), strides multiples of 8.
+ */
+moe_status_t moe_rotary(const uint16_t *q, int64_t q_stride_t, int64_t q_stride_h, uint16_t *q_out, int64_t q_out_stride_t,
+                        int64_t q_out_stride_h, int q_heads, const uint16_t *k, int64_t k_stride_t, int64_t k_stride_h,
+                        uint16_t *k_out, int64_t k_out_stride_t, int64_t k_out_stride_h, int k_heads, int T, int head_dim,
+                        const int32_t *positions, const uint64_t *turns, int pairs, float amplitude, int interleaved, int offset,
+                        const uint16_t *q_norm, const uint16_t *k_norm, float eps, cudaStream_t stream);
+
+/* The paged cache of b7 and b8: a token's latent vector c (latent_dim values) and its rotary key (64) side by side,
+ *   data  bf16 [num_blocks][block_size][latent_dim + 64]
+ * Slots past a request's length may hold anything. */
+typedef struct {
+    uint16_t *data;         /* 16-byte aligned */
+    int32_t num_blocks;     /* 1 .. 2^31-1, num_blocks * block_size <= 2^31-1 */
+    int32_t latent_dim;     /* 256 or 512 */
+    int32_t block_size;     /* 16, 32, 64 or 128 */
+} moe_latent_cache_t;
+
+/*
+ * b7: writes T tokens' latent vectors c (bf16, rows ldc elements apart) and rotary keys k (bf16 [64], rows ldk apart) to the slots
+ * slot_map [T] (block * block_size + offset; a negative one is skipped) of the cache.  With norm (bf16 [latent_dim])
+ * c * rms(c) * norm is written; with turns (32 of them) k is rotated to positions [T] as b6 does; without, k as it is.  Both NULL or
+ * neither of positions and turns.  A slot past the cache is skipped and recorded (MOE_ERR_DEVICE_ASSERT).  Where two tokens
+ * have one slot, either's values may be there afterwards.  T <= 2^24; c, k, norm 16-byte aligned, ldc and ldk multiples of 8.
+ * ws: 512 bytes or more.
+ */
+moe_status_t moe_latent_append(const uint16_t *c, int64_t ldc, const uint16_t *k, int64_t ldk, const int64_t *slot_map, int T,
+                               const int32_t *positions, const uint64_t *turns, float amplitude, int interleaved,
+                               const uint16_t *norm, float eps, const moe_latent_cache_t *cache, void *ws, size_t ws_bytes,
+                               cudaStream_t stream);
+
+/* Bytes of workspace of moe_latent_attention for up to T new tokens of up to B requests; 0 for sizes that it does not take. */
+size_t moe_latent_attention_workspace_size(int T, int B, int heads, int latent_dim);
+
+/*
+ * b8: softmax attention of the new tokens over the latent cache, which holds them already.  All heads share a token's latent vector
+ * c_j and rotary key r_j; the products with the matrices that make a head's keys and values from c_j are absorbed into the
+ * query (before) and the output (after), so that
+ *   x_j = softmax_scale (q_latent.c_j + q_rope.r_j)
+ *   out [T, heads, latent_dim] bf16 = sum_j softmax_j(x) c_j
+ *   lse [T, heads] fp32 or NULL     = log sum_j exp(x_j)
+ * q_latent [T, heads, latent_dim] and q_rope [T, heads, 64] bf16, element (t, h, i) at t * stride_t + h * stride_h + i.  Rows of a request,
+ * what they see (causal or not), rows that see nothing, rows past q_offsets[B], table entries that are not read and device-side errors are as in
+ * moe_kv_attention.  What a row does not see has no influence, NaN included; a row that sees a token with a value that is not finite is
+ * NaN in those dims at least.  Products are exact, sums and softmax statistics fp32; the weights are
+ * rounded to bf16, relative to themselves.  The same arguments give the same bits on the same device.
+ * heads <= 256, B <= 8192, T <= 2^20, T * heads < 2^31; q 16-byte aligned, strides multiples of 8.  Three launches at most.
+ */
+moe_status_t moe_latent_attention(const uint16_t *q_latent, int64_t ql_stride_t, int64_t ql_stride_h, const uint16_t *q_rope,
+                                  int64_t qr_stride_t, int64_t qr_stride_h, int T, int heads, const moe_latent_cache_t *cache,
+                                  const int32_t *block_table, int max_blocks, const int32_t *q_offsets, const int32_t *kv_lens,
+                                  int B, float softmax_scale, int causal, uint16_t *out, float *lse, void *ws, size_t ws_bytes,
+                                  cudaStream_t stream);
 
 #ifdef __cplusplus
 }
