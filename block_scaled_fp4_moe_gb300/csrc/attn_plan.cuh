@@ -1,5 +1,6 @@
-// attn_plan.cuh -- what the two attention kernels share: units of work, the
+// attn_plan.cuh -- what the attention kernels share: units of work, the
 // plan that lists them, and a CTA's walk through its range (attn.cu says how).
+// A kernel whose tiles or costs are others defines them before it includes this.
 #pragma once
 
 #include "attn.h"
@@ -7,11 +8,17 @@
 namespace moe {
 namespace {
 
-constexpr int kTile = 128;             // tokens of a tile
+#ifndef MOE_PLAN_TILE
+#define MOE_PLAN_TILE 128
+#define MOE_PLAN_UNIT_COST 2
+#define MOE_PLAN_MIN_COST 2
+#endif
+constexpr int kTile = MOE_PLAN_TILE;   // tokens of a tile
 constexpr int kSubs = kTile / 16;      // sub-blocks of a tile
-constexpr int kUnitCost = 2;           // a unit's fixed work, in tiles
-// Least range of a CTA, in tiles (us with 2, 4 and 6: one request of 1,000 tokens 9.8, 10.8 and 13.4, four of 2,000 12.2, 14.5 and 15.4).
-constexpr int kMinCost = 2;
+constexpr int kUnitCost = MOE_PLAN_UNIT_COST;      // a unit's fixed work, in tiles
+// Least range of a CTA, in tiles (us with 2, 4 and 6 of 128 tokens: one request of 1,000 tokens 9.8, 10.8 and 13.4, four of 2,000 12.2, 14.5
+// and 15.4).
+constexpr int kMinCost = MOE_PLAN_MIN_COST;
 constexpr int kPlanThreads = 1024;
 constexpr unsigned long long kWaitLimitNs = 200ull * 1000 * 1000;
 
@@ -237,15 +244,15 @@ struct Walk {
     const AttnArgs &a;
     const RowTile *recs;
     long long pos, end, base, per;
-    int rt, head, n_recs;
+    int rt, head, n_recs, cta;
     RowTile r;
-    __device__ Walk(const AttnArgs &args, const Plan &pl, const RowTile *tiles) : a(args), recs(tiles) {
+    __device__ Walk(const AttnArgs &args, const Plan &pl, const RowTile *tiles, int which = (int)blockIdx.x) : a(args), recs(tiles), cta(which) {
         n_recs = pl.row_tiles;
         per = pl.per;
-        pos = (long long)blockIdx.x * per;
+        pos = (long long)cta * per;
         end = min(pos + per, pl.work);
         rt = n_recs;
-        if ((int)blockIdx.x >= pl.ctas || pos >= pl.work)
+        if (cta >= pl.ctas || pos >= pl.work)
             return;
         int lo = 0, hi = n_recs;                // the last row tile with before <= pos
         while (hi - lo > 1) {
@@ -278,7 +285,7 @@ struct Walk {
                 pc.tile0 = r.tile0;
                 pc.t0 = lo;
                 pc.t1 = hi;
-                pc.first = pc.last = (int)blockIdx.x;
+                pc.first = pc.last = cta;
                 pc.first_tiles = pc.last_tiles = r.tiles;
                 const long long t0 = base + kUnitCost, t1 = t0 + r.tiles - 1;
                 if (r.tiles > 0 && (t0 < pos || t1 >= end)) {      // cut

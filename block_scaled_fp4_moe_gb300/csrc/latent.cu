@@ -1,146 +1,882 @@
 // latent.cu -- attention over a cache of one latent vector and one rotary key a token (moe_attn.h, b8).
 //
-//   x_j = softmax_scale (q_latent.c_j + q_rope.r_j),   out = sum_j p_j c_j / sum_j p_j,   p_j = exp(x_j - max x)
+//   s_j = q_latent.c_j + q_rope.r_j,   p_j = 2^((s_j - m) f),  f = softmax_scale log2(e),   out = sum_j p_j c_j / sum_j p_j
 //
-// The plain form: a CTA has a token's sixteen heads and walks the cache in tiles of 32 tokens in shared memory, with running maxima and
-// sums; two dims of every head's sum in a thread's registers.
-#include "attn.h"
+// All heads of a token read the same cache, so a row (a token's head) costs no bytes of its own: a token of the cache is 2 (L + 64) bytes and
+// 2 (2 L + 64) operations a row, 121 operations a byte at 64 rows.  The work is to keep the loads running beside two products.
+//
+// Both products are made with the cache as the M side, which is never padded however few rows there are:
+//   S^T = K Q^T     M = 64 tokens,      N = rows (up to 64), K = L + 64: the tile as it lies in the cache, dims innermost
+//   O^T += C^T P^T  M = 128 dims a time, N = rows,           K = 64 tokens: the same bytes, read along the other axis
+// A tile of 64 tokens is loaded once, by tensor copies (128-byte swizzle) of 64 dims each: the rotary key's 8 KB, and pairs of 64 dims (16 KB)
+// in a ring of their own, which the second product gives back one by one.  O^T (L columns of 32-bit sums for 64 rows: 256
+// columns) and two S^T stay in tensor memory.
+//
+// Softmax.  In S^T a row is a column, spread over 64 lanes, and a maximum over tokens would be a walk through shuffles for each.
+// None is needed: any score of a row serves as its reference m as long as the powers stay in range, and weights rounded to bf16
+// lose the same whatever their size.  The reference is the score of the piece's first token; a row's moves (to its
+// maximum, with O and the sum) when a power passes 2^32, which one vote a tile finds out.
+// s - m is taken before the factor, so that it is as exact as the scores, of any size.
+//
+// What a row does not see: its weight is 0, and the values of such tokens must be finite for the product.  In tiles that some row does not see
+// in full (the last ones of a request) values past the last row's end become zero; those that some rows see become zero where they
+// are not finite, and their weight NaN for the rows that do see them.
+//
+// Work is cut as in attn.cu (attn_plan.cuh): units of rows, their tiles laid end to end and cut into equal ranges; a range that cuts a
+// unit leaves its sums in the workspace, and latent_join_kernel adds them up, a few rows a CTA (one request's parts are many:
+// the last CTA alone would be a while at it).  With more than 64 rows a token two CTAs take the halves of a
+// unit's rows, side by side, so that the second reads the cache from L2.
+//
+// Warps: 0..7 softmax (warp % 4 = lane quarter, 16 tokens each; warp / 4 = half of the rows), 8 streams the cache, 9 issues the products.
+#define MOE_PLAN_TILE 64
+#define MOE_PLAN_UNIT_COST 3
+#define MOE_PLAN_MIN_COST 4
+#include "attn_plan.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kHeads = 16, kTokens = 32, kThreads = 256;
+constexpr int kSoftWarps = 8, kThreads = (kSoftWarps + 2) * 32, kSoft = kSoftWarps * 32;
+constexpr int kMaxRows = 64;                 // of a CTA's unit
+constexpr int kChunkBytes = kTile * 128;     // 64 dims of a tile
+constexpr int kMaxSlots = 12;                // pairs of chunks in the ring
+constexpr int kRopeSlots = 2;
+constexpr int kSCol = 256;                   // tensor memory: O^T at 64 m, S^T from here
+constexpr float kMostPower = 32.0f;
+
+// A cut unit that begins in a CTA: where its rows go, its parts.
+struct LatentJoin {
+    long long row;                           // first of its rows in out
+    int rows, first, last;
+};
+
+struct LatentArgs {
+    AttnArgs a;                              // the plan's view: one key/value head, `heads` query heads
+    LatentProblem p;
+    int split;                               // CTAs that share a unit's rows: 1 or 2
+    int q_rows;                              // rows of the query buffer
+    int slots;                               // pairs in the ring
+    int cap;                                 // rows of a part
+    float factor;
+    LatentJoin *joins;
+    float *part;                             // [slot][cap][L]
+    float2 *part_sum;                        // [slot][cap]: m, sum
+};
 
 template <int L>
-__global__ void __launch_bounds__(kThreads) latent_plain_kernel(const LatentProblem p, uint32_t *hdr) {
-    constexpr int W = L + kRopeDims, P = W + 2;            // a row's pitch: its threads read other banks
-    constexpr int D = L / kThreads;
-    extern __shared__ uint16_t rows[];                     // queries [kHeads][P], tokens [kTokens][P]
-    __shared__ float s_x[kHeads][kTokens], s_m[kHeads], s_l[kHeads], s_by[kHeads];
-    __shared__ int s_request;
-    const int tid = threadIdx.x, t = blockIdx.x, h0 = blockIdx.y * kHeads;
-    pdl_wait();
-    pdl_trigger();
-    if (tid == 0)
-        s_request = -1;
-    int bad = 0;
-    __syncthreads();
-    for (int b = tid; b < p.B; b += kThreads) {
-        const int lo = p.q_offsets[b], hi = p.q_offsets[b + 1], kv = p.kv_lens[b];
-        bad |= lo < 0 || hi < lo || hi > p.T || kv < 0 || kv > (long long)p.max_blocks * p.cache.block_size;
-        if (t >= lo && t < hi)
-            s_request = b;
+struct LatentSmem {
+    static constexpr int kPairs = L / 128;
+    static constexpr int kChunks = L / 64 + 1;
+    uint8_t *ring, *rope, *p, *q;
+    uint64_t *pair_full, *pair_empty, *rope_full, *rope_empty, *s_full, *p_ready, *o_done, *o_free, *q_ready;
+    float *ref, *fac, *sum;                  // [64] each
+    float *red;                              // [4][64], over the weights while no product reads them
+    int *hi;                                 // [64]
+    uint32_t *bad;                           // a bit for each token of a tile
+    uint32_t *taddr;
+    static constexpr size_t kTail = (2 * kMaxSlots + 2 * kRopeSlots + 8) * 8 + 64 * 4 * 4 + 16;
+    __host__ __device__ static size_t fixed(int q_rows) { return (size_t)kRopeSlots * kChunkBytes + kChunkBytes + (size_t)q_rows * 128 * kChunks + kTail + 1024; }
+    __host__ __device__ static size_t bytes(int q_rows, int slots) { return fixed(q_rows) + (size_t)slots * 2 * kChunkBytes; }
+    __host__ static int slots_for(int q_rows) {
+        const int n = (int)((227 * 1024 - fixed(q_rows)) / (2 * kChunkBytes));
+        return n < kMaxSlots ? n : kMaxSlots;
     }
-    if (__syncthreads_or(bad)) {
-        if (tid == 0)
-            record_status(hdr, MOE_ERR_DEVICE_ASSERT);
-        return;
+    __device__ LatentSmem(uint8_t *base, int q_rows, int slots) {
+        ring = base;
+        rope = ring + (size_t)slots * 2 * kChunkBytes;
+        p = rope + kRopeSlots * kChunkBytes;
+        q = p + kChunkBytes;
+        uint64_t *b = reinterpret_cast<uint64_t *>(q + (size_t)q_rows * 128 * kChunks);
+        pair_full = b;
+        pair_empty = b + kMaxSlots;
+        rope_full = b + 2 * kMaxSlots;
+        rope_empty = rope_full + kRopeSlots;
+        s_full = rope_empty + kRopeSlots;
+        p_ready = s_full + 2;
+        o_done = p_ready + 1;
+        o_free = o_done + 1;
+        q_ready = o_free + 1;
+        ref = reinterpret_cast<float *>(s_full + 8);
+        fac = ref + 64;
+        sum = fac + 64;
+        red = reinterpret_cast<float *>(p);
+        hi = reinterpret_cast<int *>(sum + 64);
+        bad = reinterpret_cast<uint32_t *>(hi + 64);
+        taddr = bad + 2;
     }
-    const int b = s_request;
-    if (b < 0)
-        return;
-    const int kv = p.kv_lens[b], last = p.causal ? kv - (p.q_offsets[b + 1] - t) + 1 : kv, seen = min(kv, last);
-    uint16_t *qs = rows, *ks = rows + kHeads * P;
-    for (int i = tid; i < kHeads * W; i += kThreads) {
-        const int h = i / W, d = i % W;
-        uint16_t v = 0;
-        if (h0 + h < p.heads)
-            v = d < L ? p.ql[t * p.ql_st + (h0 + h) * p.ql_sh + d] : p.qr[t * p.qr_st + (h0 + h) * p.qr_sh + d - L];
-        qs[h * P + d] = v;
+};
+
+// A CTA's share of a piece: its rows and the tiles that they see.
+struct Mine {
+    int row0, rows, n_side;                  // rows, and rounded up to the MMA's N
+    int tok0, tiles;
+    int hi_min, hi_max;                      // positions that the first and the last row see
+
+    __device__ Mine(const LatentArgs &g, const Piece &pc) {
+        const int part = g.split == 1 ? 0 : (int)blockIdx.x & 1;
+        const int per = g.split == 1 ? pc.rows : ((pc.rows + 1) / 2 + 15) / 16 * 16;
+        row0 = pc.row0 + part * per;
+        rows = max(0, min(pc.rows - part * per, per));
+        n_side = (rows + 15) / 16 * 16;
+        tok0 = (pc.tile0 + pc.t0) * kTile;
+        tiles = hi_min = hi_max = 0;
+        if (rows > 0) {
+            int lo;
+            row_range(g.a.p, g.a.group, pc.kv, pc.n, row0, lo, hi_min);
+            row_range(g.a.p, g.a.group, pc.kv, pc.n, row0 + rows - 1, lo, hi_max);
+            const int end = min((pc.tile0 + pc.t1) * kTile, hi_max);
+            tiles = end > tok0 ? (end - tok0 + kTile - 1) / kTile : 0;
+        }
     }
-    if (tid < kHeads) {
-        s_m[tid] = -INFINITY;
-        s_l[tid] = 0.0f;
+};
+
+// ------------------------------------------------------------------ tcgen05
+
+// Rows of 128 bytes in swizzled atoms of 8, the summed axis along the row.
+__device__ __forceinline__ uint64_t desc_along(uint32_t addr) {
+    return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// The same bytes with the summed axis across the rows; 64 further elements along the row lie a chunk further on.
+__device__ __forceinline__ uint64_t desc_across(uint32_t addr) {
+    return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(kChunkBytes >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// fp32 sums of bf16 products; across: both operands are read across their rows.
+__device__ __forceinline__ uint32_t idesc_bf16(int m, int n, bool across) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (across ? (1u << 15) | (1u << 16) : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
+}
+
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n.reg .pred p, q;\nelect.sync _|p, 0xffffffff;\nsetp.ne.b32 q, %4, 0;\n"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void commit(uint64_t *bar) {
+    asm volatile(
+        "{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\n"
+        "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 16 lanes x 32 columns: v[4 i + 2 k + e] is lane lane / 4 + 8 k, column 8 i + 2 (lane % 4) + e.
+__device__ __forceinline__ void tmem_ld_16x32(float (&v)[16], uint32_t addr) {
+    uint32_t *u = reinterpret_cast<uint32_t *>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]), "=r"(u[9]),
+          "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_32x16(float (&v)[16], uint32_t addr) {
+    uint32_t *u = reinterpret_cast<uint32_t *>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]), "=r"(u[9]),
+          "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_32x16(uint32_t addr, const float (&v)[16]) {
+    const uint32_t *u = reinterpret_cast<const uint32_t *>(v);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n"
+                 "tcgen05.wait::st.sync.aligned;" ::"r"(addr),
+                 "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]),
+                 "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
+                 : "memory");
+}
+
+// [1][rows][64 dims] or [2][rows][64 dims] of chunks c.. and rows row.. of the cache.
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int row, int c, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(c), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// A barrier of the softmax warps, and one that or's a predicate.
+__device__ __forceinline__ void soft_sync() { named_barrier_sync(1, kSoft); }
+__device__ __forceinline__ bool soft_any(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, 1, %2, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(kSoft)
+        : "memory");
+    return r != 0;
+}
+
+// Waits of a role's warp; after one that gave up it waits no more.
+struct Waiter {
+    uint32_t *hdr;
+    bool dead;
+    __device__ void operator()(uint64_t *bar, uint32_t parity) {
+        if (!dead) {
+            dead = !__all_sync(0xffffffffu, wait_phase(bar, parity));
+            if (dead && (threadIdx.x & 31) == 0)
+                record_status(hdr, MOE_ERR_DEVICE_TIMEOUT);
+        }
+        fence_after();
     }
-    float o[kHeads][D];
-#pragma unroll
-    for (int h = 0; h < kHeads; ++h)
-#pragma unroll
-        for (int d = 0; d < D; ++d)
-            o[h][d] = 0.0f;
-    auto wide = [](uint16_t v) { return __uint_as_float((uint32_t)v << 16); };
-    for (int j0 = 0; j0 < seen; j0 += kTokens) {
-        __syncthreads();
-        for (int i = tid; i < kTokens * W; i += kThreads) {
-            const int j = j0 + i / W, d = i % W;
-            uint16_t v = 0;
-            if (j < seen) {
-                int page = p.table[(size_t)b * p.max_blocks + j / p.cache.block_size];
-                if (page < 0 || page >= p.cache.num_blocks) {
-                    record_status(hdr, MOE_ERR_DEVICE_ASSERT);
+};
+
+// ------------------------------------------------------------ the cache's tiles
+
+template <int L>
+__device__ __forceinline__ void latent_stream(const LatentArgs &g, const Plan &pl, const LatentSmem<L> &s, const CUtensorMap *pair_map,
+                                              const CUtensorMap *chunk_map) {
+    const AttnProblem &p = g.a.p;
+    const int lane = threadIdx.x & 31;
+    const int box_shift = min(g.a.shift, 6), subs = kTile >> box_shift;          // a box's rows lie in one block
+    Waiter wait{g.a.hdr, false};
+    Walk walk(g.a, pl, g.a.recs, (int)blockIdx.x / g.split);
+    Piece pc;
+    uint32_t pairs = 0, ropes = 0;
+    while (walk.next(pc)) {
+        const Mine m(g, pc);
+        const int32_t *row = p.table + (size_t)pc.request * p.max_blocks;
+        // the rows of the cache of 32 boxes at a time, a lane each; the next ones' block ids on their way
+        auto fetch = [&](int box) {
+            const long long tok = (long long)m.tok0 + ((long long)(box + lane) << box_shift);
+            return tok < m.hi_max && box + lane < m.tiles * subs ? __ldg(row + (tok >> g.a.shift)) : -1;
+        };
+        int next = m.tiles > 0 ? fetch(0) : -1, at = 0;
+        for (int t = 0; t < m.tiles; ++t) {
+            const int box = t * subs;
+            if (box % 32 == 0) {
+                int page = next;
+                const long long tok = (long long)m.tok0 + ((long long)(box + lane) << box_shift);
+                const bool used = tok < m.hi_max && box + lane < m.tiles * subs;
+                if (used && (page < 0 || page >= p.cache.num_blocks)) {
+                    record_status(g.a.hdr, MOE_ERR_DEVICE_ASSERT);
                     page = 0;
                 }
-                v = p.cache.data[((size_t)page * p.cache.block_size + j % p.cache.block_size) * W + d];
+                at = used ? (page << g.a.shift) + (int)(tok & ((1 << g.a.shift) - 1)) : -1;
+                next = box + 32 < m.tiles * subs ? fetch(box + 32) : -1;
             }
-            ks[(i / W) * P + d] = v;
-        }
-        __syncthreads();
-        for (int i = tid; i < kHeads * kTokens; i += kThreads) {
-            const int h = i / kTokens, j = i % kTokens;
-            float s = 0.0f;
-            for (int d = 0; d < W; ++d)
-                s = fmaf(wide(qs[h * P + d]), wide(ks[j * P + d]), s);
-            s_x[h][j] = j0 + j < seen ? s * p.scale : -INFINITY;
-        }
-        __syncthreads();
-        if (tid < kHeads) {
-            float m = s_m[tid];
-            for (int j = 0; j < kTokens; ++j)
-                m = s_x[tid][j] > m || isnan(s_x[tid][j]) ? s_x[tid][j] : m;
-            const float z = m == -INFINITY ? 0.0f : m;
-            s_by[tid] = expf(s_m[tid] - z);
-            float l = s_l[tid] * s_by[tid];
-            for (int j = 0; j < kTokens; ++j) {
-                s_x[tid][j] = expf(s_x[tid][j] - z);
-                l += s_x[tid][j];
-            }
-            s_m[tid] = m;
-            s_l[tid] = l;
-        }
-        __syncthreads();
-        const int n = min(kTokens, seen - j0);
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-#pragma unroll
-            for (int h = 0; h < kHeads; ++h)
-                o[h][d] *= s_by[h];
-            for (int j = 0; j < n; ++j) {
-                const float c = wide(ks[j * P + tid + d * kThreads]);
-#pragma unroll
-                for (int h = 0; h < kHeads; ++h)
-                    o[h][d] = fmaf(s_x[h][j], c, o[h][d]);
+            // boxes of this tile that hold something
+            const int live = min(subs, (m.hi_max - (m.tok0 + t * kTile) + (1 << box_shift) - 1) >> box_shift);
+            const uint32_t chunk_bytes = (uint32_t)(live << box_shift) * 128;
+            auto load = [&](uint8_t *dst, uint64_t *bar, int c, int n) {         // chunks c .. c + n - 1
+                if (lane == 0)
+                    mbar_arrive_expect_tx(bar, chunk_bytes * n);
+                __syncwarp();
+                const int sub = lane % subs, k = lane / subs;
+                const int to = __shfl_sync(0xffffffffu, at, (box & 31) + sub);
+                if (wait.dead)
+                    return;
+                if (subs == 1) {
+                    if (lane == 0)
+                        copy_box(smem_u32(dst), n == 2 ? pair_map : chunk_map, to, c, bar);
+                } else if (k < n && sub < live) {
+                    copy_box(smem_u32(dst + k * kChunkBytes + (sub << box_shift) * 128), chunk_map, to, c + k, bar);
+                }
+            };
+            const uint32_t rs = ropes % kRopeSlots;
+            if (ropes >= kRopeSlots)
+                wait(s.rope_empty + rs, (ropes / kRopeSlots - 1) & 1);
+            load(s.rope + rs * kChunkBytes, s.rope_full + rs, L / 64, 1);
+            ++ropes;
+            for (int i = 0; i < LatentSmem<L>::kPairs; ++i, ++pairs) {
+                const uint32_t slot = pairs % g.slots, turn = pairs / g.slots;
+                if (turn > 0)
+                    wait(s.pair_empty + slot, (turn - 1) & 1);
+                load(s.ring + (size_t)slot * 2 * kChunkBytes, s.pair_full + slot, 2 * i, 2);
             }
         }
     }
+    // copies in flight end before the CTA's memory goes away
+    for (uint32_t i = pairs > (uint32_t)g.slots ? pairs - g.slots : 0; i < pairs && !wait.dead; ++i)
+        wait(s.pair_full + i % g.slots, (i / g.slots) & 1);
+    for (uint32_t i = ropes > kRopeSlots ? ropes - kRopeSlots : 0; i < ropes && !wait.dead; ++i)
+        wait(s.rope_full + i % kRopeSlots, (i / kRopeSlots) & 1);
+}
+
+// --------------------------------------------------------------- products
+
+template <int L>
+__device__ __forceinline__ void latent_issue(const LatentArgs &g, const Plan &pl, const LatentSmem<L> &s, uint32_t tmem) {
+    constexpr int kPairs = LatentSmem<L>::kPairs;
+    Waiter wait{g.a.hdr, false};
+    Walk walk(g.a, pl, g.a.recs, (int)blockIdx.x / g.split);
+    Piece pc;
+    uint32_t sp = 0, op = 0, ropes = 0, tiles = 0, weights = 0, units = 0;       // pairs met by the first and by the second product, ...
+    const uint64_t dp = desc_across(smem_u32(s.p));
+    while (walk.next(pc)) {
+        const Mine m(g, pc);
+        if (m.tiles == 0)
+            continue;
+        const uint32_t is = idesc_bf16(kTile, m.n_side, false), io = idesc_bf16(128, m.n_side, true);
+        const int q_chunk = g.q_rows * 128;
+        wait(s.q_ready, units & 1);
+        // O^T += C^T P^T of the oldest tile whose weights are there
+        auto values = [&](bool first) {
+            if (first && units > 0)
+                wait(s.o_free, (units - 1) & 1);
+            for (int i = 0; i < kPairs; ++i, ++op) {
+                const uint32_t slot = op % g.slots;
+                const uint64_t dv = desc_across(smem_u32(s.ring + (size_t)slot * 2 * kChunkBytes));
+                if (!wait.dead) {
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        mma(tmem + 64 * i, dv + k * (16 * 128 >> 4), dp + k * (16 * 128 >> 4), io, !first || k > 0);
+                }
+                commit(s.pair_empty + slot);
+            }
+            commit(s.o_done);
+        };
+        bool pending = false;                      // a tile's second product is to be issued
+        for (int t = 0; t < m.tiles; ++t, ++tiles, ++ropes) {
+            const uint32_t d = tmem + kSCol + 64 * (tiles & 1);
+            const uint64_t begun = globaltimer_ns();
+            // while the tile is on its way the weights of the one before may come first
+            auto arrived = [&](uint64_t *bar, uint32_t parity) {
+                while (pending && !wait.dead && !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+                    if (__all_sync(0xffffffffu, mbar_try_wait(s.p_ready, weights & 1))) {
+                        fence_after();
+                        ++weights;
+                        values(t == 1);
+                        pending = false;
+                    } else if (globaltimer_ns() - begun > kWaitLimitNs) {
+                        break;
+                    }
+                wait(bar, parity);
+            };
+            const uint32_t rs = ropes % kRopeSlots;
+            arrived(s.rope_full + rs, (ropes / kRopeSlots) & 1);
+            const uint64_t dq = desc_along(smem_u32(s.q)), dr = desc_along(smem_u32(s.rope + rs * kChunkBytes));
+            if (!wait.dead) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma(d, dr + k * 2, dq + (L / 64) * (q_chunk >> 4) + k * 2, is, k > 0);
+            }
+            for (int i = 0; i < kPairs; ++i, ++sp) {
+                const uint32_t slot = sp % g.slots;
+                arrived(s.pair_full + slot, (sp / g.slots) & 1);
+                const uint64_t dk = desc_along(smem_u32(s.ring + (size_t)slot * 2 * kChunkBytes));
+                if (!wait.dead) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma(d, dk + (k >> 2) * (kChunkBytes >> 4) + (k & 3) * 2, dq + (2 * i + (k >> 2)) * (q_chunk >> 4) + (k & 3) * 2, is, 1);
+                }
+            }
+            commit(s.s_full + (tiles & 1));
+            commit(s.rope_empty + rs);
+            if (pending) {
+                wait(s.p_ready, weights & 1);
+                ++weights;
+                values(t == 1);
+            }
+            pending = true;
+        }
+        wait(s.p_ready, weights & 1);
+        ++weights;
+        values(m.tiles == 1);
+        ++units;
+    }
+    // issued products end before the CTA's memory goes away
+    if (tiles > 0)
+        wait(s.o_done, (tiles - 1) & 1);
+}
+
+// ------------------------------------------------------------------ softmax
+
+template <int L>
+__device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Plan &pl, const LatentSmem<L> &s, uint32_t tmem) {
+    constexpr int kPairs = LatentSmem<L>::kPairs;
+    const LatentProblem &p = g.p;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, tid = threadIdx.x;
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    const int cta = (int)blockIdx.x / g.split, part = g.split == 1 ? 0 : (int)blockIdx.x & 1;
+    const int col0 = 32 * half + 2 * (lane & 3);            // this thread's columns: col0 + 8 i + e
+    const int tok_a = 16 * quarter + (lane >> 2);           // its tokens of a tile: tok_a + 8 k
+    const float f = g.factor;
+    Waiter wait{g.a.hdr, false};
+    Walk walk(g.a, pl, g.a.recs, cta);
+    Piece pc;
+    LatentJoin join{0, 0, 0, 0};
+    uint32_t tiles = 0;                                      // so far
+    while (walk.next(pc)) {
+        const Mine m(g, pc);
+        if (m.rows == 0)
+            continue;
+        const bool whole = pc.first == pc.last;
+        const long long out_row = (long long)pc.q0 * p.heads + m.row0;
+        const int slot = (cta * 2 + (cta == pc.first)) * g.split + part;
+        if (!whole && cta == pc.first)
+            join = LatentJoin{out_row, m.rows, pc.first, pc.last};
+        if (m.tiles == 0) {                                  // nothing that these rows see
+            if (whole) {
+                uint4 *to = reinterpret_cast<uint4 *>(p.out + out_row * L);
+                for (int i = tid; i < m.rows * (L / 8); i += kSoft)
+                    to[i] = make_uint4(0, 0, 0, 0);
+                if (p.lse && tid < m.rows)
+                    p.lse[out_row + tid] = -INFINITY;
+            } else if (tid < m.rows) {
+                __stcg(g.part_sum + (size_t)slot * g.cap + tid, make_float2(-INFINITY, 0.0f));
+            }
+            continue;
+        }
+        // queries, zero past the last row; the scores of the unit before are all made
+        for (int i = tid; i < m.n_side * (L / 8 + 8); i += kSoft) {
+            const int r = i / (L / 8 + 8), c = i % (L / 8 + 8);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (r < m.rows) {
+                const int64_t t = pc.q0 + (m.row0 + r) / p.heads, h = (m.row0 + r) % p.heads;
+                v = c < L / 8 ? __ldg(reinterpret_cast<const uint4 *>(p.ql + t * p.ql_st + h * p.ql_sh) + c)
+                              : __ldg(reinterpret_cast<const uint4 *>(p.qr + t * p.qr_st + h * p.qr_sh) + c - L / 8);
+            }
+            *reinterpret_cast<uint4 *>(s.q + (size_t)(c >> 3) * g.q_rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+        }
+        if (tid < kMaxRows) {
+            int lo, hi = m.hi_max;
+            if (tid < m.rows)
+                row_range(g.a.p, g.a.group, pc.kv, pc.n, m.row0 + tid, lo, hi);
+            s.hi[tid] = hi;
+        }
+        fence_async();
+        soft_sync();
+        if (tid == 0)
+            mbar_arrive(s.q_ready);
+        const int groups = max(0, min(4, (m.n_side - 32 * half) / 8));           // columns of this warp, by 8
+        float ref[8], sum[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            ref[i] = sum[i] = 0.0f;
+        for (int t = 0; t < m.tiles; ++t, ++tiles) {
+            const int tok = m.tok0 + t * kTile;
+            const bool edge = tok + kTile > m.hi_min;        // some row does not see all of the tile
+            wait(s.s_full + (tiles & 1), (tiles >> 1) & 1);
+            float x[16];
+            tmem_ld_16x32(x, lanes + kSCol + 64 * (tiles & 1) + 32 * half);
+            if (edge) {
+                if (tid < 2)
+                    s.bad[tid] = 0;
+                soft_sync();
+                const int j0 = max(0, m.hi_min - tok), n = (kTile - j0) * (L / 8);
+                for (int i = tid; i < n; i += kSoft) {
+                    const int j = j0 + i / (L / 8), c = i % (L / 8);
+                    const uint32_t ring = (tiles * kPairs + c / 16) % g.slots;
+                    uint4 *at = reinterpret_cast<uint4 *>(s.ring + (size_t)ring * 2 * kChunkBytes + (c / 8 & 1) * kChunkBytes + j * 128 +
+                                                          (((c & 7) ^ (j & 7)) << 4));
+                    if (tok + j >= m.hi_max) {
+                        *at = make_uint4(0, 0, 0, 0);
+                        continue;
+                    }
+                    const uint4 v = *at;
+                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    bool odd = false;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t not_finite = __vcmpeq2(w[e] & 0x7F807F80u, 0x7F807F80u);
+                        odd |= not_finite != 0;
+                        w[e] &= ~not_finite;
+                    }
+                    if (odd) {
+                        atomicOr(s.bad + j / 32, 1u << (j & 31));
+                        *at = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                fence_async();
+                soft_sync();
+            }
+            if (t == 0) {
+                // the first token's scores are the references; rows that do not see it see nothing here
+                if (quarter == 0 && lane < 4)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        s.ref[col0 + 8 * (i >> 1) + (i & 1)] = x[4 * (i >> 1) + (i & 1)];
+                soft_sync();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int col = col0 + 8 * (i >> 1) + (i & 1);
+                    ref[i] = tok < s.hi[col] ? s.ref[col] : 0.0f;
+                }
+            }
+            if (t > 0)                                       // the weights before have been read
+                wait(s.o_done, (tiles - 1) & 1);
+            float w[16];
+            auto weigh = [&]() -> bool {                     // weights of the scores; whether one has grown too far
+                bool grew = false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < groups) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const float y = (x[4 * i + 2 * k + e] - ref[2 * i + e]) * f;
+                                float v = ex2(y);
+                                bool up = y > kMostPower;
+                                if (edge) {
+                                    const int j = tok_a + 8 * k;
+                                    const bool sees = tok + j < s.hi[col0 + 8 * i + e];
+                                    if (s.bad[j / 32] >> (j & 31) & 1)
+                                        v = __uint_as_float(0x7FFFFFFFu);
+                                    v = sees ? v : 0.0f;
+                                    up &= sees;
+                                }
+                                w[4 * i + 2 * k + e] = v;
+                                grew |= up;
+                            }
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int j = tok_a + 8 * k, c = col0 + 8 * i;       // 8 columns are 16 bytes
+                            *reinterpret_cast<uint32_t *>(s.p + j * 128 + (((c >> 3) ^ (j & 7)) << 4) + (c & 7) * 2) =
+                                bf16_pair(w[4 * i + 2 * k], w[4 * i + 2 * k + 1]);
+                        }
+                    }
+                fence_async();
+                return grew;
+            };
+            const bool grew = weigh();
+            fence_before();
+            if (soft_any(grew)) {
+                // references to the maxima; with them the sums, and O
+                float top[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int col = col0 + 8 * (i >> 1) + (i & 1);
+                    top[i] = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (!edge || tok + tok_a + 8 * k < s.hi[col])
+                            top[i] = fmaxf(top[i], x[4 * (i >> 1) + 2 * k + (i & 1)]);
+#pragma unroll
+                    for (int d = 4; d < 32; d *= 2)
+                        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], d));
+                    if (lane < 4)
+                        s.red[64 * quarter + col] = top[i];
+                }
+                soft_sync();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int col = col0 + 8 * (i >> 1) + (i & 1);
+                    const float most = fmaxf(fmaxf(s.red[col], s.red[64 + col]), fmaxf(s.red[128 + col], s.red[192 + col]));
+                    const bool moves = (most - ref[i]) * f > kMostPower;         // the other rows keep theirs, and their bits
+                    const float to = moves ? most : ref[i];
+                    const float by = t == 0 ? 0.0f : moves ? ex2((ref[i] - to) * f) : 1.0f;
+                    ref[i] = to;
+                    sum[i] = t == 0 ? 0.0f : sum[i] * by;
+                    if (quarter == 0 && lane < 4)
+                        s.fac[col] = by;
+                }
+                soft_sync();
+                if (t > 0) {
+                    fence_after();
+                    for (int i = 0; i < 2 * kPairs; ++i)
+                        if (16 * (i & 1) < 8 * groups) {
+                            float o[16];
+                            const int c = 32 * half + 16 * (i & 1);
+                            tmem_ld_32x16(o, lanes + 64 * (i >> 1) + c);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                o[e] *= s.fac[c + e];
+                            tmem_st_32x16(lanes + 64 * (i >> 1) + c, o);
+                        }
+                }
+                weigh();
+                fence_before();
+                soft_sync();
+            }
+            if (tid == 0)
+                mbar_arrive(s.p_ready);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < groups)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        sum[2 * i + e] += w[4 * i + e] + w[4 * i + 2 + e];
+        }
+        wait(s.o_done, (tiles - 1) & 1);
+        // sums of the columns: eight lanes, four warps, in this order
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int col = col0 + 8 * (i >> 1) + (i & 1);
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2)
+                sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], d);
+            if (lane < 4)
+                s.red[64 * quarter + col] = sum[i];
+            if (quarter == 0 && lane < 4)
+                s.ref[col] = ref[i];
+        }
+        soft_sync();
+        if (tid < kMaxRows)
+            s.sum[tid] = (s.red[tid] + s.red[64 + tid]) + (s.red[128 + tid] + s.red[192 + tid]);
+        soft_sync();
+        if (tid < m.rows) {
+            const float l = s.sum[tid];
+            if (!whole)
+                __stcg(g.part_sum + (size_t)slot * g.cap + tid, make_float2(l == 0.0f ? -INFINITY : s.ref[tid], l));
+            else if (p.lse)
+                p.lse[out_row + tid] = l == 0.0f ? -INFINITY : fmaf(s.ref[tid], p.scale, logf(l));
+        }
+        for (int i = 0; i < 2 * kPairs; ++i) {
+            const int c = 32 * half + 16 * (i & 1), n = m.rows - c;              // rows c .. c + 15 of dims 128 (i / 2) + lane
+            if (n <= 0)
+                continue;
+            float o[16];
+            tmem_ld_32x16(o, lanes + 64 * (i >> 1) + c);
+            const int dim = 128 * (i >> 1) + 32 * quarter + lane;
+            if (!whole) {
+                float *to = g.part + ((size_t)slot * g.cap + c) * L + dim;
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (e < n)
+                        __stcg(to + (size_t)e * L, o[e]);
+                continue;
+            }
+            // lanes 2 i and 2 i + 1 exchange, so that each has two dims of a row
+            uint16_t *to = p.out + (out_row + c + (lane & 1)) * L + (dim & ~1);
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+                const float l0 = s.sum[c + e], l1 = s.sum[c + e + 1];
+                const float a = o[e] * (l0 == 0.0f ? 0.0f : __fdividef(1.0f, l0)), b = o[e + 1] * (l1 == 0.0f ? 0.0f : __fdividef(1.0f, l1));
+                const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
+                if (e + (lane & 1) < n)
+                    *reinterpret_cast<uint32_t *>(to + (size_t)e * L) = lane & 1 ? bf16_pair(other, b) : bf16_pair(a, other);
+            }
+        }
+        fence_before();
+        soft_sync();                                         // also: s.sum and s.ref have been read
+        if (tid == 0)
+            mbar_arrive(s.o_free);
+    }
+    if (tid == 0)
+        g.joins[blockIdx.x] = join;
+}
+
+template <int L>
+__global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_constant__ LatentArgs g, const __grid_constant__ CUtensorMap pair_map,
+                                                             const __grid_constant__ CUtensorMap chunk_map) {
+    extern __shared__ __align__(1024) uint8_t raw_smem[];
+    const LatentSmem<L> s(raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023), g.q_rows, g.slots);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kMaxSlots; ++i) {
+            mbar_init(s.pair_full + i, 1);
+            mbar_init(s.pair_empty + i, 1);
+        }
+        for (int i = 0; i < kRopeSlots; ++i) {
+            mbar_init(s.rope_full + i, 1);
+            mbar_init(s.rope_empty + i, 1);
+        }
+        mbar_init(s.s_full, 1);
+        mbar_init(s.s_full + 1, 1);
+        mbar_init(s.p_ready, 1);
+        mbar_init(s.o_done, 1);
+        mbar_init(s.o_free, 1);
+        mbar_init(s.q_ready, 1);
+        fence_barrier_init();
+    }
+    if (warp == kSoftWarps + 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(s.taddr)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    fence_before();
     __syncthreads();
+    fence_after();
+    const uint32_t tmem = *s.taddr;
+    pdl_wait();
+    pdl_trigger();
+    const Plan pl = *g.a.plan;
+    if (warp < kSoftWarps)
+        latent_softmax<L>(g, pl, s, tmem);
+    else if (warp == kSoftWarps)
+        latent_stream<L>(g, pl, s, &pair_map, &chunk_map);
+    else
+        latent_issue<L>(g, pl, s, tmem);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == kSoftWarps + 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+__global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(AttnArgs a) {
+    extern __shared__ int s_first[];
+    __shared__ long long red[32];
+    pdl_wait();
+    pdl_trigger();
+    make_plan(a, s_first, red, a.recs, a.plan, true);
+}
+
+// The parts of the cut unit that begins in CTA blockIdx.x, in the order of the cache: a row in L / 4 threads.
+constexpr int kJoinThreads = 256;
+template <int L>
+__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentArgs g) {
+    constexpr int kRows = kJoinThreads / (L / 4), U = 8;
+    pdl_wait();
+    pdl_trigger();
+    const LatentJoin j = g.joins[blockIdx.x];
+    const int r = blockIdx.y * kRows + threadIdx.x / (L / 4), d = threadIdx.x % (L / 4);
+    if (r >= j.rows)
+        return;
+    const int part = g.split == 1 ? 0 : (int)blockIdx.x & 1;
+    auto slot = [&](int k) { return (size_t)((k * 2 + (k == j.first)) * g.split + part) * g.cap + r; };
+    float m = -INFINITY;
+    for (int k0 = j.first; k0 <= j.last; k0 += U) {
+        float2 e[U];
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h) {
-        if (h0 + h >= p.heads)
-            break;
-        const float l = s_l[h];
-        const size_t at = (size_t)t * p.heads + h0 + h;
-        for (int d = 0; d < D; ++d) {
-            uint16_t v;
-            asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(v) : "f"(seen > 0 ? o[h][d] / l : 0.0f));
-            p.out[at * L + tid + d * kThreads] = v;
-        }
-        if (tid == 0 && p.lse)
-            p.lse[at] = seen > 0 ? s_m[h] + logf(l) : -INFINITY;
+        for (int u = 0; u < U; ++u)
+            e[u] = k0 + u <= j.last ? __ldcg(g.part_sum + slot(k0 + u)) : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            m = fmaxf(m, e[u].x);
     }
+    float l = 0.0f;
+    float4 o = make_float4(0, 0, 0, 0);
+    for (int k0 = j.first; k0 <= j.last; k0 += U) {
+        float2 e[U];
+        float4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool in = k0 + u <= j.last;
+            e[u] = in ? __ldcg(g.part_sum + slot(k0 + u)) : make_float2(-INFINITY, 0.0f);
+            v[u] = in ? __ldcg(reinterpret_cast<const float4 *>(g.part + slot(k0 + u) * L) + d) : make_float4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (e[u].y == 0.0f)                              // it saw nothing: its sums were not written
+                continue;
+            const float w = ex2((e[u].x - m) * g.factor);
+            l = fmaf(e[u].y, w, l);
+            o.x = fmaf(v[u].x, w, o.x);
+            o.y = fmaf(v[u].y, w, o.y);
+            o.z = fmaf(v[u].z, w, o.z);
+            o.w = fmaf(v[u].w, w, o.w);
+        }
+    }
+    const float by = l == 0.0f ? 0.0f : 1.0f / l;
+    reinterpret_cast<uint2 *>(g.p.out + (j.row + r) * L)[d] = make_uint2(bf16_pair(o.x * by, o.y * by), bf16_pair(o.z * by, o.w * by));
+    if (d == 0 && g.p.lse)
+        g.p.lse[j.row + r] = l == 0.0f ? -INFINITY : fmaf(m, g.p.scale, logf(l));
+}
+
+// How rows become units.  Two CTAs share a unit where a token has more than 64 rows, or requests do on average: the cache is
+// then read from memory once for up to 128 rows.  Units of a single token's heads are even.
+struct Shape {
+    int split, rows, q_rows, cap;
+    Shape(int T, int B, int heads) {
+        const long long all = (long long)T * heads;
+        split = (T <= B ? heads : (all + B - 1) / B) > kMaxRows ? 2 : 1;
+        const int most = split * kMaxRows;
+        if (T <= B) {
+            const int units = (heads + most - 1) / most;
+            rows = (heads + units - 1) / units;
+        } else {
+            rows = most;
+        }
+        q_rows = split == 1 ? rows : (rows + 1) / 2;
+        if (q_rows > all)
+            q_rows = (int)all;
+        q_rows = (q_rows + 15) / 16 * 16;
+        cap = q_rows;
+    }
+};
+
+int max_units(int T, int B, const Shape &s, int heads) { return (int)((long long)T * heads / s.rows + B); }
+
+struct LatentLayout {
+    size_t plan, recs, joins, part, part_sum, total;
+    LatentLayout(int T, int B, int heads, int L) {
+        const Shape s(T, B, heads);
+        size_t o = kInitBytes;
+        auto take = [&](size_t bytes) { o = align_up(o, 256); size_t r = o; o += bytes; return r; };
+        plan = take(sizeof(Plan));
+        recs = take((size_t)max_units(T, B, s, heads) * sizeof(RowTile));
+        joins = take(kMaxAttnCtas * sizeof(LatentJoin));
+        part = take((size_t)2 * kMaxAttnCtas * s.cap * L * sizeof(float));       // a CTA has parts of at most two units
+        part_sum = take((size_t)2 * kMaxAttnCtas * s.cap * sizeof(float2));
+        total = align_up(o, 256);
+    }
+};
+
+template <int L>
+cudaError_t launch(const LatentProblem &p, void *ws, int sms, cudaStream_t stream) {
+    const LatentLayout lay(p.T, p.B, p.heads, L);
+    const Shape shape(p.T, p.B, p.heads);
+    int shift = 4;
+    while ((1 << shift) < p.cache.block_size)
+        ++shift;
+    LatentArgs g{};
+    AttnProblem &ap = g.a.p;                                 // what the plan looks at
+    ap.T = p.T;
+    ap.q_heads = p.heads;
+    ap.cache.num_blocks = p.cache.num_blocks;
+    ap.cache.kv_heads = 1;
+    ap.cache.block_size = p.cache.block_size;
+    ap.table = p.table;
+    ap.max_blocks = p.max_blocks;
+    ap.q_offsets = p.q_offsets;
+    ap.kv_lens = p.kv_lens;
+    ap.B = p.B;
+    ap.causal = p.causal;
+    const int ctas = (sms < kMaxAttnCtas ? sms : kMaxAttnCtas) / shape.split * shape.split;
+    g.a.group = p.heads;
+    g.a.shift = shift;
+    g.a.rows = shape.rows;
+    g.a.ctas = ctas / shape.split;
+    g.a.max_tiles = max_units(p.T, p.B, shape, p.heads);
+    g.a.plan = ws_at<Plan>(ws, lay.plan);
+    g.a.recs = ws_at<RowTile>(ws, lay.recs);
+    g.a.hdr = ws_at<uint32_t>(ws, 0);
+    g.p = p;
+    g.split = shape.split;
+    g.q_rows = shape.q_rows;
+    g.slots = LatentSmem<L>::slots_for(shape.q_rows);
+    g.cap = shape.cap;
+    const double factor = (double)p.scale * 1.44269504088896340736;
+    g.factor = factor < 3.4e38 ? (float)factor : 3.4e38f;
+    g.joins = ws_at<LatentJoin>(ws, lay.joins);
+    g.part = ws_at<float>(ws, lay.part);
+    g.part_sum = ws_at<float2>(ws, lay.part_sum);
+    // the cache as [chunk of 64 dims][slot][64 dims]
+    const uint64_t dims[3] = {64, (uint64_t)p.cache.num_blocks * p.cache.block_size, L / 64 + 1}, strides[2] = {(L + kRopeDims) * 2, 128};
+    uint32_t box[3] = {64, (uint32_t)(p.cache.block_size < kTile ? p.cache.block_size : kTile), 1};
+    CUtensorMap chunk_map, pair_map;
+    cudaError_t e = encode_tiled(&chunk_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.cache.data, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    box[2] = 2;
+    if (e == cudaSuccess)
+        e = encode_tiled(&pair_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.cache.data, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    const size_t smem = LatentSmem<L>::bytes(g.q_rows, g.slots);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(latent_kernel<L>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess)
+        e = launch_pdl(latent_plan_kernel, dim3(1), dim3(kPlanThreads), p.B * sizeof(int), stream, g.a);
+    if (e == cudaSuccess)
+        e = launch_pdl(latent_kernel<L>, dim3(ctas), dim3(kThreads), smem, stream, g, pair_map, chunk_map);
+    constexpr int kRows = kJoinThreads / (L / 4);
+    return e != cudaSuccess ? e : launch_pdl(latent_join_kernel<L>, dim3(ctas, (shape.cap + kRows - 1) / kRows), dim3(kJoinThreads), 0, stream, g);
 }
 
 }  // namespace
 
-size_t latent_attention_workspace(int, int, int, int) { return align_up(kInitBytes, 256); }
+size_t latent_attention_workspace(int T, int B, int heads, int latent_dim) {
+    return T == 0 || B == 0 ? align_up(kInitBytes, 256) : LatentLayout(T, B, heads, latent_dim).total;
+}
 
-cudaError_t launch_latent_attention(const LatentProblem &p, void *ws, int, cudaStream_t stream) {
-    const dim3 grid(p.T, (p.heads + kHeads - 1) / kHeads);
-    auto go = [&](auto kernel, int W) {
-        const size_t smem = (size_t)(kHeads + kTokens) * (W + 2) * 2;
-        cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        return r != cudaSuccess ? r : launch_pdl(kernel, grid, dim3(kThreads), smem, stream, p, ws_at<uint32_t>(ws, 0));
-    };
-    return p.cache.latent_dim == 256 ? go(latent_plain_kernel<256>, 256 + kRopeDims) : go(latent_plain_kernel<512>, 512 + kRopeDims);
+cudaError_t launch_latent_attention(const LatentProblem &p, void *ws, int sms, cudaStream_t stream) {
+    return p.cache.latent_dim == 256 ? launch<256>(p, ws, sms, stream) : launch<512>(p, ws, sms, stream);
 }
 
 }  // namespace moe
