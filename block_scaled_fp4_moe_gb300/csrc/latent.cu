@@ -132,25 +132,32 @@ struct Mine {
 
 // ------------------------------------------------------------------ tcgen05
 
-// Rows of 128 bytes in swizzled atoms of 8, the summed axis along the row.
-__device__ __forceinline__ uint64_t desc_along(uint32_t addr) {
-    return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-// The same bytes with the summed axis across the rows; 64 further elements along the row lie a chunk further on.
-__device__ __forceinline__ uint64_t desc_across(uint32_t addr) {
-    return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(kChunkBytes >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
+// Operand descriptors, rows of 128 bytes in swizzled atoms of 8.  Low word: address, and the distance of 64 further elements along the
+// row where the summed axis runs across the rows (a chunk; not used where it runs along).  The high word is the same for all.
+constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_along(uint32_t addr) { return ((addr & 0x3FFFF) >> 4) | 1u << 16; }
+__device__ __forceinline__ uint32_t desc_across(uint32_t addr) { return ((addr & 0x3FFFF) >> 4) | (uint32_t)(kChunkBytes >> 4) << 16; }
 
 // fp32 sums of bf16 products; across: both operands are read across their rows.
 __device__ __forceinline__ uint32_t idesc_bf16(int m, int n, bool across) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (across ? (1u << 15) | (1u << 16) : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
 }
 
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Four products in a row, the operands' addresses STEP 16-byte units apart, issued by one elected lane of a converged warp.
+template <int STEP>
+__device__ __forceinline__ void mma4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n.reg .pred p, q;\nelect.sync _|p, 0xffffffff;\nsetp.ne.b32 q, %4, 0;\n"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n.reg .pred p, q;\n.reg .b64 a, b;\n.reg .b32 x, y;\n"
+        "elect.sync _|p, 0xffffffff;\nsetp.ne.b32 q, %4, 0;\n"
+        "mov.b64 a, {%1, %5};\nmov.b64 b, {%2, %5};\n"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n"
+        "add.u32 x, %1, %6;\nadd.u32 y, %2, %6;\nmov.b64 a, {x, %5};\nmov.b64 b, {y, %5};\n"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, 1;\n"
+        "add.u32 x, x, %6;\nadd.u32 y, y, %6;\nmov.b64 a, {x, %5};\nmov.b64 b, {y, %5};\n"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, 1;\n"
+        "add.u32 x, x, %6;\nadd.u32 y, y, %6;\nmov.b64 a, {x, %5};\nmov.b64 b, {y, %5};\n"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, 1;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHigh), "n"(STEP)
         : "memory");
 }
 
@@ -221,6 +228,17 @@ __device__ __forceinline__ bool soft_any(bool v) {
         : "r"((uint32_t)v), "r"(kSoft)
         : "memory");
     return r != 0;
+}
+
+// Whether a phase has ended, at once.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 // Waits of a role's warp; after one that gave up it waits no more.
@@ -318,7 +336,7 @@ __device__ __forceinline__ void latent_issue(const LatentArgs &g, const Plan &pl
     Walk walk(g.a, pl, g.a.recs, (int)blockIdx.x / g.split);
     Piece pc;
     uint32_t sp = 0, op = 0, ropes = 0, tiles = 0, weights = 0, units = 0;       // pairs met by the first and by the second product, ...
-    const uint64_t dp = desc_across(smem_u32(s.p));
+    const uint32_t dp = desc_across(smem_u32(s.p));
     while (walk.next(pc)) {
         const Mine m(g, pc);
         if (m.tiles == 0)
@@ -332,12 +350,8 @@ __device__ __forceinline__ void latent_issue(const LatentArgs &g, const Plan &pl
                 wait(s.o_free, (units - 1) & 1);
             for (int i = 0; i < kPairs; ++i, ++op) {
                 const uint32_t slot = op % g.slots;
-                const uint64_t dv = desc_across(smem_u32(s.ring + (size_t)slot * 2 * kChunkBytes));
-                if (!wait.dead) {
-#pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        mma(tmem + 64 * i, dv + k * (16 * 128 >> 4), dp + k * (16 * 128 >> 4), io, !first || k > 0);
-                }
+                if (!wait.dead)
+                    mma4<16 * 128 / 16>(tmem + 64 * i, desc_across(smem_u32(s.ring + (size_t)slot * 2 * kChunkBytes)), dp, io, !first);
                 commit(s.pair_empty + slot);
             }
             commit(s.o_done);
@@ -346,35 +360,33 @@ __device__ __forceinline__ void latent_issue(const LatentArgs &g, const Plan &pl
         for (int t = 0; t < m.tiles; ++t, ++tiles, ++ropes) {
             const uint32_t d = tmem + kSCol + 64 * (tiles & 1);
             const uint64_t begun = globaltimer_ns();
-            // while the tile is on its way the weights of the one before may come first
+            // the tile before comes first if its weights are there when a part of this tile is
             auto arrived = [&](uint64_t *bar, uint32_t parity) {
-                while (pending && !wait.dead && !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
-                    if (__all_sync(0xffffffffu, mbar_try_wait(s.p_ready, weights & 1))) {
+                while (pending && !wait.dead) {
+                    const bool here = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+                    if (__all_sync(0xffffffffu, mbar_test_wait(s.p_ready, weights & 1))) {
                         fence_after();
                         ++weights;
                         values(t == 1);
                         pending = false;
-                    } else if (globaltimer_ns() - begun > kWaitLimitNs) {
+                    } else if (here || globaltimer_ns() - begun > kWaitLimitNs) {
                         break;
                     }
+                }
                 wait(bar, parity);
             };
             const uint32_t rs = ropes % kRopeSlots;
             arrived(s.rope_full + rs, (ropes / kRopeSlots) & 1);
-            const uint64_t dq = desc_along(smem_u32(s.q)), dr = desc_along(smem_u32(s.rope + rs * kChunkBytes));
-            if (!wait.dead) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma(d, dr + k * 2, dq + (L / 64) * (q_chunk >> 4) + k * 2, is, k > 0);
-            }
+            const uint32_t dq = desc_along(smem_u32(s.q));
+            if (!wait.dead)
+                mma4<2>(d, desc_along(smem_u32(s.rope + rs * kChunkBytes)), dq + (L / 64) * (q_chunk >> 4), is, 0);
             for (int i = 0; i < kPairs; ++i, ++sp) {
                 const uint32_t slot = sp % g.slots;
                 arrived(s.pair_full + slot, (sp / g.slots) & 1);
-                const uint64_t dk = desc_along(smem_u32(s.ring + (size_t)slot * 2 * kChunkBytes));
+                const uint32_t dk = desc_along(smem_u32(s.ring + (size_t)slot * 2 * kChunkBytes));
                 if (!wait.dead) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma(d, dk + (k >> 2) * (kChunkBytes >> 4) + (k & 3) * 2, dq + (2 * i + (k >> 2)) * (q_chunk >> 4) + (k & 3) * 2, is, 1);
+                    mma4<2>(d, dk, dq + 2 * i * (q_chunk >> 4), is, 1);
+                    mma4<2>(d, dk + (kChunkBytes >> 4), dq + (2 * i + 1) * (q_chunk >> 4), is, 1);
                 }
             }
             commit(s.s_full + (tiles & 1));
