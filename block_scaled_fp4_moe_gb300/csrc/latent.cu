@@ -27,7 +27,8 @@
 // the last CTA alone would be a while at it).  With more than 64 rows a token two CTAs take the halves of a
 // unit's rows, side by side, so that the second reads the cache from L2.
 //
-// Warps: 0..7 softmax (warp % 4 = lane quarter, 16 tokens each; warp / 4 = half of the rows), 8 streams the cache, 9 issues the products.
+// Warps: 0..7 softmax (warp % 4 = lane quarter, 16 tokens each; warp / 4 = half of the rows), 8 streams the cache, 9 and 10 issue the products
+// (one warp for both was often at the scores' when weights were ready: 64 requests of 16,384 tokens, 64 heads, 292 us).
 #define MOE_PLAN_TILE 64
 #define MOE_PLAN_UNIT_COST 3
 #define MOE_PLAN_MIN_COST 4
@@ -36,7 +37,7 @@
 namespace moe {
 namespace {
 
-constexpr int kSoftWarps = 8, kThreads = (kSoftWarps + 2) * 32, kSoft = kSoftWarps * 32;
+constexpr int kSoftWarps = 8, kThreads = (kSoftWarps + 3) * 32, kSoft = kSoftWarps * 32;
 constexpr int kMaxRows = 64;                 // of a CTA's unit
 constexpr int kChunkBytes = kTile * 128;     // 64 dims of a tile
 constexpr int kMaxSlots = 12;                // pairs of chunks in the ring
@@ -93,7 +94,7 @@ struct LatentSmem {
         rope_empty = rope_full + kRopeSlots;
         s_full = rope_empty + kRopeSlots;
         p_ready = s_full + 2;
-        o_done = p_ready + 1;
+        o_done = p_ready + 2;
         o_free = o_done + 1;
         q_ready = o_free + 1;
         ref = reinterpret_cast<float *>(s_full + 8);
@@ -230,17 +231,6 @@ __device__ __forceinline__ bool soft_any(bool v) {
     return r != 0;
 }
 
-// Whether a phase has ended, at once.
-__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 // Waits of a role's warp; after one that gave up it waits no more.
 struct Waiter {
     uint32_t *hdr;
@@ -329,81 +319,87 @@ __device__ __forceinline__ void latent_stream(const LatentArgs &g, const Plan &p
 
 // --------------------------------------------------------------- products
 
+// A place in a ring of slots, and the parity of its full barrier.
+struct Place {
+    uint32_t slot = 0, parity = 0;
+    __device__ void next(uint32_t slots) {
+        if (++slot == slots) {
+            slot = 0;
+            parity ^= 1;
+        }
+    }
+};
+
+// S^T = K Q^T
 template <int L>
-__device__ __forceinline__ void latent_issue(const LatentArgs &g, const Plan &pl, const LatentSmem<L> &s, uint32_t tmem) {
+__device__ __forceinline__ void latent_scores(const LatentArgs &g, const Plan &pl, const LatentSmem<L> &s, uint32_t tmem) {
     constexpr int kPairs = LatentSmem<L>::kPairs;
     Waiter wait{g.a.hdr, false};
     Walk walk(g.a, pl, g.a.recs, (int)blockIdx.x / g.split);
     Piece pc;
-    uint32_t sp = 0, op = 0, ropes = 0, tiles = 0, weights = 0, units = 0;       // pairs met by the first and by the second product, ...
+    Place pair, rope;
+    uint32_t tiles = 0, units = 0;
+    const uint32_t q_chunk = (uint32_t)g.q_rows * 128 / 16, dq = desc_along(smem_u32(s.q));
+    while (walk.next(pc)) {
+        const Mine m(g, pc);
+        if (m.tiles == 0)
+            continue;
+        const uint32_t is = idesc_bf16(kTile, m.n_side, false);
+        wait(s.q_ready, units & 1);
+        ++units;
+        for (int t = 0; t < m.tiles; ++t, ++tiles) {
+            const uint32_t d = tmem + kSCol + 64 * (tiles & 1);
+            if (tiles >= 2)                        // the weights of the scores that were here have been made
+                wait(s.p_ready + (tiles & 1), ((tiles >> 1) - 1) & 1);
+            wait(s.rope_full + rope.slot, rope.parity);
+            if (!wait.dead)
+                mma4<2>(d, desc_along(smem_u32(s.rope + rope.slot * kChunkBytes)), dq + (L / 64) * q_chunk, is, 0);
+            commit(s.rope_empty + rope.slot);
+            rope.next(kRopeSlots);
+            for (int i = 0; i < kPairs; ++i) {
+                const uint32_t dk = desc_along(smem_u32(s.ring + (size_t)pair.slot * 2 * kChunkBytes));
+                wait(s.pair_full + pair.slot, pair.parity);
+                if (!wait.dead) {
+                    mma4<2>(d, dk, dq + 2 * i * q_chunk, is, 1);
+                    mma4<2>(d, dk + (kChunkBytes >> 4), dq + (2 * i + 1) * q_chunk, is, 1);
+                }
+                pair.next(g.slots);
+            }
+            commit(s.s_full + (tiles & 1));
+        }
+    }
+    if (tiles > 0)                                 // issued products end before the CTA's memory goes away
+        wait(s.s_full + ((tiles - 1) & 1), ((tiles - 1) >> 1) & 1);
+}
+
+// O^T += C^T P^T
+template <int L>
+__device__ __forceinline__ void latent_values(const LatentArgs &g, const Plan &pl, const LatentSmem<L> &s, uint32_t tmem) {
+    Waiter wait{g.a.hdr, false};
+    Walk walk(g.a, pl, g.a.recs, (int)blockIdx.x / g.split);
+    Piece pc;
+    Place pair;
+    uint32_t tiles = 0, units = 0;
     const uint32_t dp = desc_across(smem_u32(s.p));
     while (walk.next(pc)) {
         const Mine m(g, pc);
         if (m.tiles == 0)
             continue;
-        const uint32_t is = idesc_bf16(kTile, m.n_side, false), io = idesc_bf16(128, m.n_side, true);
-        const int q_chunk = g.q_rows * 128;
-        wait(s.q_ready, units & 1);
-        // O^T += C^T P^T of the oldest tile whose weights are there
-        auto values = [&](bool first) {
-            if (first && units > 0)
-                wait(s.o_free, (units - 1) & 1);
-            for (int i = 0; i < kPairs; ++i, ++op) {
-                const uint32_t slot = op % g.slots;
+        const uint32_t io = idesc_bf16(128, m.n_side, true);
+        if (units > 0)
+            wait(s.o_free, (units - 1) & 1);
+        ++units;
+        for (int t = 0; t < m.tiles; ++t, ++tiles) {
+            wait(s.p_ready + (tiles & 1), (tiles >> 1) & 1);
+            for (int i = 0; i < LatentSmem<L>::kPairs; ++i) {
                 if (!wait.dead)
-                    mma4<16 * 128 / 16>(tmem + 64 * i, desc_across(smem_u32(s.ring + (size_t)slot * 2 * kChunkBytes)), dp, io, !first);
-                commit(s.pair_empty + slot);
+                    mma4<16 * 128 / 16>(tmem + 64 * i, desc_across(smem_u32(s.ring + (size_t)pair.slot * 2 * kChunkBytes)), dp, io, t > 0);
+                commit(s.pair_empty + pair.slot);
+                pair.next(g.slots);
             }
             commit(s.o_done);
-        };
-        bool pending = false;                      // a tile's second product is to be issued
-        for (int t = 0; t < m.tiles; ++t, ++tiles, ++ropes) {
-            const uint32_t d = tmem + kSCol + 64 * (tiles & 1);
-            const uint64_t begun = globaltimer_ns();
-            // the tile before comes first if its weights are there when a part of this tile is
-            auto arrived = [&](uint64_t *bar, uint32_t parity) {
-                while (pending && !wait.dead) {
-                    const bool here = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
-                    if (__all_sync(0xffffffffu, mbar_test_wait(s.p_ready, weights & 1))) {
-                        fence_after();
-                        ++weights;
-                        values(t == 1);
-                        pending = false;
-                    } else if (here || globaltimer_ns() - begun > kWaitLimitNs) {
-                        break;
-                    }
-                }
-                wait(bar, parity);
-            };
-            const uint32_t rs = ropes % kRopeSlots;
-            arrived(s.rope_full + rs, (ropes / kRopeSlots) & 1);
-            const uint32_t dq = desc_along(smem_u32(s.q));
-            if (!wait.dead)
-                mma4<2>(d, desc_along(smem_u32(s.rope + rs * kChunkBytes)), dq + (L / 64) * (q_chunk >> 4), is, 0);
-            for (int i = 0; i < kPairs; ++i, ++sp) {
-                const uint32_t slot = sp % g.slots;
-                arrived(s.pair_full + slot, (sp / g.slots) & 1);
-                const uint32_t dk = desc_along(smem_u32(s.ring + (size_t)slot * 2 * kChunkBytes));
-                if (!wait.dead) {
-                    mma4<2>(d, dk, dq + 2 * i * (q_chunk >> 4), is, 1);
-                    mma4<2>(d, dk + (kChunkBytes >> 4), dq + (2 * i + 1) * (q_chunk >> 4), is, 1);
-                }
-            }
-            commit(s.s_full + (tiles & 1));
-            commit(s.rope_empty + rs);
-            if (pending) {
-                wait(s.p_ready, weights & 1);
-                ++weights;
-                values(t == 1);
-            }
-            pending = true;
         }
-        wait(s.p_ready, weights & 1);
-        ++weights;
-        values(m.tiles == 1);
-        ++units;
     }
-    // issued products end before the CTA's memory goes away
     if (tiles > 0)
         wait(s.o_done, (tiles - 1) & 1);
 }
@@ -610,7 +606,7 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Plan &
                 soft_sync();
             }
             if (tid == 0)
-                mbar_arrive(s.p_ready);
+                mbar_arrive(s.p_ready + (tiles & 1));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (i < groups)
@@ -695,6 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
         mbar_init(s.s_full, 1);
         mbar_init(s.s_full + 1, 1);
         mbar_init(s.p_ready, 1);
+        mbar_init(s.p_ready + 1, 1);
         mbar_init(s.o_done, 1);
         mbar_init(s.o_free, 1);
         mbar_init(s.q_ready, 1);
@@ -715,8 +712,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
         latent_softmax<L>(g, pl, s, tmem);
     else if (warp == kSoftWarps)
         latent_stream<L>(g, pl, s, &pair_map, &chunk_map);
+    else if (warp == kSoftWarps + 1)
+        latent_scores<L>(g, pl, s, tmem);
     else
-        latent_issue<L>(g, pl, s, tmem);
+        latent_values<L>(g, pl, s, tmem);
     fence_before();
     __syncthreads();
     fence_after();
