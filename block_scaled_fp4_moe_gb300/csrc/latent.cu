@@ -245,6 +245,17 @@ struct Waiter {
     }
 };
 
+// A place in a ring of slots, and the parity of its full barrier.
+struct Place {
+    uint32_t slot = 0, parity = 0;
+    __device__ void next(uint32_t slots) {
+        if (++slot == slots) {
+            slot = 0;
+            parity ^= 1;
+        }
+    }
+};
+
 // ------------------------------------------------------------ the cache's tiles
 
 template <int L>
@@ -256,7 +267,9 @@ __device__ __forceinline__ void latent_stream(const LatentArgs &g, const Plan &p
     Waiter wait{g.a.hdr, false};
     Walk walk(g.a, pl, g.a.recs, (int)blockIdx.x / g.split);
     Piece pc;
+    Place pair, rope;
     uint32_t pairs = 0, ropes = 0;
+    const int sub = lane % subs, chunk = lane / subs;      // of a tile's boxes, this lane's
     while (walk.next(pc)) {
         const Mine m(g, pc);
         const int32_t *row = p.table + (size_t)pc.request * p.max_blocks;
@@ -279,34 +292,34 @@ __device__ __forceinline__ void latent_stream(const LatentArgs &g, const Plan &p
                 at = used ? (page << g.a.shift) + (int)(tok & ((1 << g.a.shift) - 1)) : -1;
                 next = box + 32 < m.tiles * subs ? fetch(box + 32) : -1;
             }
+            const int to = __shfl_sync(0xffffffffu, at, (box & 31) + sub);
             // boxes of this tile that hold something
             const int live = min(subs, (m.hi_max - (m.tok0 + t * kTile) + (1 << box_shift) - 1) >> box_shift);
             const uint32_t chunk_bytes = (uint32_t)(live << box_shift) * 128;
-            auto load = [&](uint8_t *dst, uint64_t *bar, int c, int n) {         // chunks c .. c + n - 1
+            // chunks c .. c + n - 1
+            auto load = [&](uint8_t *dst, uint64_t *full, uint64_t *empty, uint32_t parity, bool used, int c, int n) {
+                if (used)
+                    wait(empty, parity);
                 if (lane == 0)
-                    mbar_arrive_expect_tx(bar, chunk_bytes * n);
-                __syncwarp();
-                const int sub = lane % subs, k = lane / subs;
-                const int to = __shfl_sync(0xffffffffu, at, (box & 31) + sub);
+                    mbar_arrive_expect_tx(full, chunk_bytes * n);
+                if (subs > 1)
+                    __syncwarp();
                 if (wait.dead)
                     return;
                 if (subs == 1) {
                     if (lane == 0)
-                        copy_box(smem_u32(dst), n == 2 ? pair_map : chunk_map, to, c, bar);
-                } else if (k < n && sub < live) {
-                    copy_box(smem_u32(dst + k * kChunkBytes + (sub << box_shift) * 128), chunk_map, to, c + k, bar);
+                        copy_box(smem_u32(dst), n == 2 ? pair_map : chunk_map, to, c, full);
+                } else if (chunk < n && sub < live) {
+                    copy_box(smem_u32(dst + chunk * kChunkBytes + (sub << box_shift) * 128), chunk_map, to, c + chunk, full);
                 }
             };
-            const uint32_t rs = ropes % kRopeSlots;
-            if (ropes >= kRopeSlots)
-                wait(s.rope_empty + rs, (ropes / kRopeSlots - 1) & 1);
-            load(s.rope + rs * kChunkBytes, s.rope_full + rs, L / 64, 1);
+            load(s.rope + rope.slot * kChunkBytes, s.rope_full + rope.slot, s.rope_empty + rope.slot, rope.parity ^ 1, ropes >= kRopeSlots, L / 64, 1);
+            rope.next(kRopeSlots);
             ++ropes;
             for (int i = 0; i < LatentSmem<L>::kPairs; ++i, ++pairs) {
-                const uint32_t slot = pairs % g.slots, turn = pairs / g.slots;
-                if (turn > 0)
-                    wait(s.pair_empty + slot, (turn - 1) & 1);
-                load(s.ring + (size_t)slot * 2 * kChunkBytes, s.pair_full + slot, 2 * i, 2);
+                load(s.ring + pair.slot * (2 * kChunkBytes), s.pair_full + pair.slot, s.pair_empty + pair.slot, pair.parity ^ 1, pairs >= (uint32_t)g.slots,
+                     2 * i, 2);
+                pair.next(g.slots);
             }
         }
     }
@@ -318,17 +331,6 @@ __device__ __forceinline__ void latent_stream(const LatentArgs &g, const Plan &p
 }
 
 // --------------------------------------------------------------- products
-
-// A place in a ring of slots, and the parity of its full barrier.
-struct Place {
-    uint32_t slot = 0, parity = 0;
-    __device__ void next(uint32_t slots) {
-        if (++slot == slots) {
-            slot = 0;
-            parity ^= 1;
-        }
-    }
-};
 
 // S^T = K Q^T
 template <int L>
