@@ -246,7 +246,9 @@ struct Walk {
     long long pos, end, base, per;
     int rt, head, n_recs, cta;
     RowTile r;
-    __device__ Walk(const AttnArgs &args, const Plan &pl, const RowTile *tiles, int which = (int)blockIdx.x) : a(args), recs(tiles), cta(which) {
+    // wide: by a converged warp, row tiles in global memory; the search looks at 32 of them at a time
+    __device__ Walk(const AttnArgs &args, const Plan &pl, const RowTile *tiles, int which = (int)blockIdx.x, bool wide = false)
+        : a(args), recs(tiles), cta(which) {
         n_recs = pl.row_tiles;
         per = pl.per;
         pos = (long long)cta * per;
@@ -255,6 +257,12 @@ struct Walk {
         if (cta >= pl.ctas || pos >= pl.work)
             return;
         int lo = 0, hi = n_recs;                // the last row tile with before <= pos
+        while (wide && hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32, i = lo + (int)(threadIdx.x & 31) * step;
+            const int n = __popc(__ballot_sync(0xffffffffu, i < hi && recs[i].before <= pos));       // the first always is
+            hi = min(hi, lo + n * step);
+            lo += (n - 1) * step;
+        }
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (recs[mid].before <= pos)

@@ -265,7 +265,7 @@ __device__ __forceinline__ void latent_stream(const LatentArgs &g, const Plan &p
     const int lane = threadIdx.x & 31;
     const int box_shift = min(g.a.shift, 6), subs = kTile >> box_shift;          // a box's rows lie in one block
     Waiter wait{g.a.hdr, false};
-    Walk walk(g.a, pl, g.a.recs, (int)blockIdx.x / g.split);
+    Walk walk(g.a, pl, g.a.recs, (int)blockIdx.x / g.split, true);
     Piece pc;
     Place pair, rope;
     uint32_t pairs = 0, ropes = 0;
@@ -337,7 +337,7 @@ template <int L>
 __device__ __forceinline__ void latent_scores(const LatentArgs &g, const Plan &pl, const LatentSmem<L> &s, uint32_t tmem) {
     constexpr int kPairs = LatentSmem<L>::kPairs;
     Waiter wait{g.a.hdr, false};
-    Walk walk(g.a, pl, g.a.recs, (int)blockIdx.x / g.split);
+    Walk walk(g.a, pl, g.a.recs, (int)blockIdx.x / g.split, true);
     Piece pc;
     Place pair, rope;
     uint32_t tiles = 0, units = 0;
@@ -378,7 +378,7 @@ __device__ __forceinline__ void latent_scores(const LatentArgs &g, const Plan &p
 template <int L>
 __device__ __forceinline__ void latent_values(const LatentArgs &g, const Plan &pl, const LatentSmem<L> &s, uint32_t tmem) {
     Waiter wait{g.a.hdr, false};
-    Walk walk(g.a, pl, g.a.recs, (int)blockIdx.x / g.split);
+    Walk walk(g.a, pl, g.a.recs, (int)blockIdx.x / g.split, true);
     Piece pc;
     Place pair;
     uint32_t tiles = 0, units = 0;
@@ -420,9 +420,10 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Plan &
     const int tok_a = 16 * quarter + (lane >> 2);           // its tokens of a tile: tok_a + 8 k
     const float f = g.factor;
     Waiter wait{g.a.hdr, false};
-    Walk walk(g.a, pl, g.a.recs, cta);
+    Walk walk(g.a, pl, g.a.recs, cta, true);
     Piece pc;
     LatentJoin join{0, 0, 0, 0};
+    bool stored = false;                                     // results on their way out of the query buffer
     uint32_t tiles = 0;                                      // so far
     while (walk.next(pc)) {
         const Mine m(g, pc);
@@ -445,23 +446,37 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Plan &
             }
             continue;
         }
-        // queries, zero past the last row; the scores of the unit before are all made
-        for (int i = tid; i < m.n_side * (L / 8 + 8); i += kSoft) {
-            const int r = i / (L / 8 + 8), c = i % (L / 8 + 8);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (r < m.rows) {
-                const int64_t t = pc.q0 + (m.row0 + r) / p.heads, h = (m.row0 + r) % p.heads;
-                v = c < L / 8 ? __ldg(reinterpret_cast<const uint4 *>(p.ql + t * p.ql_st + h * p.ql_sh) + c)
-                              : __ldg(reinterpret_cast<const uint4 *>(p.qr + t * p.qr_st + h * p.qr_sh) + c - L / 8);
-            }
-            *reinterpret_cast<uint4 *>(s.q + (size_t)(c >> 3) * g.q_rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+        // queries, zero past the last row, a warp a row and all rows' copies in flight together; the scores of the unit before are all
+        // made, and its results have left the buffer
+        if (stored) {
+            if (tid == 0)
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            soft_sync();
+            stored = false;
         }
+        for (int r = warp; r < m.n_side; r += kSoftWarps) {
+            const int64_t t = pc.q0 + (m.row0 + r) / p.heads, h = (m.row0 + r) % p.heads;
+            const uint16_t *ql = p.ql + t * p.ql_st + h * p.ql_sh, *qr = p.qr + t * p.qr_st + h * p.qr_sh;
+#pragma unroll
+            for (int k = 0; k < (L / 8 + 8 + 31) / 32; ++k) {
+                const int c = lane + 32 * k;
+                uint8_t *to = s.q + (size_t)(c >> 3) * g.q_rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+                if (c < L / 8 + 8) {
+                    if (r < m.rows)
+                        cp_async16(to, c < L / 8 ? ql + 8 * c : qr + (8 * c - L));
+                    else
+                        *reinterpret_cast<uint4 *>(to) = make_uint4(0, 0, 0, 0);
+                }
+            }
+        }
+        cp_async_commit();
         if (tid < kMaxRows) {
             int lo, hi = m.hi_max;
             if (tid < m.rows)
                 row_range(g.a.p, g.a.group, pc.kv, pc.n, m.row0 + tid, lo, hi);
             s.hi[tid] = hi;
         }
+        cp_async_wait<0>();
         fence_async();
         soft_sync();
         if (tid == 0)
@@ -630,47 +645,63 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Plan &
                 s.ref[col] = ref[i];
         }
         soft_sync();
-        if (tid < kMaxRows)
-            s.sum[tid] = (s.red[tid] + s.red[64 + tid]) + (s.red[128 + tid] + s.red[192 + tid]);
-        soft_sync();
         if (tid < m.rows) {
-            const float l = s.sum[tid];
+            const float l = (s.red[tid] + s.red[64 + tid]) + (s.red[128 + tid] + s.red[192 + tid]);
+            s.sum[tid] = l == 0.0f ? 0.0f : 1.0f / l;
             if (!whole)
                 __stcg(g.part_sum + (size_t)slot * g.cap + tid, make_float2(l == 0.0f ? -INFINITY : s.ref[tid], l));
             else if (p.lse)
                 p.lse[out_row + tid] = l == 0.0f ? -INFINITY : fmaf(s.ref[tid], p.scale, logf(l));
         }
-        for (int i = 0; i < 2 * kPairs; ++i) {
-            const int c = 32 * half + 16 * (i & 1), n = m.rows - c;              // rows c .. c + 15 of dims 128 (i / 2) + lane
-            if (n <= 0)
-                continue;
-            float o[16];
-            tmem_ld_32x16(o, lanes + 64 * (i >> 1) + c);
-            const int dim = 128 * (i >> 1) + 32 * quarter + lane;
-            if (!whole) {
-                float *to = g.part + ((size_t)slot * g.cap + c) * L + dim;
+        soft_sync();
+        if (!whole) {
+#pragma unroll 2
+            for (int i = 0; i < 2 * kPairs; ++i) {
+                const int c = 32 * half + 16 * (i & 1), n = m.rows - c;          // rows c .. c + 15 of dims 128 (i / 2) + lane
+                if (n <= 0)
+                    continue;
+                float o[16];
+                tmem_ld_32x16(o, lanes + 64 * (i >> 1) + c);
+                float *to = g.part + ((size_t)slot * g.cap + c) * L + 128 * (i >> 1) + 32 * quarter + lane;
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     if (e < n)
                         __stcg(to + (size_t)e * L, o[e]);
-                continue;
             }
-            // lanes 2 i and 2 i + 1 exchange, so that each has two dims of a row
-            uint16_t *to = p.out + (out_row + c + (lane & 1)) * L + (dim & ~1);
+        } else {
+            // rows of out lie one after the other: they are put together where the queries were, and leave as one copy
+#pragma unroll 2
+            for (int i = 0; i < 2 * kPairs; ++i) {
+                const int c = 32 * half + 16 * (i & 1), n = m.rows - c;
+                if (n <= 0)
+                    continue;
+                float o[16];
+                tmem_ld_32x16(o, lanes + 64 * (i >> 1) + c);
+                const int odd = lane & 1;
+                uint8_t *to = s.q + (size_t)(c + odd) * (2 * L) + 256 * (i >> 1) + 64 * quarter + 4 * (lane >> 1);
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-                const float l0 = s.sum[c + e], l1 = s.sum[c + e + 1];
-                const float a = o[e] * (l0 == 0.0f ? 0.0f : __fdividef(1.0f, l0)), b = o[e + 1] * (l1 == 0.0f ? 0.0f : __fdividef(1.0f, l1));
-                const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
-                if (e + (lane & 1) < n)
-                    *reinterpret_cast<uint32_t *>(to + (size_t)e * L) = lane & 1 ? bf16_pair(other, b) : bf16_pair(a, other);
+                for (int e = 0; e < 16; e += 2) {            // lanes 2 i and 2 i + 1 exchange, so that each has two dims of a row
+                    const float a = o[e] * s.sum[c + e], b = o[e + 1] * s.sum[c + e + 1];
+                    const float other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+                    if (e + odd < n)
+                        *reinterpret_cast<uint32_t *>(to + e * (2 * L)) = odd ? bf16_pair(other, b) : bf16_pair(a, other);
+                }
             }
+            fence_async();
+            stored = true;
         }
         fence_before();
         soft_sync();                                         // also: s.sum and s.ref have been read
-        if (tid == 0)
+        if (tid == 0) {
             mbar_arrive(s.o_free);
+            if (stored)
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\ncp.async.bulk.commit_group;" ::"l"(p.out + out_row * L),
+                             "r"(smem_u32(s.q)), "r"((uint32_t)m.rows * (2 * L))
+                             : "memory");
+        }
     }
+    if (stored && tid == 0)
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (tid == 0)
         g.joins[blockIdx.x] = join;
 }
