@@ -316,6 +316,7 @@ __device__ __forceinline__ void latent_stream(const LatentArgs &g, const Plan &p
             load(s.rope + rope.slot * kChunkBytes, s.rope_full + rope.slot, s.rope_empty + rope.slot, rope.parity ^ 1, ropes >= kRopeSlots, L / 64, 1);
             rope.next(kRopeSlots);
             ++ropes;
+#pragma unroll 1
             for (int i = 0; i < LatentSmem<L>::kPairs; ++i, ++pairs) {
                 load(s.ring + pair.slot * (2 * kChunkBytes), s.pair_full + pair.slot, s.pair_empty + pair.slot, pair.parity ^ 1, pairs >= (uint32_t)g.slots,
                      2 * i, 2);
@@ -358,6 +359,7 @@ __device__ __forceinline__ void latent_scores(const LatentArgs &g, const Plan &p
                 mma4<2>(d, desc_along(smem_u32(s.rope + rope.slot * kChunkBytes)), dq + (L / 64) * q_chunk, is, 0);
             commit(s.rope_empty + rope.slot);
             rope.next(kRopeSlots);
+#pragma unroll 1
             for (int i = 0; i < kPairs; ++i) {
                 const uint32_t dk = desc_along(smem_u32(s.ring + (size_t)pair.slot * 2 * kChunkBytes));
                 wait(s.pair_full + pair.slot, pair.parity);
@@ -393,6 +395,7 @@ __device__ __forceinline__ void latent_values(const LatentArgs &g, const Plan &p
         ++units;
         for (int t = 0; t < m.tiles; ++t, ++tiles) {
             wait(s.p_ready + (tiles & 1), (tiles >> 1) & 1);
+#pragma unroll 1
             for (int i = 0; i < LatentSmem<L>::kPairs; ++i) {
                 if (!wait.dead)
                     mma4<16 * 128 / 16>(tmem + 64 * i, desc_across(smem_u32(s.ring + (size_t)pair.slot * 2 * kChunkBytes)), dp, io, t > 0);
@@ -539,38 +542,38 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Plan &
             if (t > 0)                                       // the weights before have been read
                 wait(s.o_done, (tiles - 1) & 1);
             float w[16];
-            auto weigh = [&]() -> bool {                     // weights of the scores; whether one has grown too far
-                bool grew = false;
+            // weights of the scores, two columns in an instruction; whether one has grown too far
+            auto weigh = [&]() -> bool {
+                float most = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (i < groups) {
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const float y = (x[4 * i + 2 * k + e] - ref[2 * i + e]) * f;
-                                float v = ex2(y);
-                                bool up = y > kMostPower;
-                                if (edge) {
-                                    const int j = tok_a + 8 * k;
-                                    const bool sees = tok + j < s.hi[col0 + 8 * i + e];
-                                    if (s.bad[j / 32] >> (j & 31) & 1)
-                                        v = __uint_as_float(0x7FFFFFFFu);
-                                    v = sees ? v : 0.0f;
-                                    up &= sees;
-                                }
-                                w[4 * i + 2 * k + e] = v;
-                                grew |= up;
-                            }
-#pragma unroll
                         for (int k = 0; k < 2; ++k) {
+                            float y0, y1;
+                            asm("{\n.reg .b64 a, b;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nadd.rn.f32x2 a, a, b;\nmov.b64 b, {%6, %6};\n"
+                                "mul.rn.f32x2 a, a, b;\nmov.b64 {%0, %1}, a;\n}\n"
+                                : "=f"(y0), "=f"(y1)
+                                : "f"(x[4 * i + 2 * k]), "f"(x[4 * i + 2 * k + 1]), "f"(-ref[2 * i]), "f"(-ref[2 * i + 1]), "f"(f));
+                            float v0 = ex2(y0), v1 = ex2(y1);
                             const int j = tok_a + 8 * k, c = col0 + 8 * i;       // 8 columns are 16 bytes
-                            *reinterpret_cast<uint32_t *>(s.p + j * 128 + (((c >> 3) ^ (j & 7)) << 4) + (c & 7) * 2) =
-                                bf16_pair(w[4 * i + 2 * k], w[4 * i + 2 * k + 1]);
+                            if (edge) {
+                                const bool sees0 = tok + j < s.hi[c], sees1 = tok + j < s.hi[c + 1];
+                                if (s.bad[j / 32] >> (j & 31) & 1)
+                                    v0 = v1 = __uint_as_float(0x7FFFFFFFu);
+                                v0 = sees0 ? v0 : 0.0f;
+                                v1 = sees1 ? v1 : 0.0f;
+                                y0 = sees0 ? y0 : -INFINITY;
+                                y1 = sees1 ? y1 : -INFINITY;
+                            }
+                            w[4 * i + 2 * k] = v0;
+                            w[4 * i + 2 * k + 1] = v1;
+                            most = fmaxf(most, fmaxf(y0, y1));
+                            *reinterpret_cast<uint32_t *>(s.p + j * 128 + (((c >> 3) ^ (j & 7)) << 4) + (c & 7) * 2) = bf16_pair(v0, v1);
                         }
                     }
                 fence_async();
-                return grew;
+                return most > kMostPower;
             };
             const bool grew = weigh();
             fence_before();
@@ -607,6 +610,7 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Plan &
                 soft_sync();
                 if (t > 0) {
                     fence_after();
+#pragma unroll 1
                     for (int i = 0; i < 2 * kPairs; ++i)
                         if (16 * (i & 1) < 8 * groups) {
                             float o[16];
@@ -655,7 +659,7 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Plan &
         }
         soft_sync();
         if (!whole) {
-#pragma unroll 2
+#pragma unroll 1
             for (int i = 0; i < 2 * kPairs; ++i) {
                 const int c = 32 * half + 16 * (i & 1), n = m.rows - c;          // rows c .. c + 15 of dims 128 (i / 2) + lane
                 if (n <= 0)
@@ -670,7 +674,7 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Plan &
             }
         } else {
             // rows of out lie one after the other: they are put together where the queries were, and leave as one copy
-#pragma unroll 2
+#pragma unroll 1
             for (int i = 0; i < 2 * kPairs; ++i) {
                 const int c = 32 * half + 16 * (i & 1), n = m.rows - c;
                 if (n <= 0)
