@@ -244,25 +244,17 @@ struct Walk {
     const AttnArgs &a;
     const RowTile *recs;
     long long pos, end, base, per;
-    int rt, head, n_recs, cta;
+    int rt, head, n_recs;
     RowTile r;
-    // wide: by a converged warp, row tiles in global memory; the search looks at 32 of them at a time
-    __device__ Walk(const AttnArgs &args, const Plan &pl, const RowTile *tiles, int which = (int)blockIdx.x, bool wide = false)
-        : a(args), recs(tiles), cta(which) {
+    __device__ Walk(const AttnArgs &args, const Plan &pl, const RowTile *tiles) : a(args), recs(tiles) {
         n_recs = pl.row_tiles;
         per = pl.per;
-        pos = (long long)cta * per;
+        pos = (long long)blockIdx.x * per;
         end = min(pos + per, pl.work);
         rt = n_recs;
-        if (cta >= pl.ctas || pos >= pl.work)
+        if ((int)blockIdx.x >= pl.ctas || pos >= pl.work)
             return;
         int lo = 0, hi = n_recs;                // the last row tile with before <= pos
-        while (wide && hi - lo > 1) {
-            const int step = (hi - lo + 31) / 32, i = lo + (int)(threadIdx.x & 31) * step;
-            const int n = __popc(__ballot_sync(0xffffffffu, i < hi && recs[i].before <= pos));       // the first always is
-            hi = min(hi, lo + n * step);
-            lo += (n - 1) * step;
-        }
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (recs[mid].before <= pos)
@@ -293,7 +285,7 @@ struct Walk {
                 pc.tile0 = r.tile0;
                 pc.t0 = lo;
                 pc.t1 = hi;
-                pc.first = pc.last = cta;
+                pc.first = pc.last = (int)blockIdx.x;
                 pc.first_tiles = pc.last_tiles = r.tiles;
                 const long long t0 = base + kUnitCost, t1 = t0 + r.tiles - 1;
                 if (r.tiles > 0 && (t0 < pos || t1 >= end)) {      // cut

@@ -45,6 +45,9 @@ constexpr int kRopeSlots = 2;
 constexpr int kSCol = 256;                   // tensor memory: O^T at 64 m, S^T from here
 constexpr float kMostPower = 32.0f;
 
+constexpr int kSmallUnits = 152, kSmallRequests = 256;       // most of a plan that every CTA makes for itself
+constexpr long long kSmallTokens = 1ll << 29;               // and tokens of a request: its work fits an int
+
 // A cut unit that begins in a CTA: where its rows go, its parts.
 struct LatentJoin {
     long long row;                           // first of its rows in out
@@ -55,6 +58,7 @@ struct LatentArgs {
     AttnArgs a;                              // the plan's view: one key/value head, `heads` query heads
     LatentProblem p;
     int split;                               // CTAs that share a unit's rows: 1 or 2
+    int small;                               // whether every CTA makes the plan for itself
     int q_rows;                              // rows of the query buffer
     int slots;                               // pairs in the ring
     int cap;                                 // rows of a part
@@ -70,12 +74,16 @@ struct LatentSmem {
     static constexpr int kChunks = L / 64 + 1;
     uint8_t *ring, *rope, *p, *q;
     uint64_t *pair_full, *pair_empty, *rope_full, *rope_empty, *s_full, *p_ready, *o_done, *o_free, *q_ready;
-    float *ref, *fac, *sum;                  // [64] each
-    float *red;                              // [4][64], over the weights while no product reads them
+    Plan *plan;
+    float *ref, *sum;                        // [64] each
+    float *red, *fac;                        // [4][64] and [64], over the weights while no product reads them
     int *hi;                                 // [64]
     uint32_t *bad;                           // a bit for each token of a tile
     uint32_t *taddr;
-    static constexpr size_t kTail = (2 * kMaxSlots + 2 * kRopeSlots + 8) * 8 + 64 * 4 * 4 + 16;
+    int *before;                             // [kSmallUnits], and which request and row tile of it
+    uint16_t *which;
+    static constexpr int kBars = 2 * kMaxSlots + 2 * kRopeSlots + 8;
+    static constexpr size_t kTail = kBars * 8 + sizeof(Plan) + 3 * 64 * 4 + 16 + kSmallUnits * 6;
     __host__ __device__ static size_t fixed(int q_rows) { return (size_t)kRopeSlots * kChunkBytes + kChunkBytes + (size_t)q_rows * 128 * kChunks + kTail + 1024; }
     __host__ __device__ static size_t bytes(int q_rows, int slots) { return fixed(q_rows) + (size_t)slots * 2 * kChunkBytes; }
     __host__ static int slots_for(int q_rows) {
@@ -97,13 +105,90 @@ struct LatentSmem {
         o_done = p_ready + 2;
         o_free = o_done + 1;
         q_ready = o_free + 1;
-        ref = reinterpret_cast<float *>(s_full + 8);
-        fac = ref + 64;
-        sum = fac + 64;
+        plan = reinterpret_cast<Plan *>(b + kBars);
+        ref = reinterpret_cast<float *>(plan + 1);
+        sum = ref + 64;
         red = reinterpret_cast<float *>(p);
+        fac = red + 256;
         hi = reinterpret_cast<int *>(sum + 64);
         bad = reinterpret_cast<uint32_t *>(hi + 64);
         taddr = bad + 2;
+        before = reinterpret_cast<int *>(bad + 4);
+        which = reinterpret_cast<uint16_t *>(before + kSmallUnits);
+    }
+};
+
+// A warp's walk through the range of its CTA (of its CTAs, where they share units), as Walk's; the units are listed in shared memory or
+// in the workspace, and the search for the first looks at 32 of them at a time.
+template <int L>
+struct LatentWalk {
+    const LatentArgs &g;
+    const LatentSmem<L> &s;
+    long long pos, end, base, per;
+    int unit, units, cta;
+    RowTile r;
+
+    __device__ long long begins(int u) const { return g.small ? s.before[u] : g.a.recs[u].before; }
+    __device__ void load() {
+        if (!g.small) {
+            r = g.a.recs[unit];
+            return;
+        }
+        const int request = s.which[unit] & 255, q0 = __ldg(g.a.p.q_offsets + request);
+        r = row_tile(g.a, request, q0, __ldg(g.a.p.q_offsets + request + 1) - q0, __ldg(g.a.p.kv_lens + request), (s.which[unit] >> 8) * g.a.rows);
+        r.before = s.before[unit];
+    }
+    __device__ LatentWalk(const LatentArgs &args, const LatentSmem<L> &smem) : g(args), s(smem), cta((int)blockIdx.x / args.split) {
+        const Plan pl = *s.plan;
+        units = pl.row_tiles;
+        per = pl.per;
+        pos = (long long)cta * per;
+        end = min(pos + per, pl.work);
+        unit = units;
+        if (cta >= pl.ctas || pos >= pl.work)
+            return;
+        int lo = 0, hi = units;                 // the last unit that begins at pos or before
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32, i = lo + (int)(threadIdx.x & 31) * step;
+            const int n = __popc(__ballot_sync(0xffffffffu, i < hi && begins(i) <= pos));        // the first always does
+            hi = min(hi, lo + n * step);
+            lo += (n - 1) * step;
+        }
+        unit = lo;
+        load();
+        base = r.before;
+    }
+    // The next piece; false at the end of the range.
+    __device__ bool next(Piece &pc) {
+        while (unit < units && base < end) {
+            const int lo = (int)min(max(pos - base - kUnitCost, 0ll), (long long)r.tiles);
+            const int hi = (int)max(min(end - base - kUnitCost, (long long)r.tiles), 0ll);
+            const bool mine = r.tiles == 0 ? base >= pos : hi > lo;
+            if (mine) {
+                pc.request = r.request;
+                pc.head = 0;
+                pc.row0 = r.row0;
+                pc.q0 = r.q0;
+                pc.n = r.n;
+                pc.kv = r.kv;
+                pc.rows = min(g.a.rows, r.n * g.a.group - r.row0);
+                pc.tile0 = r.tile0;
+                pc.t0 = lo;
+                pc.t1 = hi;
+                pc.first = pc.last = cta;
+                const long long t0 = base + kUnitCost, t1 = t0 + r.tiles - 1;
+                if (r.tiles > 0 && (t0 < pos || t1 >= end)) {      // cut
+                    pc.first = t0 < pos ? (int)(t0 / per) : cta;
+                    pc.last = t1 >= end ? (int)(t1 / per) : cta;
+                }
+            }
+            base += r.tiles + kUnitCost;
+            if (++unit < units && base < end)
+                load();
+            if (mine)
+                return true;
+        }
+        return false;
     }
 };
 
@@ -113,6 +198,7 @@ struct Mine {
     int tok0, tiles;
     int hi_min, hi_max;                      // positions that the first and the last row see
 
+    __device__ Mine() {}
     __device__ Mine(const LatentArgs &g, const Piece &pc) {
         const int part = g.split == 1 ? 0 : (int)blockIdx.x & 1;
         const int per = g.split == 1 ? pc.rows : ((pc.rows + 1) / 2 + 15) / 16 * 16;
@@ -259,13 +345,13 @@ struct Place {
 // ------------------------------------------------------------ the cache's tiles
 
 template <int L>
-__device__ __forceinline__ void latent_stream(const LatentArgs &g, const Plan &pl, const LatentSmem<L> &s, const CUtensorMap *pair_map,
+__device__ __forceinline__ void latent_stream(const LatentArgs &g, const LatentSmem<L> &s, const CUtensorMap *pair_map,
                                               const CUtensorMap *chunk_map) {
     const AttnProblem &p = g.a.p;
     const int lane = threadIdx.x & 31;
     const int box_shift = min(g.a.shift, 6), subs = kTile >> box_shift;          // a box's rows lie in one block
-    Waiter wait{g.a.hdr, false};
-    Walk walk(g.a, pl, g.a.recs, (int)blockIdx.x / g.split, true);
+    bool dead = false;
+    LatentWalk<L> walk(g, s);
     Piece pc;
     Place pair, rope;
     uint32_t pairs = 0, ropes = 0;
@@ -296,16 +382,16 @@ __device__ __forceinline__ void latent_stream(const LatentArgs &g, const Plan &p
             // boxes of this tile that hold something
             const int live = min(subs, (m.hi_max - (m.tok0 + t * kTile) + (1 << box_shift) - 1) >> box_shift);
             const uint32_t chunk_bytes = (uint32_t)(live << box_shift) * 128;
-            // chunks c .. c + n - 1
+            // chunks c .. c + n - 1.  Every lane waits for itself; one copies where a box is a chunk's whole tile
             auto load = [&](uint8_t *dst, uint64_t *full, uint64_t *empty, uint32_t parity, bool used, int c, int n) {
-                if (used)
-                    wait(empty, parity);
+                if (used && !dead && (subs > 1 || lane == 0) && !wait_phase(empty, parity)) {
+                    record_status(g.a.hdr, MOE_ERR_DEVICE_TIMEOUT);
+                    dead = true;
+                }
+                if (dead)
+                    return;
                 if (lane == 0)
                     mbar_arrive_expect_tx(full, chunk_bytes * n);
-                if (subs > 1)
-                    __syncwarp();
-                if (wait.dead)
-                    return;
                 if (subs == 1) {
                     if (lane == 0)
                         copy_box(smem_u32(dst), n == 2 ? pair_map : chunk_map, to, c, full);
@@ -322,23 +408,23 @@ __device__ __forceinline__ void latent_stream(const LatentArgs &g, const Plan &p
                      2 * i, 2);
                 pair.next(g.slots);
             }
+            dead = __any_sync(0xffffffffu, dead);
         }
     }
     // copies in flight end before the CTA's memory goes away
+    Waiter wait{g.a.hdr, dead};
     for (uint32_t i = pairs > (uint32_t)g.slots ? pairs - g.slots : 0; i < pairs && !wait.dead; ++i)
         wait(s.pair_full + i % g.slots, (i / g.slots) & 1);
     for (uint32_t i = ropes > kRopeSlots ? ropes - kRopeSlots : 0; i < ropes && !wait.dead; ++i)
         wait(s.rope_full + i % kRopeSlots, (i / kRopeSlots) & 1);
 }
 
-// --------------------------------------------------------------- products
-
 // S^T = K Q^T
 template <int L>
-__device__ __forceinline__ void latent_scores(const LatentArgs &g, const Plan &pl, const LatentSmem<L> &s, uint32_t tmem) {
+__device__ __forceinline__ void latent_scores(const LatentArgs &g, const LatentSmem<L> &s, uint32_t tmem) {
     constexpr int kPairs = LatentSmem<L>::kPairs;
     Waiter wait{g.a.hdr, false};
-    Walk walk(g.a, pl, g.a.recs, (int)blockIdx.x / g.split, true);
+    LatentWalk<L> walk(g, s);
     Piece pc;
     Place pair, rope;
     uint32_t tiles = 0, units = 0;
@@ -378,9 +464,9 @@ __device__ __forceinline__ void latent_scores(const LatentArgs &g, const Plan &p
 
 // O^T += C^T P^T
 template <int L>
-__device__ __forceinline__ void latent_values(const LatentArgs &g, const Plan &pl, const LatentSmem<L> &s, uint32_t tmem) {
+__device__ __forceinline__ void latent_values(const LatentArgs &g, const LatentSmem<L> &s, uint32_t tmem) {
     Waiter wait{g.a.hdr, false};
-    Walk walk(g.a, pl, g.a.recs, (int)blockIdx.x / g.split, true);
+    LatentWalk<L> walk(g, s);
     Piece pc;
     Place pair;
     uint32_t tiles = 0, units = 0;
@@ -412,51 +498,48 @@ __device__ __forceinline__ void latent_values(const LatentArgs &g, const Plan &p
 // ------------------------------------------------------------------ softmax
 
 template <int L>
-__device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Plan &pl, const LatentSmem<L> &s, uint32_t tmem) {
+__device__ __forceinline__ void latent_softmax(const LatentArgs &g, const LatentSmem<L> &s, uint32_t tmem) {
     constexpr int kPairs = LatentSmem<L>::kPairs;
     const LatentProblem &p = g.p;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, tid = threadIdx.x;
     const int quarter = warp & 3, half = warp >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-    const int cta = (int)blockIdx.x / g.split, part = g.split == 1 ? 0 : (int)blockIdx.x & 1;
+    const int part = g.split == 1 ? 0 : (int)blockIdx.x & 1;
     const int col0 = 32 * half + 2 * (lane & 3);            // this thread's columns: col0 + 8 i + e
     const int tok_a = 16 * quarter + (lane >> 2);           // its tokens of a tile: tok_a + 8 k
     const float f = g.factor;
     Waiter wait{g.a.hdr, false};
-    Walk walk(g.a, pl, g.a.recs, cta, true);
-    Piece pc;
+    LatentWalk<L> walk(g, s);
+    Piece pc{};
+    Mine m;
     LatentJoin join{0, 0, 0, 0};
-    bool stored = false;                                     // results on their way out of the query buffer
     uint32_t tiles = 0;                                      // so far
-    while (walk.next(pc)) {
-        const Mine m(g, pc);
-        if (m.rows == 0)
-            continue;
-        const bool whole = pc.first == pc.last;
-        const long long out_row = (long long)pc.q0 * p.heads + m.row0;
-        const int slot = (cta * 2 + (cta == pc.first)) * g.split + part;
-        if (!whole && cta == pc.first)
-            join = LatentJoin{out_row, m.rows, pc.first, pc.last};
-        if (m.tiles == 0) {                                  // nothing that these rows see
-            if (whole) {
-                uint4 *to = reinterpret_cast<uint4 *>(p.out + out_row * L);
+    auto first_row = [&] { return (long long)pc.q0 * p.heads + m.row0; };
+    auto slot_of = [&] { return (walk.cta * 2 + (walk.cta == pc.first)) * g.split + part; };
+    // the next piece with something to see; those without have their results at once
+    auto advance = [&]() -> bool {
+        while (walk.next(pc)) {
+            m = Mine(g, pc);
+            if (m.rows == 0)
+                continue;
+            if (pc.first != pc.last && walk.cta == pc.first)
+                join = LatentJoin{first_row(), m.rows, pc.first, pc.last};
+            if (m.tiles > 0)
+                return true;
+            if (pc.first == pc.last) {
+                uint4 *to = reinterpret_cast<uint4 *>(p.out + first_row() * L);
                 for (int i = tid; i < m.rows * (L / 8); i += kSoft)
                     to[i] = make_uint4(0, 0, 0, 0);
                 if (p.lse && tid < m.rows)
-                    p.lse[out_row + tid] = -INFINITY;
+                    p.lse[first_row() + tid] = -INFINITY;
             } else if (tid < m.rows) {
-                __stcg(g.part_sum + (size_t)slot * g.cap + tid, make_float2(-INFINITY, 0.0f));
+                __stcg(g.part_sum + (size_t)slot_of() * g.cap + tid, make_float2(-INFINITY, 0.0f));
             }
-            continue;
         }
-        // queries, zero past the last row, a warp a row and all rows' copies in flight together; the scores of the unit before are all
-        // made, and its results have left the buffer
-        if (stored) {
-            if (tid == 0)
-                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-            soft_sync();
-            stored = false;
-        }
+        return false;
+    };
+    // a piece's queries on their way, zero past the last row: a warp a row, all copies in flight together
+    auto load_queries = [&] {
         for (int r = warp; r < m.n_side; r += kSoftWarps) {
             const int64_t t = pc.q0 + (m.row0 + r) / p.heads, h = (m.row0 + r) % p.heads;
             const uint16_t *ql = p.ql + t * p.ql_st + h * p.ql_sh, *qr = p.qr + t * p.qr_st + h * p.qr_sh;
@@ -473,6 +556,12 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Plan &
             }
         }
         cp_async_commit();
+    };
+    bool more = advance(), stored = false;
+    if (more)
+        load_queries();
+    while (more) {
+        const bool whole = pc.first == pc.last;
         if (tid < kMaxRows) {
             int lo, hi = m.hi_max;
             if (tid < m.rows)
@@ -622,6 +711,7 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Plan &
                             tmem_st_32x16(lanes + 64 * (i >> 1) + c, o);
                         }
                 }
+                soft_sync();                                 // the factors lie where the weights go
                 weigh();
                 fence_before();
                 soft_sync();
@@ -635,6 +725,12 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Plan &
                     for (int e = 0; e < 2; ++e)
                         sum[2 * i + e] += w[4 * i + e] + w[4 * i + 2 + e];
         }
+        // the scores are all made: the next piece's queries may come, unless results are put together where they go
+        const long long out_row = first_row();
+        const int slot = slot_of(), rows = m.rows;
+        more = advance();
+        if (more && !whole)
+            load_queries();
         wait(s.o_done, (tiles - 1) & 1);
         // sums of the columns: eight lanes, four warps, in this order
 #pragma unroll
@@ -649,7 +745,7 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Plan &
                 s.ref[col] = ref[i];
         }
         soft_sync();
-        if (tid < m.rows) {
+        if (tid < rows) {
             const float l = (s.red[tid] + s.red[64 + tid]) + (s.red[128 + tid] + s.red[192 + tid]);
             s.sum[tid] = l == 0.0f ? 0.0f : 1.0f / l;
             if (!whole)
@@ -661,7 +757,7 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Plan &
         if (!whole) {
 #pragma unroll 1
             for (int i = 0; i < 2 * kPairs; ++i) {
-                const int c = 32 * half + 16 * (i & 1), n = m.rows - c;          // rows c .. c + 15 of dims 128 (i / 2) + lane
+                const int c = 32 * half + 16 * (i & 1), n = rows - c;          // rows c .. c + 15 of dims 128 (i / 2) + lane
                 if (n <= 0)
                     continue;
                 float o[16];
@@ -676,7 +772,7 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Plan &
             // rows of out lie one after the other: they are put together where the queries were, and leave as one copy
 #pragma unroll 1
             for (int i = 0; i < 2 * kPairs; ++i) {
-                const int c = 32 * half + 16 * (i & 1), n = m.rows - c;
+                const int c = 32 * half + 16 * (i & 1), n = rows - c;
                 if (n <= 0)
                     continue;
                 float o[16];
@@ -698,10 +794,16 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Plan &
         soft_sync();                                         // also: s.sum and s.ref have been read
         if (tid == 0) {
             mbar_arrive(s.o_free);
-            if (stored)
+            if (whole)
                 asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\ncp.async.bulk.commit_group;" ::"l"(p.out + out_row * L),
-                             "r"(smem_u32(s.q)), "r"((uint32_t)m.rows * (2 * L))
+                             "r"(smem_u32(s.q)), "r"((uint32_t)rows * (2 * L))
                              : "memory");
+        }
+        if (whole && more) {
+            if (tid == 0)
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            soft_sync();
+            load_queries();
         }
     }
     if (stored && tid == 0)
@@ -744,15 +846,26 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
     const uint32_t tmem = *s.taddr;
     pdl_wait();
     pdl_trigger();
-    const Plan pl = *g.a.plan;
+    if (g.small) {                               // the plan, made where the cache's tiles go and kept in few words
+        RowTile *recs = reinterpret_cast<RowTile *>(s.ring + 1024);
+        make_small_plan(g.a, reinterpret_cast<long long *>(s.ring), recs, s.plan, blockIdx.x == 0);
+        for (int i = threadIdx.x; i < s.plan->row_tiles; i += kThreads) {
+            s.before[i] = (int)recs[i].before;
+            s.which[i] = (uint16_t)(recs[i].request | recs[i].row0 / g.a.rows << 8);
+        }
+        fence_async();
+    } else if (threadIdx.x == 0) {
+        *s.plan = *g.a.plan;
+    }
+    __syncthreads();
     if (warp < kSoftWarps)
-        latent_softmax<L>(g, pl, s, tmem);
+        latent_softmax<L>(g, s, tmem);
     else if (warp == kSoftWarps)
-        latent_stream<L>(g, pl, s, &pair_map, &chunk_map);
+        latent_stream<L>(g, s, &pair_map, &chunk_map);
     else if (warp == kSoftWarps + 1)
-        latent_scores<L>(g, pl, s, tmem);
+        latent_scores<L>(g, s, tmem);
     else
-        latent_values<L>(g, pl, s, tmem);
+        latent_values<L>(g, s, tmem);
     fence_before();
     __syncthreads();
     fence_after();
@@ -768,56 +881,108 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(AttnArgs a) {
     make_plan(a, s_first, red, a.recs, a.plan, true);
 }
 
-// The parts of the cut unit that begins in CTA blockIdx.x, in the order of the cache: a row in L / 4 threads.
+// The parts of cut units, in the order of the cache.  A CTA takes rows of all cut units in turn: L / 4 threads with four dims each for
+// every second part, so that many parts' loads are in flight.
 constexpr int kJoinThreads = 256;
 template <int L>
-__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentArgs g) {
-    constexpr int kRows = kJoinThreads / (L / 4), U = 8;
+__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentArgs g, int ctas) {
+    constexpr int kDims = L / 4, kGroups = kJoinThreads / kDims, U = 8;
+    __shared__ int s_end[kMaxAttnCtas];          // rows to join of the CTAs up to this one
+    __shared__ float s_w[kMaxAttnCtas];
+    __shared__ float s_red[2][kJoinThreads / 32];
+    __shared__ float4 s_o[kJoinThreads - kDims];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
     pdl_trigger();
-    const LatentJoin j = g.joins[blockIdx.x];
-    const int r = blockIdx.y * kRows + threadIdx.x / (L / 4), d = threadIdx.x % (L / 4);
-    if (r >= j.rows)
+    int n = tid < ctas ? g.joins[tid].rows : 0;
+    const int any = __syncthreads_or(n);
+    if (!any)
         return;
-    const int part = g.split == 1 ? 0 : (int)blockIdx.x & 1;
-    auto slot = [&](int k) { return (size_t)((k * 2 + (k == j.first)) * g.split + part) * g.cap + r; };
-    float m = -INFINITY;
-    for (int k0 = j.first; k0 <= j.last; k0 += U) {
-        float2 e[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            e[u] = k0 + u <= j.last ? __ldcg(g.part_sum + slot(k0 + u)) : make_float2(-INFINITY, 0.0f);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            m = fmaxf(m, e[u].x);
+    for (int d = 1; d < 32; d *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, n, d);
+        n += lane >= d ? v : 0;
     }
-    float l = 0.0f;
-    float4 o = make_float4(0, 0, 0, 0);
-    for (int k0 = j.first; k0 <= j.last; k0 += U) {
-        float2 e[U];
-        float4 v[U];
+    if (tid < kMaxAttnCtas)
+        s_end[tid] = n;
+    __syncthreads();
+    int ahead = 0;
+    for (int w = 0; w < warp && w < kMaxAttnCtas / 32; ++w)
+        ahead += s_end[32 * w + 31];
+    __syncthreads();
+    if (tid < kMaxAttnCtas)
+        s_end[tid] = n + ahead;
+    __syncthreads();
+    const int total = s_end[kMaxAttnCtas - 1];
+    for (int i = blockIdx.x; i < total; i += gridDim.x) {
+        const int c = __syncthreads_count(tid < kMaxAttnCtas && s_end[tid] <= i);
+        const LatentJoin j = g.joins[c];
+        const int r = i - (c ? s_end[c - 1] : 0), part = g.split == 1 ? 0 : c & 1, parts = j.last - j.first + 1;
+        auto slot = [&](int k) { return (size_t)(((j.first + k) * 2 + (k == 0)) * g.split + part) * g.cap + r; };
+        const float2 e = tid < parts ? __ldcg(g.part_sum + slot(tid)) : make_float2(-INFINITY, 0.0f);
+        float m = e.x;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const bool in = k0 + u <= j.last;
-            e[u] = in ? __ldcg(g.part_sum + slot(k0 + u)) : make_float2(-INFINITY, 0.0f);
-            v[u] = in ? __ldcg(reinterpret_cast<const float4 *>(g.part + slot(k0 + u) * L) + d) : make_float4(0, 0, 0, 0);
+        for (int d = 16; d > 0; d /= 2)
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        if (lane == 0)
+            s_red[0][warp] = m;
+        __syncthreads();
+        m = s_red[0][0];
+#pragma unroll
+        for (int w = 1; w < kJoinThreads / 32; ++w)
+            m = fmaxf(m, s_red[0][w]);
+        const float w0 = ex2((e.x - m) * g.factor);
+        if (tid < parts)
+            s_w[tid] = e.y == 0.0f ? -1.0f : w0;             // below zero: it saw nothing, and its sums were not written
+        float l = e.y == 0.0f ? 0.0f : e.y * w0;
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2)
+            l += __shfl_xor_sync(0xffffffffu, l, d);
+        if (lane == 0)
+            s_red[1][warp] = l;
+        __syncthreads();
+        l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinThreads / 32; ++w)
+            l += s_red[1][w];
+        const int d = tid % kDims, group = tid / kDims;
+        float4 o = make_float4(0, 0, 0, 0);
+        for (int k0 = group; k0 < parts; k0 += U * kGroups) {
+            float4 v[U];
+            float w[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = k0 + u * kGroups;
+                const bool in = k < parts && !(s_w[k] < 0.0f);
+                w[u] = in ? s_w[k] : 0.0f;
+                v[u] = in ? __ldcg(reinterpret_cast<const float4 *>(g.part + slot(k) * L) + d) : make_float4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                o.x = fmaf(v[u].x, w[u], o.x);
+                o.y = fmaf(v[u].y, w[u], o.y);
+                o.z = fmaf(v[u].z, w[u], o.z);
+                o.w = fmaf(v[u].w, w[u], o.w);
+            }
         }
+        if (group > 0)
+            s_o[tid - kDims] = o;
+        __syncthreads();
+        if (group == 0) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (e[u].y == 0.0f)                              // it saw nothing: its sums were not written
-                continue;
-            const float w = ex2((e[u].x - m) * g.factor);
-            l = fmaf(e[u].y, w, l);
-            o.x = fmaf(v[u].x, w, o.x);
-            o.y = fmaf(v[u].y, w, o.y);
-            o.z = fmaf(v[u].z, w, o.z);
-            o.w = fmaf(v[u].w, w, o.w);
+            for (int q = 0; q < kGroups - 1; ++q) {
+                const float4 v = s_o[q * kDims + d];
+                o.x += v.x;
+                o.y += v.y;
+                o.z += v.z;
+                o.w += v.w;
+            }
+            const float by = l == 0.0f ? 0.0f : 1.0f / l;
+            reinterpret_cast<uint2 *>(g.p.out + (j.row + r) * L)[d] = make_uint2(bf16_pair(o.x * by, o.y * by), bf16_pair(o.z * by, o.w * by));
+            if (d == 0 && g.p.lse)
+                g.p.lse[j.row + r] = l == 0.0f ? -INFINITY : fmaf(m, g.p.scale, logf(l));
         }
     }
-    const float by = l == 0.0f ? 0.0f : 1.0f / l;
-    reinterpret_cast<uint2 *>(g.p.out + (j.row + r) * L)[d] = make_uint2(bf16_pair(o.x * by, o.y * by), bf16_pair(o.z * by, o.w * by));
-    if (d == 0 && g.p.lse)
-        g.p.lse[j.row + r] = l == 0.0f ? -INFINITY : fmaf(m, g.p.scale, logf(l));
 }
 
 // How rows become units.  Two CTAs share a unit where a token has more than 64 rows, or requests do on average: the cache is
@@ -890,6 +1055,7 @@ cudaError_t launch(const LatentProblem &p, void *ws, int sms, cudaStream_t strea
     g.a.hdr = ws_at<uint32_t>(ws, 0);
     g.p = p;
     g.split = shape.split;
+    g.small = g.a.max_tiles <= kSmallUnits && p.B <= kSmallRequests && (long long)p.max_blocks * p.cache.block_size <= kSmallTokens;
     g.q_rows = shape.q_rows;
     g.slots = LatentSmem<L>::slots_for(shape.q_rows);
     g.cap = shape.cap;
@@ -909,12 +1075,11 @@ cudaError_t launch(const LatentProblem &p, void *ws, int sms, cudaStream_t strea
     const size_t smem = LatentSmem<L>::bytes(g.q_rows, g.slots);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(latent_kernel<L>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess)
+    if (e == cudaSuccess && !g.small)
         e = launch_pdl(latent_plan_kernel, dim3(1), dim3(kPlanThreads), p.B * sizeof(int), stream, g.a);
     if (e == cudaSuccess)
         e = launch_pdl(latent_kernel<L>, dim3(ctas), dim3(kThreads), smem, stream, g, pair_map, chunk_map);
-    constexpr int kRows = kJoinThreads / (L / 4);
-    return e != cudaSuccess ? e : launch_pdl(latent_join_kernel<L>, dim3(ctas, (shape.cap + kRows - 1) / kRows), dim3(kJoinThreads), 0, stream, g);
+    return e != cudaSuccess ? e : launch_pdl(latent_join_kernel<L>, dim3(4 * ctas), dim3(kJoinThreads), 0, stream, g, ctas);
 }
 
 }  // namespace
