@@ -291,11 +291,18 @@ __device__ __forceinline__ void tmem_st_32x16(uint32_t addr, const float (&v)[16
                  : "memory");
 }
 
-// [1][rows][64 dims] or [2][rows][64 dims] of chunks c.. and rows row.. of the cache.
-__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int row, int c, uint64_t *bar) {
+// [1][rows][64 dims] or [2][rows][64 dims] of chunks c.. and rows row.. of the cache, by one elected lane of a converged warp (in a
+// branch of one lane a copy takes 60 ns to issue).
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int row, int c, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(c), "r"(smem_u32(bar))
+        "{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\n"
+        "@p cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n}\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(c), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\n@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}\n" ::"r"(bar), "r"(bytes)
         : "memory");
 }
 
@@ -355,7 +362,6 @@ __device__ __forceinline__ void latent_stream(const LatentArgs &g, const LatentS
     Piece pc;
     Place pair, rope;
     uint32_t pairs = 0, ropes = 0;
-    const int sub = lane % subs, chunk = lane / subs;      // of a tile's boxes, this lane's
     while (walk.next(pc)) {
         const Mine m(g, pc);
         const int32_t *row = p.table + (size_t)pc.request * p.max_blocks;
@@ -378,37 +384,44 @@ __device__ __forceinline__ void latent_stream(const LatentArgs &g, const LatentS
                 at = used ? (page << g.a.shift) + (int)(tok & ((1 << g.a.shift) - 1)) : -1;
                 next = box + 32 < m.tiles * subs ? fetch(box + 32) : -1;
             }
-            const int to = __shfl_sync(0xffffffffu, at, (box & 31) + sub);
-            // boxes of this tile that hold something
+            // boxes of this tile that hold something, and where in the cache
             const int live = min(subs, (m.hi_max - (m.tok0 + t * kTile) + (1 << box_shift) - 1) >> box_shift);
             const uint32_t chunk_bytes = (uint32_t)(live << box_shift) * 128;
-            // chunks c .. c + n - 1.  Every lane waits for itself; one copies where a box is a chunk's whole tile
-            auto load = [&](uint8_t *dst, uint64_t *full, uint64_t *empty, uint32_t parity, bool used, int c, int n) {
-                if (used && !dead && (subs > 1 || lane == 0) && !wait_phase(empty, parity)) {
-                    record_status(g.a.hdr, MOE_ERR_DEVICE_TIMEOUT);
-                    dead = true;
+            int to[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                to[k] = __shfl_sync(0xffffffffu, at, ((box & 31) + k) & 31);
+            // chunks c .. c + n - 1
+            auto load = [&](uint32_t dst, uint64_t *full, uint64_t *empty, uint32_t parity, bool used, int c, int n) {
+                if (used && !dead) {
+                    dead = !__all_sync(0xffffffffu, wait_phase(empty, parity));
+                    if (dead && lane == 0)
+                        record_status(g.a.hdr, MOE_ERR_DEVICE_TIMEOUT);
                 }
                 if (dead)
                     return;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(full, chunk_bytes * n);
+                const uint32_t bar = smem_u32(full);
+                expect_bytes(bar, chunk_bytes * n);
                 if (subs == 1) {
-                    if (lane == 0)
-                        copy_box(smem_u32(dst), n == 2 ? pair_map : chunk_map, to, c, full);
-                } else if (chunk < n && sub < live) {
-                    copy_box(smem_u32(dst + chunk * kChunkBytes + (sub << box_shift) * 128), chunk_map, to, c + chunk, full);
+                    copy_box(dst, n == 2 ? pair_map : chunk_map, to[0], c, bar);
+                    return;
                 }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k < live)
+                        for (int i = 0; i < n; ++i)
+                            copy_box(dst + i * kChunkBytes + (k << box_shift) * 128, chunk_map, to[k], c + i, bar);
             };
-            load(s.rope + rope.slot * kChunkBytes, s.rope_full + rope.slot, s.rope_empty + rope.slot, rope.parity ^ 1, ropes >= kRopeSlots, L / 64, 1);
+            load(smem_u32(s.rope) + rope.slot * kChunkBytes, s.rope_full + rope.slot, s.rope_empty + rope.slot, rope.parity ^ 1, ropes >= kRopeSlots,
+                 L / 64, 1);
             rope.next(kRopeSlots);
             ++ropes;
 #pragma unroll 1
             for (int i = 0; i < LatentSmem<L>::kPairs; ++i, ++pairs) {
-                load(s.ring + pair.slot * (2 * kChunkBytes), s.pair_full + pair.slot, s.pair_empty + pair.slot, pair.parity ^ 1, pairs >= (uint32_t)g.slots,
-                     2 * i, 2);
+                load(smem_u32(s.ring) + pair.slot * (2 * kChunkBytes), s.pair_full + pair.slot, s.pair_empty + pair.slot, pair.parity ^ 1,
+                     pairs >= (uint32_t)g.slots, 2 * i, 2);
                 pair.next(g.slots);
             }
-            dead = __any_sync(0xffffffffu, dead);
         }
     }
     // copies in flight end before the CTA's memory goes away
