@@ -641,8 +641,6 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Latent
                     ref[i] = tok < s.hi[col] ? s.ref[col] : 0.0f;
                 }
             }
-            if (t > 0)                                       // the weights before have been read
-                wait(s.o_done, (tiles - 1) & 1);
             float w[16];
             // weights of the scores, two columns in an instruction; whether one has grown too far
             auto weigh = [&]() -> bool {
@@ -658,8 +656,8 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Latent
                                 : "=f"(y0), "=f"(y1)
                                 : "f"(x[4 * i + 2 * k]), "f"(x[4 * i + 2 * k + 1]), "f"(-ref[2 * i]), "f"(-ref[2 * i + 1]), "f"(f));
                             float v0 = ex2(y0), v1 = ex2(y1);
-                            const int j = tok_a + 8 * k, c = col0 + 8 * i;       // 8 columns are 16 bytes
                             if (edge) {
+                                const int j = tok_a + 8 * k, c = col0 + 8 * i;
                                 const bool sees0 = tok + j < s.hi[c], sees1 = tok + j < s.hi[c + 1];
                                 if (s.bad[j / 32] >> (j & 31) & 1)
                                     v0 = v1 = __uint_as_float(0x7FFFFFFFu);
@@ -671,13 +669,27 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Latent
                             w[4 * i + 2 * k] = v0;
                             w[4 * i + 2 * k + 1] = v1;
                             most = fmaxf(most, fmaxf(y0, y1));
-                            *reinterpret_cast<uint32_t *>(s.p + j * 128 + (((c >> 3) ^ (j & 7)) << 4) + (c & 7) * 2) = bf16_pair(v0, v1);
+                        }
+                    }
+                return most > kMostPower;
+            };
+            auto store = [&] {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < groups) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int j = tok_a + 8 * k, c = col0 + 8 * i;       // 8 columns are 16 bytes
+                            *reinterpret_cast<uint32_t *>(s.p + j * 128 + (((c >> 3) ^ (j & 7)) << 4) + (c & 7) * 2) =
+                                bf16_pair(w[4 * i + 2 * k], w[4 * i + 2 * k + 1]);
                         }
                     }
                 fence_async();
-                return most > kMostPower;
             };
             const bool grew = weigh();
+            if (t > 0)                                       // the weights before have been read
+                wait(s.o_done, (tiles - 1) & 1);
+            store();
             fence_before();
             if (soft_any(grew)) {
                 // references to the maxima; with them the sums, and O
@@ -726,6 +738,7 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Latent
                 }
                 soft_sync();                                 // the factors lie where the weights go
                 weigh();
+                store();
                 fence_before();
                 soft_sync();
             }
