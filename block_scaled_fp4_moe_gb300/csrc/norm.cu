@@ -161,7 +161,7 @@ cudaError_t launch_rms_norm(const NormProblem &p, int sms, cudaStream_t stream) 
         return launch<4, true>(p, 256, stream);
     if (chunks <= 1024 && p.T <= sms)
         return launch<1, false>(p, threads(1), stream);
-    if (chunks <= 2048)
+    if (chunks <= 256 || (chunks <= 2048 && p.T <= 4 * sms))
         return launch<2, false>(p, threads(2), stream);
     return launch<4, false>(p, threads(4), stream);
 }

@@ -5,9 +5,11 @@
 // The angle of a far position needs more bits than fp32 has: f is held in units of 2^-64 turns, p f modulo 2^64 is one
 // integer product and is exact, and its upper 32 bits, as a signed fraction of a turn rounded to fp32, are within 2^-26 turns.
 //
-// Lanes.  A head has D / 8 lanes (rounded up to a power of two) with eight dims each, so that a norm's sum is a few shuffles.
-// With halves a pair's other half is in the lane 2 pairs / 16 away.  Cosines and sines are made once for a token
-// and CTA, in shared memory, for all heads.
+// Lanes.  A lane has 16 dims of a head: where pairs are halves, eight of each half, so that no values pass between lanes; a norm's
+// sum is a few shuffles over the head's lanes (a power of two of them).  A warp has a token and a few sets of heads, whose loads are all
+// in flight before it makes the token's cosines and sines (in shared memory; a lane keeps its eight): no warp waits for another.
+#include <type_traits>
+
 #include "attn.h"
 
 namespace moe {
@@ -38,81 +40,111 @@ __device__ __forceinline__ float2 turn_of(int position, uint64_t turns, float am
     return make_float2(c * amplitude, s * amplitude);
 }
 
-// Eight dims of a head, `c` the chunk of the rotated part that they are (of 2 pairs / 8), to their rotated values.  cs: the pairs'.
-// The lane of the other half is lane + or - span.  All lanes of the warp take part.
-__device__ __forceinline__ void rotate8(float (&v)[8], int c, bool in, int span, int interleaved, const float2 *cs) {
-    if (interleaved) {
-        if (!in)
-            return;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 t = cs[4 * c + i];
-            const float a = v[2 * i], b = v[2 * i + 1];
-            v[2 * i] = a * t.x - b * t.y;
-            v[2 * i + 1] = b * t.x + a * t.y;
-        }
-        return;
-    }
-    const bool second = c >= span;
-    const int lane = threadIdx.x & 31, other = in ? (second ? lane - span : lane + span) : lane;
-    const int first = 8 * (second ? c - span : c);
+// Eight pairs in two times eight dims.
+template <bool INTER>
+__device__ __forceinline__ void rotate16_as(float (&u)[8], float (&v)[8], const float2 (&cs)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float o = __shfl_sync(0xffffffffu, v[i], other);
-        if (in) {
-            const float2 t = cs[first + i];
-            v[i] = second ? v[i] * t.x + o * t.y : v[i] * t.x - o * t.y;
-        }
+        float &a = INTER ? (i < 4 ? u[2 * i & 7] : v[2 * i & 7]) : u[i];
+        float &b = INTER ? (i < 4 ? u[(2 * i & 7) + 1] : v[(2 * i & 7) + 1]) : v[i];
+        const float x = a, y = b;
+        a = x * cs[i].x - y * cs[i].y;
+        b = y * cs[i].x + x * cs[i].y;
     }
 }
+__device__ __forceinline__ void rotate16(float (&u)[8], float (&v)[8], int interleaved, const float2 (&cs)[8]) {
+    if (interleaved)
+        rotate16_as<true>(u, v, cs);
+    else
+        rotate16_as<false>(u, v, cs);
+}
 
-constexpr int kRotaryThreads = 256;
+constexpr int kRotaryWarps = 4;
 
-// One CTA: a token's heads blockIdx.y, + gridDim.y, ... (in sets of as many as the CTA holds).
-template <int LANES>
-__global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryProblem p) {
-    __shared__ float2 cs[128];
+// A warp: a token and SETS sets of 32 / LANES heads.  Item i of a head: pairs 8 i .. 8 i + 7, or, behind those, two chunks of eight dims
+// that are not rotated.
+template <int LANES, int SETS, bool NORM>
+__global__ void __launch_bounds__(kRotaryWarps * 32) rotary_kernel(const RotaryProblem p) {
+    __shared__ float2 s_cs[kRotaryWarps][128];
     pdl_wait();
     pdl_trigger();
-    const int t = blockIdx.x, pos = p.positions[t];
+    constexpr int kSet = 32 / LANES;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = p.q.heads + p.k.heads;
+    const int segments = (heads + SETS * kSet - 1) / (SETS * kSet);
+    const int64_t job = (int64_t)blockIdx.x * kRotaryWarps + warp;
+    const int t = (int)(job / segments), h0 = (int)(job % segments) * (SETS * kSet) + lane / LANES;
+    if (t >= p.T)
+        return;
+    const int pos = p.positions[t];
     if (pos < 0)
         return;
-    if ((int)threadIdx.x < p.pairs)
-        cs[threadIdx.x] = turn_of(pos, __ldg(p.turns + threadIdx.x), p.amplitude);
-    __syncthreads();
-    const int c = threadIdx.x % LANES, set = kRotaryThreads / LANES;
-    const int first = p.offset / 8, span = p.pairs / 8;
-    const bool in = c >= first && c < first + 2 * span, live = c < p.D / 8;
-    const int heads = p.q.heads + p.k.heads;
-    for (int h0 = blockIdx.y * set; h0 < heads; h0 += gridDim.y * set) {      // the same trips for all lanes
-        const int h = h0 + threadIdx.x / LANES;
-        const bool is_q = h < p.q.heads, mine = live && h < heads;
-        const HeadSet &x = is_q ? p.q : p.k;
-        const int at = is_q ? h : h - p.q.heads;
-        const uint16_t *src = x.in + t * x.st + at * x.sh + 8 * c;
-        uint16_t *dst = x.out + t * x.ost + at * x.osh + 8 * c;
-        float v[8];
-        widen(v, mine ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0));
-        if (p.q.norm || p.k.norm) {
+    const int item = lane % LANES, first = p.offset / 8, span = p.pairs / 8, rest = p.D / 8 - 2 * span;
+    const bool in = item < span;
+    // the lane's chunks: neither, one or both exist
+    int c0 = 2 * (item - span), c1 = c0 + 1;
+    const bool has0 = in || c0 < rest, has1 = in || c1 < rest;
+    if (in) {
+        c0 = first + (p.interleaved ? 2 * item : item);
+        c1 = p.interleaved ? c0 + 1 : c0 + span;
+    } else {
+        c0 += c0 < first ? 0 : 2 * span;
+        c1 += c1 < first ? 0 : 2 * span;
+    }
+    uint4 raw[SETS][2];
+#pragma unroll
+    for (int u = 0; u < SETS; ++u) {
+        const int h = h0 + u * kSet;
+        const bool is_q = h < p.q.heads;
+        const uint16_t *src = is_q ? p.q.in + t * p.q.st + h * p.q.sh : p.k.in + t * p.k.st + (h - p.q.heads) * p.k.sh;
+        raw[u][0] = has0 && h < heads ? *reinterpret_cast<const uint4 *>(src + 8 * c0) : make_uint4(0, 0, 0, 0);
+        raw[u][1] = has1 && h < heads ? *reinterpret_cast<const uint4 *>(src + 8 * c1) : make_uint4(0, 0, 0, 0);
+    }
+    for (int i = lane; i < p.pairs; i += 32)
+        s_cs[warp][i] = turn_of(pos, __ldg(p.turns + i), p.amplitude);
+    __syncwarp();
+    float2 cs[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        cs[i] = in ? s_cs[warp][8 * item + i] : make_float2(1.0f, 0.0f);
+#pragma unroll
+    for (int u = 0; u < SETS; ++u) {
+        const int h = h0 + u * kSet;
+        const bool is_q = h < p.q.heads;
+        const uint16_t *src = is_q ? p.q.in + t * p.q.st + h * p.q.sh : p.k.in + t * p.k.st + (h - p.q.heads) * p.k.sh;
+        uint16_t *dst = is_q ? p.q.out + t * p.q.ost + h * p.q.osh : p.k.out + t * p.k.ost + (h - p.q.heads) * p.k.osh;
+        const uint16_t *norm = is_q ? p.q.norm : p.k.norm;
+        float a[8], b[8];
+        widen(a, raw[u][0]);
+        widen(b, raw[u][1]);
+        if (NORM) {
             float s = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                s = fmaf(v[i], v[i], s);
+                s = fmaf(a[i], a[i], fmaf(b[i], b[i], s));
 #pragma unroll
             for (int d = LANES / 2; d > 0; d >>= 1)
                 s += __shfl_xor_sync(0xffffffffu, s, d);
-            if (mine && x.norm) {
+            if (norm) {
                 const float by = rsqrtf(s / (float)p.D + p.eps);
                 float w[8];
-                widen(w, __ldg(reinterpret_cast<const uint4 *>(x.norm) + c));
+                widen(w, has0 ? __ldg(reinterpret_cast<const uint4 *>(norm) + c0) : make_uint4(0, 0, 0, 0));
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    v[i] = v[i] * by * w[i];
+                    a[i] = a[i] * by * w[i];
+                widen(w, has1 ? __ldg(reinterpret_cast<const uint4 *>(norm) + c1) : make_uint4(0, 0, 0, 0));
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    b[i] = b[i] * by * w[i];
             }
         }
-        rotate8(v, c - first, in, span, p.interleaved, cs);
-        if (mine && (in || x.norm || dst != src))
-            *reinterpret_cast<uint4 *>(dst) = narrow(v);
+        if (in)
+            rotate16(a, b, p.interleaved, cs);
+        if (h < heads && (in || (NORM && norm) || dst != src)) {
+            if (has0)
+                *reinterpret_cast<uint4 *>(dst + 8 * c0) = narrow(a);
+            if (has1)
+                *reinterpret_cast<uint4 *>(dst + 8 * c1) = narrow(b);
+        }
     }
 }
 
@@ -120,10 +152,10 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryProb
 
 constexpr int kAppendWarps = 4;
 
-// A warp has a token: its latent vector in L / 256 chunks of eight values a lane, its rotary key in the first eight lanes.
+// A warp has a token: its latent vector in L / 256 chunks of eight values a lane, its rotary key in the first four lanes.
 template <int L>
 __global__ void __launch_bounds__(kAppendWarps * 32) latent_append_kernel(const LatentAppendProblem p) {
-    __shared__ float2 cs[kAppendWarps][kRopeDims / 2];
+    __shared__ float2 s_cs[kAppendWarps][kRopeDims / 2];
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -139,20 +171,29 @@ __global__ void __launch_bounds__(kAppendWarps * 32) latent_append_kernel(const 
         return;
     }
     constexpr int PER = L / 256;
-    float v[PER][8], k[8];
+    float v[PER][8], k[2][8];
 #pragma unroll
     for (int i = 0; i < PER; ++i)
         widen(v[i], *(reinterpret_cast<const uint4 *>(p.c + t * p.ldc) + lane + 32 * i));
-    const bool key = lane < kRopeDims / 8;
-    widen(k, key ? *(reinterpret_cast<const uint4 *>(p.k + t * p.ldk) + lane) : make_uint4(0, 0, 0, 0));
+    const int k0 = p.interleaved ? 2 * lane : lane, k1 = p.interleaved ? k0 + 1 : k0 + kRopeDims / 16;   // its chunks
+    const bool key = lane < kRopeDims / 16;
+    const uint4 *from = reinterpret_cast<const uint4 *>(p.k + t * p.ldk);
+    widen(k[0], key ? from[k0] : make_uint4(0, 0, 0, 0));
+    widen(k[1], key ? from[k1] : make_uint4(0, 0, 0, 0));
     uint16_t *row = p.cache.data + slot * (L + kRopeDims);
     if (p.turns) {
-        cs[warp][lane] = turn_of(p.positions[t], __ldg(p.turns + lane), p.amplitude);
+        s_cs[warp][lane] = turn_of(p.positions[t], __ldg(p.turns + lane), p.amplitude);
         __syncwarp();
-        rotate8(k, lane, key, kRopeDims / 16, p.interleaved, cs[warp]);
+        float2 cs[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            cs[i] = s_cs[warp][(8 * lane + i) & (kRopeDims / 2 - 1)];
+        rotate16(k[0], k[1], p.interleaved, cs);
     }
-    if (key)
-        *(reinterpret_cast<uint4 *>(row + L) + lane) = narrow(k);
+    if (key) {
+        reinterpret_cast<uint4 *>(row + L)[k0] = narrow(k[0]);
+        reinterpret_cast<uint4 *>(row + L)[k1] = narrow(k[1]);
+    }
     if (p.norm) {
         float s = 0.0f;
 #pragma unroll
@@ -181,11 +222,23 @@ __global__ void __launch_bounds__(kAppendWarps * 32) latent_append_kernel(const 
 }  // namespace
 
 cudaError_t launch_rotary(const RotaryProblem &p, int sms, cudaStream_t stream) {
-    const int lanes = p.D <= 64 ? 8 : p.D <= 128 ? 16 : 32, set = kRotaryThreads / lanes;
-    const int sets = (p.q.heads + p.k.heads + set - 1) / set;
-    const int split = p.T >= 4 * sms ? 1 : sets;           // a CTA for a token's heads, or for as many as it holds
-    auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(p.T, split), dim3(kRotaryThreads), 0, stream, p); };
-    return lanes == 8 ? go(rotary_kernel<8>) : lanes == 16 ? go(rotary_kernel<16>) : go(rotary_kernel<32>);
+    const int items = p.pairs / 8 + (p.D / 8 - p.pairs / 4 + 1) / 2, lanes = items <= 4 ? 4 : items <= 8 ? 8 : 16;
+    const int heads = p.q.heads + p.k.heads, set = 32 / lanes;
+    // Sets of a warp: one while that many warps fit on the GPU at once (64 tokens of 72 heads of 128, 2.6 us; with four, 3.5); else four or three,
+    // as fewer lanes go without a head (4,000 tokens of 48 heads 18.0 and 18.7 us, with two 19.5; 8,192 of 18 heads of 256 43.7 and 32.9).
+    auto waste = [&](int sets) { return (sets * set - heads % (sets * set)) % (sets * set); };
+    const int sets = (int64_t)p.T * heads * lanes <= (int64_t)sms * 512 ? 1 : waste(3) < waste(4) ? 3 : 4;
+    const int64_t jobs = (int64_t)p.T * ((heads + sets * set - 1) / (sets * set));
+    const dim3 grid((unsigned)((jobs + kRotaryWarps - 1) / kRotaryWarps));
+    auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(kRotaryWarps * 32), 0, stream, p); };
+    auto form = [&](auto lanes_of) {
+        constexpr int N = decltype(lanes_of)::value;
+        if (p.q.norm || p.k.norm)
+            return sets == 1 ? go(rotary_kernel<N, 1, true>) : sets == 3 ? go(rotary_kernel<N, 3, true>) : go(rotary_kernel<N, 4, true>);
+        return sets == 1 ? go(rotary_kernel<N, 1, false>) : sets == 3 ? go(rotary_kernel<N, 3, false>) : go(rotary_kernel<N, 4, false>);
+    };
+    return lanes == 4 ? form(std::integral_constant<int, 4>()) : lanes == 8 ? form(std::integral_constant<int, 8>())
+                                                                            : form(std::integral_constant<int, 16>());
 }
 
 cudaError_t launch_latent_append(const LatentAppendProblem &p, int, cudaStream_t stream) {
