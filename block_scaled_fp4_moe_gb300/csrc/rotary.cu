@@ -152,10 +152,9 @@ __global__ void __launch_bounds__(kRotaryWarps * 32) rotary_kernel(const RotaryP
 
 constexpr int kAppendWarps = 4;
 
-// A warp has a token: its latent vector in L / 256 chunks of eight values a lane, its rotary key in the first four lanes.
+// A warp has a token: its latent vector in L / 256 chunks of eight values a lane, a pair of its rotary key in each.
 template <int L>
 __global__ void __launch_bounds__(kAppendWarps * 32) latent_append_kernel(const LatentAppendProblem p) {
-    __shared__ float2 s_cs[kAppendWarps][kRopeDims / 2];
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -171,29 +170,26 @@ __global__ void __launch_bounds__(kAppendWarps * 32) latent_append_kernel(const 
         return;
     }
     constexpr int PER = L / 256;
-    float v[PER][8], k[2][8];
+    float v[PER][8];
+    uint4 raw[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-        widen(v[i], *(reinterpret_cast<const uint4 *>(p.c + t * p.ldc) + lane + 32 * i));
-    const int k0 = p.interleaved ? 2 * lane : lane, k1 = p.interleaved ? k0 + 1 : k0 + kRopeDims / 16;   // its chunks
-    const bool key = lane < kRopeDims / 16;
-    const uint4 *from = reinterpret_cast<const uint4 *>(p.k + t * p.ldk);
-    widen(k[0], key ? from[k0] : make_uint4(0, 0, 0, 0));
-    widen(k[1], key ? from[k1] : make_uint4(0, 0, 0, 0));
+        raw[i] = *(reinterpret_cast<const uint4 *>(p.c + t * p.ldc) + lane + 32 * i);
+    const int ka = p.interleaved ? 2 * lane : lane, kb = p.interleaved ? ka + 1 : ka + kRopeDims / 2;
+    const uint16_t *key = p.k + t * p.ldk;
+    uint16_t a = key[ka], b = key[kb];
     uint16_t *row = p.cache.data + slot * (L + kRopeDims);
     if (p.turns) {
-        s_cs[warp][lane] = turn_of(p.positions[t], __ldg(p.turns + lane), p.amplitude);
-        __syncwarp();
-        float2 cs[8];
+        const float2 cs = turn_of(p.positions[t], __ldg(p.turns + lane), p.amplitude);
+        const float x = __uint_as_float((uint32_t)a << 16), y = __uint_as_float((uint32_t)b << 16);
+        asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(a) : "f"(x * cs.x - y * cs.y));
+        asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(b) : "f"(y * cs.x + x * cs.y));
+    }
+    row[L + ka] = a;
+    row[L + kb] = b;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            cs[i] = s_cs[warp][(8 * lane + i) & (kRopeDims / 2 - 1)];
-        rotate16(k[0], k[1], p.interleaved, cs);
-    }
-    if (key) {
-        reinterpret_cast<uint4 *>(row + L)[k0] = narrow(k[0]);
-        reinterpret_cast<uint4 *>(row + L)[k1] = narrow(k[1]);
-    }
+    for (int i = 0; i < PER; ++i)
+        widen(v[i], raw[i]);
     if (p.norm) {
         float s = 0.0f;
 #pragma unroll
@@ -216,7 +212,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) latent_append_kernel(const 
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-        *(reinterpret_cast<uint4 *>(row) + lane + 32 * i) = narrow(v[i]);
+        *(reinterpret_cast<uint4 *>(row) + lane + 32 * i) = p.norm ? narrow(v[i]) : raw[i];             // without a norm the bits as they are
 }
 
 }  // namespace
@@ -227,13 +223,14 @@ cudaError_t launch_rotary(const RotaryProblem &p, int sms, cudaStream_t stream) 
     // Sets of a warp: one while that many warps fit on the GPU at once (64 tokens of 72 heads of 128, 2.6 us; with four, 3.5); else four or three,
     // as fewer lanes go without a head (4,000 tokens of 48 heads 18.0 and 18.7 us, with two 19.5; 8,192 of 18 heads of 256 43.7 and 32.9).
     auto waste = [&](int sets) { return (sets * set - heads % (sets * set)) % (sets * set); };
-    const int sets = (int64_t)p.T * heads * lanes <= (int64_t)sms * 512 ? 1 : waste(3) < waste(4) ? 3 : 4;
+    const bool norm = p.q.norm || p.k.norm;                // (it takes more registers: 22.1 us with three, 23.7 with four)
+    const int sets = (int64_t)p.T * heads * lanes <= (int64_t)sms * 512 ? 1 : waste(3) < waste(4) + norm ? 3 : 4;
     const int64_t jobs = (int64_t)p.T * ((heads + sets * set - 1) / (sets * set));
     const dim3 grid((unsigned)((jobs + kRotaryWarps - 1) / kRotaryWarps));
     auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(kRotaryWarps * 32), 0, stream, p); };
     auto form = [&](auto lanes_of) {
         constexpr int N = decltype(lanes_of)::value;
-        if (p.q.norm || p.k.norm)
+        if (norm)
             return sets == 1 ? go(rotary_kernel<N, 1, true>) : sets == 3 ? go(rotary_kernel<N, 3, true>) : go(rotary_kernel<N, 4, true>);
         return sets == 1 ? go(rotary_kernel<N, 1, false>) : sets == 3 ? go(rotary_kernel<N, 3, false>) : go(rotary_kernel<N, 4, false>);
     };
