@@ -32,6 +32,8 @@
 #define MOE_PLAN_TILE 64
 #define MOE_PLAN_UNIT_COST 3
 #define MOE_PLAN_MIN_COST 4
+#include <type_traits>
+
 #include "attn_plan.cuh"
 
 namespace moe {
@@ -642,36 +644,45 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Latent
                 }
             }
             float w[16];
-            // weights of the scores, two columns in an instruction; whether one has grown too far
-            auto weigh = [&]() -> bool {
+            // Weights of the scores, two columns in an instruction; whether one has grown too far.  (Its forms are apart, so that one has no
+            // branches: with the edge's tests inside, a tile took 150 ns more.)
+            auto weigh_as = [&](auto groups_of, auto edge_of) -> bool {
+                constexpr int G = decltype(groups_of)::value;
+                constexpr bool EDGE = decltype(edge_of)::value;
                 float most = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i < groups) {
+                for (int i = 0; i < G; ++i)
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            float y0, y1;
-                            asm("{\n.reg .b64 a, b;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nadd.rn.f32x2 a, a, b;\nmov.b64 b, {%6, %6};\n"
-                                "mul.rn.f32x2 a, a, b;\nmov.b64 {%0, %1}, a;\n}\n"
-                                : "=f"(y0), "=f"(y1)
-                                : "f"(x[4 * i + 2 * k]), "f"(x[4 * i + 2 * k + 1]), "f"(-ref[2 * i]), "f"(-ref[2 * i + 1]), "f"(f));
-                            float v0 = ex2(y0), v1 = ex2(y1);
-                            if (edge) {
-                                const int j = tok_a + 8 * k, c = col0 + 8 * i;
-                                const bool sees0 = tok + j < s.hi[c], sees1 = tok + j < s.hi[c + 1];
-                                if (s.bad[j / 32] >> (j & 31) & 1)
-                                    v0 = v1 = __uint_as_float(0x7FFFFFFFu);
-                                v0 = sees0 ? v0 : 0.0f;
-                                v1 = sees1 ? v1 : 0.0f;
-                                y0 = sees0 ? y0 : -INFINITY;
-                                y1 = sees1 ? y1 : -INFINITY;
-                            }
-                            w[4 * i + 2 * k] = v0;
-                            w[4 * i + 2 * k + 1] = v1;
-                            most = fmaxf(most, fmaxf(y0, y1));
+                    for (int k = 0; k < 2; ++k) {
+                        float y0, y1;
+                        asm("{\n.reg .b64 a, b;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nadd.rn.f32x2 a, a, b;\nmov.b64 b, {%6, %6};\n"
+                            "mul.rn.f32x2 a, a, b;\nmov.b64 {%0, %1}, a;\n}\n"
+                            : "=f"(y0), "=f"(y1)
+                            : "f"(x[4 * i + 2 * k]), "f"(x[4 * i + 2 * k + 1]), "f"(-ref[2 * i]), "f"(-ref[2 * i + 1]), "f"(f));
+                        float v0 = ex2(y0), v1 = ex2(y1);
+                        if (EDGE) {
+                            const int j = tok_a + 8 * k, c = col0 + 8 * i;
+                            const bool sees0 = tok + j < s.hi[c], sees1 = tok + j < s.hi[c + 1];
+                            if (s.bad[j / 32] >> (j & 31) & 1)
+                                v0 = v1 = __uint_as_float(0x7FFFFFFFu);
+                            v0 = sees0 ? v0 : 0.0f;
+                            v1 = sees1 ? v1 : 0.0f;
+                            y0 = sees0 ? y0 : -INFINITY;
+                            y1 = sees1 ? y1 : -INFINITY;
                         }
+                        w[4 * i + 2 * k] = v0;
+                        w[4 * i + 2 * k + 1] = v1;
+                        most = fmaxf(most, fmaxf(y0, y1));
                     }
                 return most > kMostPower;
+            };
+            auto weigh = [&]() -> bool {
+                using std::integral_constant;
+                if (groups == 4)
+                    return edge ? weigh_as(integral_constant<int, 4>(), std::true_type()) : weigh_as(integral_constant<int, 4>(), std::false_type());
+                if (groups == 2)
+                    return edge ? weigh_as(integral_constant<int, 2>(), std::true_type()) : weigh_as(integral_constant<int, 2>(), std::false_type());
+                return false;
             };
             auto store = [&] {
 #pragma unroll
@@ -789,10 +800,16 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Latent
                 float o[16];
                 tmem_ld_32x16(o, lanes + 64 * (i >> 1) + c);
                 float *to = g.part + ((size_t)slot * g.cap + c) * L + 128 * (i >> 1) + 32 * quarter + lane;
+                if (n >= 16) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (e < n)
-                        __stcg(to + (size_t)e * L, o[e]);
+                    for (int e = 0; e < 16; ++e)
+                        __stcg(to + e * L, o[e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 15; ++e)
+                        if (e < n)
+                            __stcg(to + e * L, o[e]);
+                }
             }
         } else {
             // rows of out lie one after the other: they are put together where the queries were, and leave as one copy
