@@ -764,7 +764,11 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Latent
         }
         // the scores are all made: the next piece's queries may come, unless results are put together where they go
         const long long out_row = first_row();
-        const int slot = slot_of(), rows = m.rows;
+        const int slot = slot_of();
+        int rows = m.rows;
+        if (!MOE_DBG_IN_RANGE(slot, 2 * kMaxAttnCtas, g.a.hdr) || !MOE_DBG_IN_RANGE(rows - 1, g.cap, g.a.hdr) ||
+            !MOE_DBG_IN_RANGE(out_row, (long long)p.T * p.heads - rows + 1, g.a.hdr))
+            rows = 0;
         more = advance();
         if (more && !whole)
             load_queries();
@@ -959,9 +963,14 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentA
     const int total = s_end[kMaxAttnCtas - 1];
     for (int i = blockIdx.x; i < total; i += gridDim.x) {
         const int c = __syncthreads_count(tid < kMaxAttnCtas && s_end[tid] <= i);
+        if (!MOE_DBG_IN_RANGE(c, ctas, g.a.hdr))
+            continue;
         const LatentJoin j = g.joins[c];
         const int r = i - (c ? s_end[c - 1] : 0), part = g.split == 1 ? 0 : c & 1, parts = j.last - j.first + 1;
         auto slot = [&](int k) { return (size_t)(((j.first + k) * 2 + (k == 0)) * g.split + part) * g.cap + r; };
+        if (!MOE_DBG_IN_RANGE(r, g.cap, g.a.hdr) || !MOE_DBG_IN_RANGE(parts - 1, kMaxAttnCtas, g.a.hdr) ||
+            !MOE_DBG_IN_RANGE(j.row + r, (long long)g.p.T * g.p.heads, g.a.hdr))
+            continue;
         const float2 e = tid < parts ? __ldcg(g.part_sum + slot(tid)) : make_float2(-INFINITY, 0.0f);
         float m = e.x;
 #pragma unroll
@@ -1050,7 +1059,11 @@ struct Shape {
     }
 };
 
-int max_units(int T, int B, const Shape &s, int heads) { return (int)((long long)T * heads / s.rows + B); }
+// Most units of any lengths: a request with n tokens has ceil(n heads / rows), no more than n ceil(heads / rows).
+int max_units(int T, int B, const Shape &s, int heads) {
+    const long long a = (long long)T * ((heads + s.rows - 1) / s.rows), b = ((long long)T * heads + (long long)(T < B ? T : B) * (s.rows - 1)) / s.rows;
+    return (int)(a < b ? a : b);
+}
 
 struct LatentLayout {
     size_t plan, recs, joins, part, part_sum, total;

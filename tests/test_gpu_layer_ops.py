@@ -8,6 +8,7 @@ import torch
 
 import layer_ops_reference as ref
 from block_scaled_fp4_moe_gb300 import _build, attn, moe
+from test_gpu_attn_forms import has, kernels
 
 pytestmark = pytest.mark.gpu
 
@@ -553,3 +554,34 @@ def test_two_captured_graphs_share_a_workspace():
         torch.cuda.synchronize()
         assert all(torch.equal(o, w) for o, w in zip(outs, want))
     assert moe.moe_check_device_status(ws) == 0
+
+
+# ------------------------------------------- the range-checked build, launch forms
+
+def test_range_checked_build_finds_nothing_and_computes_the_same():
+    steps = [Step([900, 30, 0, 4000], [1, 2, 0, 3], 64, 512, 64, seed=30), Step([3000], [1], 16, 256, 16, seed=31), Step([130, 700], [40, 9], 128, 512, 32, seed=32)]
+    want = [s.run() for s in steps]
+    with moe.debug_bounds():
+        for s, (out, lse) in zip(steps, want):
+            got, got_lse = s.run()
+            assert moe.moe_check_device_status(s.ws) == 0
+            assert torch.equal(got, out) and torch.equal(got_lse, lse)
+
+
+@pytest.mark.parametrize("kv,n,heads,plans", [([700] * 3, [1] * 3, 16, 0), ([64] * 152, [1] * 152, 64, 0), ([64] * 153, [1] * 153, 64, 1),
+                                              ([9] * 300, [1] * 300, 8, 1), ([300], [300], 64, 0), ([2000], [2000], 16, 1), ([500] * 150, [1] * 150, 128, 0),
+                                              ([70] * 100, [2] * 100, 40, 1)])
+def test_latent_attention_on_both_sides_of_the_plan_kernel(kv, n, heads, plans, tmp_path):
+    """Up to 152 units every CTA makes the plan itself, above a kernel before does."""
+    s = Step(kv, n, heads, 512, 64, seed=len(kv))
+    s.check()
+    args = (attn.LatentCache(s.data), s.table, i32(s.offsets), i32(s.kv), s.scale, torch.empty_like(s.ql, memory_format=torch.contiguous_format), None, s.ws)
+    names = [x for x in kernels(lambda: attn.moe_latent_attention(s.ql, s.qr, *args), tmp_path) if "latent" in x]
+    assert has(names, "latent_plan_kernel") == bool(plans) and has(names, "latent_kernel", 512) and has(names, "latent_join_kernel", 512), names
+
+
+@pytest.mark.parametrize("heads", [15, 16, 17, 47, 48, 49, 63, 64, 65, 80, 81, 96, 127, 128, 129, 160, 255, 256])
+def test_latent_attention_head_counts_around_the_tiles(heads):
+    """Units of 16 rows and of 64, two CTAs to a unit above, two units to a token above 128."""
+    Step([200, 333, 64], [1, 1, 1], heads, 512, 64, seed=heads).check()
+    Step([90, 130], [3, 2], heads, 256, 16, seed=heads).check()
