@@ -928,85 +928,95 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(AttnArgs a) {
     make_plan(a, s_first, red, a.recs, a.plan, true);
 }
 
-// The parts of cut units, in the order of the cache.  A CTA takes rows of all cut units in turn: L / 4 threads with four dims each for
-// every second part, so that many parts' loads are in flight.
-constexpr int kJoinThreads = 256;
+// The parts of cut units, in the order of the cache.  A warp takes 128 dims of a row at a time, by itself (with a row to a CTA and barriers
+// 9,600 rows of two or three parts each took 40 us, this way 8), several parts' loads in flight; where there are no more such
+// jobs than CTAs, the warps of one share its parts (64 rows of 152 parts: 26 us by themselves, 10).
+constexpr int kJoinWarps = 8;
 template <int L>
-__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentArgs g, int ctas) {
-    constexpr int kDims = L / 4, kGroups = kJoinThreads / kDims, U = 8;
+__global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const LatentArgs g, int ctas) {
+    constexpr int kCols = L / 128, U = 8, kPer = kMaxAttnCtas / 32;
+    __shared__ LatentJoin s_join[kMaxAttnCtas];
     __shared__ int s_end[kMaxAttnCtas];          // rows to join of the CTAs up to this one
-    __shared__ float s_w[kMaxAttnCtas];
-    __shared__ float s_red[2][kJoinThreads / 32];
-    __shared__ float4 s_o[kJoinThreads - kDims];
+    __shared__ float s_w[kJoinWarps][kMaxAttnCtas];
+    __shared__ float4 s_o[kJoinWarps][32];
+    static_assert(kMaxAttnCtas % 32 == 0 && kMaxAttnCtas <= kJoinWarps * 32, "a thread a CTA");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
     pdl_trigger();
-    int n = tid < ctas ? g.joins[tid].rows : 0;
-    const int any = __syncthreads_or(n);
-    if (!any)
+    LatentJoin mine{0, 0, 0, 0};
+    if (tid < ctas)
+        mine = g.joins[tid];
+    if (tid < kMaxAttnCtas)
+        s_join[tid] = mine;
+    if (!__syncthreads_or(mine.rows))
         return;
+    if (warp == 0) {                             // the sums of rows
+        int n[kPer], sum = 0;
 #pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-        const int v = __shfl_up_sync(0xffffffffu, n, d);
-        n += lane >= d ? v : 0;
+        for (int i = 0; i < kPer; ++i)
+            sum += n[i] = s_join[kPer * lane + i].rows;
+        int ahead = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int v = __shfl_up_sync(0xffffffffu, ahead, d);
+            ahead += lane >= d ? v : 0;
+        }
+        ahead -= sum;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            s_end[kPer * lane + i] = ahead += n[i];
     }
-    if (tid < kMaxAttnCtas)
-        s_end[tid] = n;
     __syncthreads();
-    int ahead = 0;
-    for (int w = 0; w < warp && w < kMaxAttnCtas / 32; ++w)
-        ahead += s_end[32 * w + 31];
-    __syncthreads();
-    if (tid < kMaxAttnCtas)
-        s_end[tid] = n + ahead;
-    __syncthreads();
-    const int total = s_end[kMaxAttnCtas - 1];
-    for (int i = blockIdx.x; i < total; i += gridDim.x) {
-        const int c = __syncthreads_count(tid < kMaxAttnCtas && s_end[tid] <= i);
+    const int jobs = s_end[kMaxAttnCtas - 1] * kCols;
+    const bool shared = jobs <= (int)gridDim.x;  // then one job a CTA, or none
+    const int stride = shared ? kJoinWarps : 1;
+    for (int job = shared ? (int)blockIdx.x : blockIdx.x * kJoinWarps + warp; job < jobs; job += gridDim.x * kJoinWarps) {
+        const int i = job / kCols;
+        int c = 0;                               // whose row it is: CTAs with no more rows up to them
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+            c += __popc(__ballot_sync(0xffffffffu, s_end[32 * k + lane] <= i));
         if (!MOE_DBG_IN_RANGE(c, ctas, g.a.hdr))
             continue;
-        const LatentJoin j = g.joins[c];
+        const LatentJoin j = s_join[c];
         const int r = i - (c ? s_end[c - 1] : 0), part = g.split == 1 ? 0 : c & 1, parts = j.last - j.first + 1;
-        auto slot = [&](int k) { return (size_t)(((j.first + k) * 2 + (k == 0)) * g.split + part) * g.cap + r; };
         if (!MOE_DBG_IN_RANGE(r, g.cap, g.a.hdr) || !MOE_DBG_IN_RANGE(parts - 1, kMaxAttnCtas, g.a.hdr) ||
             !MOE_DBG_IN_RANGE(j.row + r, (long long)g.p.T * g.p.heads, g.a.hdr))
             continue;
-        const float2 e = tid < parts ? __ldcg(g.part_sum + slot(tid)) : make_float2(-INFINITY, 0.0f);
-        float m = e.x;
+        auto slot = [&](int k) { return (size_t)(((j.first + k) * 2 + (k == 0)) * g.split + part) * g.cap + r; };
+        float2 e[kPer];
+        float m = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+            const int k = 32 * q + lane;
+            e[q] = k < parts ? __ldcg(g.part_sum + slot(k)) : make_float2(-INFINITY, 0.0f);
+            m = fmaxf(m, e[q].x);
+        }
 #pragma unroll
         for (int d = 16; d > 0; d /= 2)
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        if (lane == 0)
-            s_red[0][warp] = m;
-        __syncthreads();
-        m = s_red[0][0];
+        float l = 0.0f;
+        __syncwarp();
 #pragma unroll
-        for (int w = 1; w < kJoinThreads / 32; ++w)
-            m = fmaxf(m, s_red[0][w]);
-        const float w0 = ex2((e.x - m) * g.factor);
-        if (tid < parts)
-            s_w[tid] = e.y == 0.0f ? -1.0f : w0;             // below zero: it saw nothing, and its sums were not written
-        float l = e.y == 0.0f ? 0.0f : e.y * w0;
+        for (int q = 0; q < kPer; ++q) {
+            const float w = ex2((e[q].x - m) * g.factor);
+            s_w[warp][32 * q + lane] = e[q].y == 0.0f ? -1.0f : w;             // below zero: it saw nothing, and its sums were not written
+            l += e[q].y == 0.0f ? 0.0f : e[q].y * w;
+        }
 #pragma unroll
         for (int d = 16; d > 0; d /= 2)
             l += __shfl_xor_sync(0xffffffffu, l, d);
-        if (lane == 0)
-            s_red[1][warp] = l;
-        __syncthreads();
-        l = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kJoinThreads / 32; ++w)
-            l += s_red[1][w];
-        const int d = tid % kDims, group = tid / kDims;
+        __syncwarp();
+        const int d = (job % kCols) * 32 + lane;
         float4 o = make_float4(0, 0, 0, 0);
-        for (int k0 = group; k0 < parts; k0 += U * kGroups) {
+        for (int k0 = shared ? warp : 0; k0 < parts; k0 += U * stride) {
             float4 v[U];
             float w[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int k = k0 + u * kGroups;
-                const bool in = k < parts && !(s_w[k] < 0.0f);
-                w[u] = in ? s_w[k] : 0.0f;
+                const int k = k0 + u * stride;
+                const bool in = k < parts && !(s_w[warp][k] < 0.0f);
+                w[u] = in ? s_w[warp][k] : 0.0f;
                 v[u] = in ? __ldcg(reinterpret_cast<const float4 *>(g.part + slot(k) * L) + d) : make_float4(0, 0, 0, 0);
             }
 #pragma unroll
@@ -1017,23 +1027,24 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentA
                 o.w = fmaf(v[u].w, w[u], o.w);
             }
         }
-        if (group > 0)
-            s_o[tid - kDims] = o;
-        __syncthreads();
-        if (group == 0) {
+        if (shared) {
+            s_o[warp][lane] = o;
+            __syncthreads();                     // all of the CTA's warps have the same job
+            if (warp > 0)
+                break;
 #pragma unroll
-            for (int q = 0; q < kGroups - 1; ++q) {
-                const float4 v = s_o[q * kDims + d];
+            for (int w = 1; w < kJoinWarps; ++w) {
+                const float4 v = s_o[w][lane];
                 o.x += v.x;
                 o.y += v.y;
                 o.z += v.z;
                 o.w += v.w;
             }
-            const float by = l == 0.0f ? 0.0f : 1.0f / l;
-            reinterpret_cast<uint2 *>(g.p.out + (j.row + r) * L)[d] = make_uint2(bf16_pair(o.x * by, o.y * by), bf16_pair(o.z * by, o.w * by));
-            if (d == 0 && g.p.lse)
-                g.p.lse[j.row + r] = l == 0.0f ? -INFINITY : fmaf(m, g.p.scale, logf(l));
         }
+        const float by = l == 0.0f ? 0.0f : 1.0f / l;
+        reinterpret_cast<uint2 *>(g.p.out + (j.row + r) * L)[d] = make_uint2(bf16_pair(o.x * by, o.y * by), bf16_pair(o.z * by, o.w * by));
+        if (d == 0 && g.p.lse)
+            g.p.lse[j.row + r] = l == 0.0f ? -INFINITY : fmaf(m, g.p.scale, logf(l));
     }
 }
 
@@ -1135,7 +1146,7 @@ cudaError_t launch(const LatentProblem &p, void *ws, int sms, cudaStream_t strea
         e = launch_pdl(latent_plan_kernel, dim3(1), dim3(kPlanThreads), p.B * sizeof(int), stream, g.a);
     if (e == cudaSuccess)
         e = launch_pdl(latent_kernel<L>, dim3(ctas), dim3(kThreads), smem, stream, g, pair_map, chunk_map);
-    return e != cudaSuccess ? e : launch_pdl(latent_join_kernel<L>, dim3(4 * ctas), dim3(kJoinThreads), 0, stream, g, ctas);
+    return e != cudaSuccess ? e : launch_pdl(latent_join_kernel<L>, dim3(4 * ctas), dim3(kJoinWarps * 32), 0, stream, g, ctas);
 }
 
 }  // namespace
