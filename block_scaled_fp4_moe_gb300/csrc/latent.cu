@@ -23,9 +23,9 @@
 // are not finite, and their weight NaN for the rows that do see them.
 //
 // Work is cut as in attn.cu (attn_plan.cuh): units of rows, their tiles laid end to end and cut into equal ranges; a range that cuts a
-// unit leaves its sums in the workspace, and latent_join_kernel adds them up, a few rows a CTA (one request's parts are many:
-// the last CTA alone would be a while at it).  With more than 64 rows a token two CTAs take the halves of a
-// unit's rows, side by side, so that the second reads the cache from L2.
+// unit leaves its sums in the workspace, and latent_join_kernel adds them up (one request's parts are many: the last CTA alone would be a
+// while at it).  With more than 64 heads and single tokens two CTAs take the halves of a unit's rows, side by side, so that the second reads
+// the cache from L2.
 //
 // Warps: 0..7 softmax (warp % 4 = lane quarter, 16 tokens each; warp / 4 = half of the rows), 8 streams the cache, 9 and 10 issue the products
 // (one warp for both was often at the scores' when weights were ready: 64 requests of 16,384 tokens, 64 heads, 292 us).
@@ -1048,20 +1048,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Late
     }
 }
 
-// How rows become units.  Two CTAs share a unit where a token has more than 64 rows, or requests do on average: the cache is
-// then read from memory once for up to 128 rows.  Units of a single token's heads are even.
+// How rows become units.  Requests of single tokens (T <= B, so that no more is known but that) of more than 64 heads: two CTAs share units
+// of up to 128 rows, the heads cut evenly, so that the cache is read from memory once (48 ragged requests of 96 heads 106 us, and 115 with a
+// unit a CTA; 64 of 128 heads 236 and 263).  Otherwise units of 64 rows, a CTA each: what several tokens of a request read again comes from L2
+// as often as not, and no CTA waits for rows that its unit lacks (16 requests of 1..4 tokens of 32 heads 76 us, and 91 with two CTAs a unit; one
+// of 400 tokens of 64 heads 169 and 181).
 struct Shape {
     int split, rows, q_rows, cap;
     Shape(int T, int B, int heads) {
         const long long all = (long long)T * heads;
-        split = (T <= B ? heads : (all + B - 1) / B) > kMaxRows ? 2 : 1;
-        const int most = split * kMaxRows;
-        if (T <= B) {
-            const int units = (heads + most - 1) / most;
-            rows = (heads + units - 1) / units;
-        } else {
-            rows = most;
-        }
+        split = T <= B && heads > kMaxRows ? 2 : 1;
+        const int most = split * kMaxRows, units = T <= B ? (heads + most - 1) / most : 1;
+        rows = T <= B ? (heads + units - 1) / units : kMaxRows;
         q_rows = split == 1 ? rows : (rows + 1) / 2;
         if (q_rows > all)
             q_rows = (int)all;

@@ -569,7 +569,7 @@ def test_range_checked_build_finds_nothing_and_computes_the_same():
 
 
 @pytest.mark.parametrize("kv,n,heads,plans", [([700] * 3, [1] * 3, 16, 0), ([64] * 152, [1] * 152, 64, 0), ([64] * 153, [1] * 153, 64, 1),
-                                              ([9] * 300, [1] * 300, 8, 1), ([300], [300], 64, 0), ([2000], [2000], 16, 1), ([500] * 150, [1] * 150, 128, 0),
+                                              ([9] * 300, [1] * 300, 8, 1), ([150], [150], 64, 0), ([2000], [2000], 16, 1), ([500] * 150, [1] * 150, 128, 0),
                                               ([70] * 100, [2] * 100, 40, 1)])
 def test_latent_attention_on_both_sides_of_the_plan_kernel(kv, n, heads, plans, tmp_path):
     """Up to 152 units every CTA makes the plan itself, above a kernel before does."""
@@ -585,3 +585,11 @@ def test_latent_attention_head_counts_around_the_tiles(heads):
     """Units of 16 rows and of 64, two CTAs to a unit above, two units to a token above 128."""
     Step([200, 333, 64], [1, 1, 1], heads, 512, 64, seed=heads).check()
     Step([90, 130], [3, 2], heads, 256, 16, seed=heads).check()
+
+
+@pytest.mark.parametrize("kv,n,heads", [([3000] * 8, [1, 2, 3, 4] * 2, 32), ([5000, 100, 4000], [1, 0, 1], 96), ([700] * 16, [1] * 16, 130),
+                                        ([9000, 64], [2, 0], 80), ([2000, 65, 1], [1, 1, 1], 129), ([900] * 4, [1, 0, 0, 3], 100)])
+def test_latent_attention_of_ragged_rows(kv, n, heads):
+    """No more tokens than requests, and more: units that two CTAs share (a request's tokens may still be several), and units of 64 rows."""
+    Step(kv, n, heads, 512, 64, seed=sum(n) + heads).check()
+    Step(kv, n, heads, 256, 16, seed=sum(n) + heads).check(causal=False)
