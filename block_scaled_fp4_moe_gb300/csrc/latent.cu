@@ -31,7 +31,7 @@
 // (one warp for both was often at the scores' when weights were ready: 64 requests of 16,384 tokens, 64 heads, 292 us).
 #define MOE_PLAN_TILE 64
 #define MOE_PLAN_UNIT_COST 3
-#define MOE_PLAN_MIN_COST 4
+#define MOE_PLAN_MIN_COST 3
 #include <type_traits>
 
 #include "attn_plan.cuh"
@@ -859,6 +859,49 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Latent
         g.joins[blockIdx.x] = join;
 }
 
+// The plan of up to 32 requests, by one warp (make_small_plan takes a microsecond longer).
+template <int L>
+__device__ __forceinline__ void few_requests_plan(const LatentArgs &g, const LatentSmem<L> &s) {
+    const AttnProblem &p = g.a.p;
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = 0, kv = 0;
+    bool bad = false;
+    if (lane < p.B) {
+        const int hi = p.q_offsets[lane + 1];
+        lo = p.q_offsets[lane];
+        kv = p.kv_lens[lane];
+        n = hi - lo;
+        bad = lo < 0 || hi < lo || hi > p.T || kv < 0 || kv > ((long long)p.max_blocks << g.a.shift);
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    const int count = bad ? 0 : (int)(((long long)n * g.a.group + g.a.rows - 1) / g.a.rows);
+    int cost = 0;                                // small plans' work fits an int
+    for (int i = 0; i < count; ++i)
+        cost += row_tile(g.a, lane, lo, n, kv, i * g.a.rows).tiles + kUnitCost;
+    int units = count, work = cost;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int u = __shfl_up_sync(0xffffffffu, units, d), w = __shfl_up_sync(0xffffffffu, work, d);
+        if (lane >= d) {
+            units += u;
+            work += w;
+        }
+    }
+    const int total = __shfl_sync(0xffffffffu, units, 31);
+    const bool fits = total <= g.a.max_tiles;    // offsets within T leave no other choice
+    int before = work - cost;
+    for (int i = 0; i < count && fits; ++i) {
+        s.before[units - count + i] = before;
+        s.which[units - count + i] = (uint16_t)(lane | i << 8);
+        before += row_tile(g.a, lane, lo, n, kv, i * g.a.rows).tiles + kUnitCost;
+    }
+    if (lane == 31) {
+        if ((bad || !fits) && blockIdx.x == 0)
+            record_status(g.a.hdr, MOE_ERR_DEVICE_ASSERT);
+        *s.plan = bad || !fits ? Plan{0, 1, 0, 0} : plan_of(g.a, work, total);
+    }
+}
+
 template <int L>
 __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_constant__ LatentArgs g, const __grid_constant__ CUtensorMap pair_map,
                                                              const __grid_constant__ CUtensorMap chunk_map) {
@@ -893,7 +936,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
     const uint32_t tmem = *s.taddr;
     pdl_wait();
     pdl_trigger();
-    if (g.small) {                               // the plan, made where the cache's tiles go and kept in few words
+    if (g.small && g.a.p.B <= 32) {              // a lane a request
+        if (warp == 0)
+            few_requests_plan<L>(g, s);
+    } else if (g.small) {                        // the plan, made where the cache's tiles go and kept in few words
         RowTile *recs = reinterpret_cast<RowTile *>(s.ring + 1024);
         make_small_plan(g.a, reinterpret_cast<long long *>(s.ring), recs, s.plan, blockIdx.x == 0);
         for (int i = threadIdx.x; i < s.plan->row_tiles; i += kThreads) {
@@ -941,8 +987,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Late
     __shared__ float4 s_o[kJoinWarps][32];
     static_assert(kMaxAttnCtas % 32 == 0 && kMaxAttnCtas <= kJoinWarps * 32, "a thread a CTA");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_trigger();                               // the kernel after may be scheduled while this one waits: it waits for this one's end
     pdl_wait();
-    pdl_trigger();
     LatentJoin mine{0, 0, 0, 0};
     if (tid < ctas)
         mine = g.joins[tid];
