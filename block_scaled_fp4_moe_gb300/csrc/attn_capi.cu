@@ -251,6 +251,10 @@ moe_status_t moe_rotary(const uint16_t *q, int64_t q_stride_t, int64_t q_stride_
         return MOE_OK;
     if (!q || !q_out || !positions || !turns || (k_heads > 0 && (!k || !k_out)))
         return MOE_ERR_INVALID_ARG;
+    // rows of an output lie apart
+    if ((T > 1 && (q_out_stride_t < head_dim || (k_heads > 0 && k_out_stride_t < head_dim))) ||
+        (q_heads > 1 && q_out_stride_h < head_dim) || (k_heads > 1 && k_out_stride_h < head_dim))
+        return MOE_ERR_INVALID_ARG;
     if ((q == q_out && (q_stride_t != q_out_stride_t || q_stride_h != q_out_stride_h)) ||
         (k_heads > 0 && k == k_out && (k_stride_t != k_out_stride_t || k_stride_h != k_out_stride_h)))
         return MOE_ERR_INVALID_ARG;

@@ -54,6 +54,7 @@ constexpr long long kSmallTokens = 1ll << 29;               // and tokens of a r
 struct LatentJoin {
     long long row;                           // first of its rows in out
     int rows, first, last;
+    int blind;                               // its first rows that see nothing
 };
 
 struct LatentArgs {
@@ -527,7 +528,7 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Latent
     LatentWalk<L> walk(g, s);
     Piece pc{};
     Mine m;
-    LatentJoin join{0, 0, 0, 0};
+    LatentJoin join{0, 0, 0, 0, 0};
     uint32_t tiles = 0;                                      // so far
     auto first_row = [&] { return (long long)pc.q0 * p.heads + m.row0; };
     auto slot_of = [&] { return (walk.cta * 2 + (walk.cta == pc.first)) * g.split + part; };
@@ -537,8 +538,11 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Latent
             m = Mine(g, pc);
             if (m.rows == 0)
                 continue;
-            if (pc.first != pc.last && walk.cta == pc.first)
-                join = LatentJoin{first_row(), m.rows, pc.first, pc.last};
+            if (pc.first != pc.last && walk.cta == pc.first) {
+                // a row sees something unless its token lies before position 0
+                const int token = p.causal ? max(0, pc.n - pc.kv) : 0;
+                join = LatentJoin{first_row(), m.rows, pc.first, pc.last, (int)max(0ll, min((long long)token * p.heads - m.row0, (long long)m.rows))};
+            }
             if (m.tiles > 0)
                 return true;
             if (pc.first == pc.last) {
@@ -640,7 +644,7 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Latent
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int col = col0 + 8 * (i >> 1) + (i & 1);
-                    ref[i] = tok < s.hi[col] ? s.ref[col] : 0.0f;
+                    ref[i] = tok < s.hi[col] ? fmaxf(s.ref[col], -3.4e38f) : 0.0f;         // finite, should that score have left fp32 below
                 }
             }
             float w[16];
@@ -787,7 +791,9 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Latent
         }
         soft_sync();
         if (tid < rows) {
-            const float l = (s.red[tid] + s.red[64 + tid]) + (s.red[128 + tid] + s.red[192 + tid]);
+            float l = (s.red[tid] + s.red[64 + tid]) + (s.red[128 + tid] + s.red[192 + tid]);
+            if (whole && l == 0.0f && s.hi[tid] > 0)         // it sees positions, and every score left fp32 below
+                l = __uint_as_float(0x7FFFFFFFu);
             s.sum[tid] = l == 0.0f ? 0.0f : 1.0f / l;
             if (!whole)
                 __stcg(g.part_sum + (size_t)slot * g.cap + tid, make_float2(l == 0.0f ? -INFINITY : s.ref[tid], l));
@@ -989,7 +995,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Late
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_trigger();                               // the kernel after may be scheduled while this one waits: it waits for this one's end
     pdl_wait();
-    LatentJoin mine{0, 0, 0, 0};
+    LatentJoin mine{0, 0, 0, 0, 0};
     if (tid < ctas)
         mine = g.joins[tid];
     if (tid < kMaxAttnCtas)
@@ -1087,6 +1093,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Late
                 o.w += v.w;
             }
         }
+        if (l == 0.0f && r >= j.blind)           // it sees positions, and every score left fp32 below
+            l = __uint_as_float(0x7FFFFFFFu);
         const float by = l == 0.0f ? 0.0f : 1.0f / l;
         reinterpret_cast<uint2 *>(g.p.out + (j.row + r) * L)[d] = make_uint2(bf16_pair(o.x * by, o.y * by), bf16_pair(o.z * by, o.w * by));
         if (d == 0 && g.p.lse)

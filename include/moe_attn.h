@@ -227,9 +227,11 @@ size_t moe_latent_attention_workspace_size(int T, int B, int heads, int latent_d
  * q_latent [T, heads, latent_dim] and q_rope [T, heads, 64] bf16, element (t, h, i) at t * stride_t + h * stride_h + i.  Rows of a request,
  * what they see (causal or not), rows that see nothing, rows past q_offsets[B], table entries that are not read and device-side errors are as in
  * moe_kv_attention.  What a row does not see has no influence, NaN included; a row that sees a token with a value that is not finite is
- * NaN in those dims at least.  Products are exact, sums and softmax statistics fp32; the weights are
- * rounded to bf16, relative to themselves.  The same arguments give the same bits on the same device.
- * heads <= 256, B <= 8192, T <= 2^20, T * heads < 2^31; q 16-byte aligned, strides multiples of 8.  Three launches at most.
+ * not finite in those dims at least.  Products are exact, sums and softmax statistics fp32; the weights are
+ * rounded to bf16, relative to themselves.  Scores may be of any size that fp32 holds; a row whose largest score leaves that range is NaN.  Latent
+ * values may be of magnitudes up to 2^70.  The same arguments give the same bits on the same device.
+ * heads <= 256, B <= 8192, T <= 2^20, T * heads < 2^31; q and out 16-byte aligned, strides multiples of 8; out overlaps no input.  Two
+ * launches, or three with many requests.
  */
 moe_status_t moe_latent_attention(const uint16_t *q_latent, int64_t ql_stride_t, int64_t ql_stride_h, const uint16_t *q_rope,
                                   int64_t qr_stride_t, int64_t qr_stride_h, int T, int heads, const moe_latent_cache_t *cache,

@@ -593,3 +593,43 @@ def test_latent_attention_of_ragged_rows(kv, n, heads):
     """No more tokens than requests, and more: units that two CTAs share (a request's tokens may still be several), and units of 64 rows."""
     Step(kv, n, heads, 512, 64, seed=sum(n) + heads).check()
     Step(kv, n, heads, 256, 16, seed=sum(n) + heads).check(causal=False)
+
+
+@pytest.mark.parametrize("kv,n", [([200], [1]), ([9000], [2]), ([700, 30], [3, 1])])
+def test_latent_attention_scores_that_leave_fp32(kv, n):
+    """Below: such tokens weigh nothing, the request's first one too; where all are, and above, the row is NaN."""
+    s = Step(kv, n, 16, 512, 64, seed=40)
+    s.ql, s.qr = torch.zeros_like(s.ql), torch.zeros_like(s.qr)
+    s.ql[:, 0::2, 0] = 1e20                                # every second head: scores -1e40 of tokens with -1e20 there
+    s.ql[..., 1] = 1.0
+    for b in range(len(kv)):
+        for j in range(kv[b]):
+            page, off = s.slot(b, j)
+            s.data[page, off, 0] = -1e20 if j % 3 == 0 else 0.0
+    out, lse = s.run()
+    assert moe.moe_check_device_status(s.ws) == 0
+    for b in range(len(kv)):
+        k = s.data[s.table[b, : -(-kv[b] // 64)].long()].double().reshape(-1, 576)[:kv[b]]
+        for t in range(s.offsets[b], s.offsets[b + 1]):
+            seen = kv[b] - (s.offsets[b + 1] - t) + 1
+            x = (s.scale * k[:seen, 1]).clone()
+            x[0::3] = -math.inf
+            want, want_lse = torch.softmax(x, 0) @ k[:seen, 1:512], torch.logsumexp(x, 0)
+            size = torch.softmax(x, 0) @ k[:seen, 1:512].abs()
+            bound = (ref.U16 + 4 * seen * ref.U32) * size * (1 + ref.U16) + ref.U16 * want.abs() + 1e-30
+            within(out[t, 0::2, 1:], want.expand(8, -1), bound.expand(8, -1))
+            assert ((lse[t, 0::2].double() - want_lse).abs() < 1e-5).all()
+    for value in (-1e20, 1e20):
+        for b in range(len(kv)):
+            for j in range(kv[b]):
+                page, off = s.slot(b, j)
+                s.data[page, off, 0] = value
+        out, lse = s.run()
+        assert out[:, 0::2, 1:].isnan().all() and lse[:, 0::2].isnan().all()
+        assert torch.isfinite(out[:, 1::2, 1:].float()).all() and torch.isfinite(lse[:, 1::2]).all()
+
+
+def test_latent_attention_rows_before_the_first_position_in_a_cut_unit():
+    """A request with more new tokens than it has tokens at all, long enough for its units to be cut."""
+    Step([900], [1400], 4, 256, 16, seed=41).check()
+    Step([130], [135], 2, 512, 64, seed=42).check()

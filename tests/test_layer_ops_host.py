@@ -48,7 +48,7 @@ def rotary(L, q=FAKE, qt=1024, qh=128, qo=FAKE + 4096, qot=1024, qoh=128, hq=8, 
 def test_rotary_refusals(L):
     for kw in (dict(T=-1), dict(hq=0), dict(hk=-1), dict(D=0), dict(pairs=0), dict(offset=-8), dict(amp=NAN), dict(amp=INF), dict(eps=-1.0), dict(inter=2),
                dict(qt=-8), dict(koh=-8), dict(q=0), dict(qo=0), dict(k=0), dict(ko=0), dict(pos=0), dict(turns=0), dict(qo=FAKE, qot=2048),
-               dict(ko=FAKE, koh=256)):
+               dict(ko=FAKE, koh=256), dict(qoh=0), dict(qot=0), dict(koh=64), dict(kot=120)):
         assert rotary(L, **kw) == INVALID, kw
     for kw in (dict(T=(1 << 20) + 1), dict(hq=1025), dict(hk=1025), dict(D=264), dict(D=132), dict(pairs=4), dict(pairs=60), dict(offset=8), dict(pairs=72),
                dict(offset=4, pairs=56), dict(pairs=1 << 30)):
