@@ -980,12 +980,12 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(AttnArgs a) {
     make_plan(a, s_first, red, a.recs, a.plan, true);
 }
 
-// The parts of cut units, in the order of the cache.  A warp takes 128 dims of a row at a time, by itself (with a row to a CTA and barriers
-// 9,600 rows of two or three parts each took 40 us, this way 8), several parts' loads in flight; where there are no more such
-// jobs than CTAs, the warps of one share its parts (64 rows of 152 parts: 26 us by themselves, 10).
+// The parts of cut units, in the order of the cache.  A warp takes a row by itself (with a row to a CTA and barriers 9,600 rows of two or
+// three parts each took 40 us); where there are fewer, 128 dims of a row, or two, four or eight warps of a CTA take those and share
+// the parts (64 rows of 152 parts: 26 us by single warps, 10).
 constexpr int kJoinWarps = 8;
 template <int L>
-__global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const LatentArgs g, int ctas) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 3) latent_join_kernel(const LatentArgs g, int ctas) {
     constexpr int kCols = L / 128, U = 8, kPer = kMaxAttnCtas / 32;
     __shared__ LatentJoin s_join[kMaxAttnCtas];
     __shared__ int s_end[kMaxAttnCtas];          // rows to join of the CTAs up to this one
@@ -1019,35 +1019,38 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Late
             s_end[kPer * lane + i] = ahead += n[i];
     }
     __syncthreads();
-    const int jobs = s_end[kMaxAttnCtas - 1] * kCols;
-    const bool shared = jobs <= (int)gridDim.x;  // then one job a CTA, or none
-    const int stride = shared ? kJoinWarps : 1;
-    for (int job = shared ? (int)blockIdx.x : blockIdx.x * kJoinWarps + warp; job < jobs; job += gridDim.x * kJoinWarps) {
-        const int i = job / kCols;
+    const int rows = s_end[kMaxAttnCtas - 1];
+    LatentJoin j{0, 0, 0, 0, 0};
+    int r = 0, part = 0, parts = 0;
+    float m = 0.0f, l = 0.0f;
+    auto slot = [&](int k) { return (size_t)(((j.first + k) * 2 + (k == 0)) * g.split + part) * g.cap + r; };
+    // row i: where it is, its reference and sum, the weights of its parts; false where the range-checked build finds it out of range
+    auto find = [&](int i) -> bool {
         int c = 0;                               // whose row it is: CTAs with no more rows up to them
 #pragma unroll
         for (int k = 0; k < kPer; ++k)
             c += __popc(__ballot_sync(0xffffffffu, s_end[32 * k + lane] <= i));
         if (!MOE_DBG_IN_RANGE(c, ctas, g.a.hdr))
-            continue;
-        const LatentJoin j = s_join[c];
-        const int r = i - (c ? s_end[c - 1] : 0), part = g.split == 1 ? 0 : c & 1, parts = j.last - j.first + 1;
+            return false;
+        j = s_join[c];
+        r = i - (c ? s_end[c - 1] : 0);
+        part = g.split == 1 ? 0 : c & 1;
+        parts = j.last - j.first + 1;
         if (!MOE_DBG_IN_RANGE(r, g.cap, g.a.hdr) || !MOE_DBG_IN_RANGE(parts - 1, kMaxAttnCtas, g.a.hdr) ||
             !MOE_DBG_IN_RANGE(j.row + r, (long long)g.p.T * g.p.heads, g.a.hdr))
-            continue;
-        auto slot = [&](int k) { return (size_t)(((j.first + k) * 2 + (k == 0)) * g.split + part) * g.cap + r; };
+            return false;
         float2 e[kPer];
-        float m = -INFINITY;
+        m = -INFINITY;
 #pragma unroll
         for (int q = 0; q < kPer; ++q) {
             const int k = 32 * q + lane;
-            e[q] = k < parts ? __ldcg(g.part_sum + slot(k)) : make_float2(-INFINITY, 0.0f);
+            e[q] = 32 * q < parts && k < parts ? __ldcg(g.part_sum + slot(k)) : make_float2(-INFINITY, 0.0f);
             m = fmaxf(m, e[q].x);
         }
 #pragma unroll
         for (int d = 16; d > 0; d /= 2)
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        float l = 0.0f;
+        l = 0.0f;
         __syncwarp();
 #pragma unroll
         for (int q = 0; q < kPer; ++q) {
@@ -1058,10 +1061,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Late
 #pragma unroll
         for (int d = 16; d > 0; d /= 2)
             l += __shfl_xor_sync(0xffffffffu, l, d);
+        if (l == 0.0f && r >= j.blind)           // it sees positions, and every score left fp32 below
+            l = __uint_as_float(0x7FFFFFFFu);
         __syncwarp();
-        const int d = (job % kCols) * 32 + lane;
+        return true;
+    };
+    // four dims of parts first, + stride, ...
+    auto add = [&](int d, int first, int stride) {
         float4 o = make_float4(0, 0, 0, 0);
-        for (int k0 = shared ? warp : 0; k0 < parts; k0 += U * stride) {
+        for (int k0 = first; k0 < parts; k0 += U * stride) {
             float4 v[U];
             float w[U];
 #pragma unroll
@@ -1079,26 +1087,41 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Late
                 o.w = fmaf(v[u].w, w[u], o.w);
             }
         }
-        if (shared) {
-            s_o[warp][lane] = o;
-            __syncthreads();                     // all of the CTA's warps have the same job
-            if (warp > 0)
-                break;
-#pragma unroll
-            for (int w = 1; w < kJoinWarps; ++w) {
-                const float4 v = s_o[w][lane];
-                o.x += v.x;
-                o.y += v.y;
-                o.z += v.z;
-                o.w += v.w;
-            }
-        }
-        if (l == 0.0f && r >= j.blind)           // it sees positions, and every score left fp32 below
-            l = __uint_as_float(0x7FFFFFFFu);
+        return o;
+    };
+    auto write = [&](int d, float4 o) {
         const float by = l == 0.0f ? 0.0f : 1.0f / l;
         reinterpret_cast<uint2 *>(g.p.out + (j.row + r) * L)[d] = make_uint2(bf16_pair(o.x * by, o.y * by), bf16_pair(o.z * by, o.w * by));
         if (d == 0 && g.p.lse)
             g.p.lse[j.row + r] = l == 0.0f ? -INFINITY : fmaf(m, g.p.scale, logf(l));
+    };
+    const int jobs = rows * kCols;
+    int share = 1;                               // warps of a job of 128 dims; then a CTA has 8 / share of them, once
+    while (share < kJoinWarps && jobs <= (int)gridDim.x * kJoinWarps / (2 * share))
+        share *= 2;
+    if (share == 1) {                            // a row a warp, or 128 dims where that leaves warps without
+        const int cols = 2 * rows >= (int)gridDim.x * kJoinWarps ? kCols : 1;
+        for (int i = blockIdx.x * kJoinWarps + warp; i < jobs / cols; i += gridDim.x * kJoinWarps)
+            if (find(i * cols / kCols))
+                for (int col = i * cols % kCols, k = 0; k < cols; ++k, ++col)
+                    write(col * 32 + lane, add(col * 32 + lane, 0, 1));
+        return;
+    }
+    const int job = blockIdx.x * (kJoinWarps / share) + warp / share, d = job % kCols * 32 + lane;
+    const bool mine_here = job < jobs && find(job / kCols);
+    if (mine_here)
+        s_o[warp][lane] = add(d, warp % share, share);
+    __syncthreads();
+    if (mine_here && warp % share == 0) {
+        float4 o = s_o[warp][lane];
+        for (int w = 1; w < share; ++w) {
+            const float4 v = s_o[warp + w][lane];
+            o.x += v.x;
+            o.y += v.y;
+            o.z += v.z;
+            o.w += v.w;
+        }
+        write(d, o);
     }
 }
 
