@@ -856,7 +856,7 @@ __device__ __forceinline__ void latent_softmax(const LatentArgs &g, const Latent
         soft_sync();                                         // also: s.sum and s.ref have been read
         if (tid == 0) {
             mbar_arrive(s.o_free);
-            if (whole)
+            if (whole && rows > 0)
                 asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\ncp.async.bulk.commit_group;" ::"l"(p.out + out_row * L),
                              "r"(smem_u32(s.q)), "r"((uint32_t)rows * (2 * L))
                              : "memory");
