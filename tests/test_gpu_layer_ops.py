@@ -635,3 +635,47 @@ def test_latent_attention_rows_before_the_first_position_in_a_cut_unit():
     """A request with more new tokens than it has tokens at all, long enough for its units to be cut."""
     Step([900], [1400], 4, 256, 16, seed=41).check()
     Step([130], [135], 2, 512, 64, seed=42).check()
+
+
+def test_calls_on_two_streams_at_once():
+    """Each with a workspace of its own; what they share is the cache, which both read."""
+    one, two = Step([20000, 300], [1, 2], 64, 512, 64, seed=50), Step([9000] * 5, [1] * 5, 96, 512, 16, seed=51)
+    want = [s.run()[0] for s in (one, two)]
+    outs = [torch.empty(s.T, s.heads, s.latent, dtype=torch.bfloat16, device="cuda") for s in (one, two)]
+    args = [(attn.LatentCache(s.data), s.table, i32(s.offsets), i32(s.kv), s.scale, o, None, torch.zeros_like(s.ws)) for s, o in zip((one, two), outs)]
+    x, w = normal(gen(3), 300, 2048), normal(gen(4), 2048)
+    clean, y = torch.empty_like(x), torch.empty_like(x)
+    attn.moe_rms_norm(x, w, 1e-6, clean)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, a, stream in zip((one, two), args, streams):
+            attn.moe_latent_attention(s.ql, s.qr, *a, stream=stream)
+        attn.moe_rms_norm(x, w, 1e-6, y, stream=streams[2])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, v) for o, v in zip(outs, want)) and torch.equal(y, clean)
+    assert all(moe.moe_check_device_status(a[-1]) == 0 for a in args)
+
+
+def test_right_behind_the_kernels_that_make_its_inputs():
+    """Queries, lengths and cache written by the kernels just before, again and again: nothing is read early."""
+    s = Step([700, 64, 1300], [1, 1, 1], 32, 512, 64, seed=52)
+    source, lens = s.data.clone(), i32(s.kv)
+    kv, ql, qr = torch.empty_like(lens), torch.empty(3, 32, 512, dtype=torch.bfloat16, device="cuda"), torch.empty(3, 32, 64, dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")
+    out = [torch.empty(3, 32, 512, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    args = (attn.LatentCache(s.data), s.table, i32(s.offsets))
+    weight, tokens = torch.ones(512, dtype=torch.bfloat16, device="cuda"), normal(gen(9), 3, 576)
+    slots = torch.tensor([int(s.table[b, (k - 1) // 64]) * 64 + (k - 1) % 64 for b, k in enumerate(s.kv)], device="cuda")
+    for i in range(30):
+        for k in range(2):                                 # the second time with a wait in between: the same bits
+            s.data.copy_(source)
+            kv.copy_(lens)
+            attn.moe_rms_norm(s.ql.reshape(96, 512) * (1 + i % 3), weight, 1e-6, ql.view(96, 512))
+            attn.moe_rotary(s.qr.contiguous(), i32([i, 2, 3]), attn.RotaryTable.make(64), qr)
+            attn.moe_latent_append(tokens[:, :512] * (1 + i % 5), tokens[:, 512:], slots, args[0], ws)
+            if k:
+                torch.cuda.synchronize()
+            attn.moe_latent_attention(ql, qr, *args, kv, s.scale, out[k], None, ws)
+        assert torch.equal(out[0], out[1]), i
+    assert moe.moe_check_device_status(ws) == 0
