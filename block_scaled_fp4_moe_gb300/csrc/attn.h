@@ -207,7 +207,8 @@ struct LatentProblem {
     uint16_t *out;
     float *lse;
 };
-size_t latent_attention_workspace(int T, int B, int heads, int latent_dim);
+size_t latent_attention_need(int T, int B, int heads, int latent_dim);           // of this call
+size_t latent_attention_workspace(int T, int B, int heads, int latent_dim);      // of any call of up to T and B
 cudaError_t launch_latent_attention(const LatentProblem &p, void *ws, int sms, cudaStream_t stream);
 
 }  // namespace moe

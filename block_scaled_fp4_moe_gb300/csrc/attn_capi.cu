@@ -321,7 +321,7 @@ moe_status_t moe_latent_attention(const uint16_t *q_latent, int64_t ql_stride_t,
         !aligned(kv_lens, 4) || !aligned(block_table, 4) || ql_stride_t % 8 || ql_stride_h % 8 || qr_stride_t % 8 || qr_stride_h % 8)
         return MOE_ERR_MISALIGNED;
     int sms = 0;
-    if ((st = check_ws(ws, ws_bytes, latent_attention_workspace(T, B, heads, cache->latent_dim))) != MOE_OK || (st = check_device(&sms)) != MOE_OK)
+    if ((st = check_ws(ws, ws_bytes, latent_attention_need(T, B, heads, cache->latent_dim))) != MOE_OK || (st = check_device(&sms)) != MOE_OK)
         return st;
     const LatentProblem p{q_latent, ql_stride_t, ql_stride_h, q_rope, qr_stride_t, qr_stride_h, T, heads, *cache, block_table, max_blocks,
                           q_offsets, kv_lens, B, softmax_scale, causal, out, lse};

@@ -1200,23 +1200,23 @@ int max_units(int T, int B, const Shape &s, int heads) {
 
 struct LatentLayout {
     size_t plan, recs, joins, part, part_sum, total;
-    LatentLayout(int T, int B, int heads, int L) {
-        const Shape s(T, B, heads);
+    LatentLayout(int units, int cap, int L) {
         size_t o = kInitBytes;
         auto take = [&](size_t bytes) { o = align_up(o, 256); size_t r = o; o += bytes; return r; };
         plan = take(sizeof(Plan));
-        recs = take((size_t)max_units(T, B, s, heads) * sizeof(RowTile));
+        recs = take((size_t)units * sizeof(RowTile));
         joins = take(kMaxAttnCtas * sizeof(LatentJoin));
-        part = take((size_t)2 * kMaxAttnCtas * s.cap * L * sizeof(float));       // a CTA has parts of at most two units
-        part_sum = take((size_t)2 * kMaxAttnCtas * s.cap * sizeof(float4));
+        part = take((size_t)2 * kMaxAttnCtas * cap * L * sizeof(float));         // a CTA has parts of at most two units
+        part_sum = take((size_t)2 * kMaxAttnCtas * cap * sizeof(float4));
         total = align_up(o, 256);
     }
+    LatentLayout(int T, int B, const Shape &s, int heads, int L) : LatentLayout(max_units(T, B, s, heads), s.cap, L) {}
 };
 
 template <int L>
 cudaError_t launch(const LatentProblem &p, void *ws, int sms, cudaStream_t stream) {
-    const LatentLayout lay(p.T, p.B, p.heads, L);
     const Shape shape(p.T, p.B, p.heads);
+    const LatentLayout lay(p.T, p.B, shape, p.heads, L);
     int shift = 4;
     while ((1 << shift) < p.cache.block_size)
         ++shift;
@@ -1273,8 +1273,27 @@ cudaError_t launch(const LatentProblem &p, void *ws, int sms, cudaStream_t strea
 
 }  // namespace
 
+size_t latent_attention_need(int T, int B, int heads, int latent_dim) {
+    return T == 0 || B == 0 ? align_up(kInitBytes, 256) : LatentLayout(T, B, Shape(T, B, heads), heads, latent_dim).total;
+}
+
+// Of any step of up to T tokens of up to B requests.  Steps have units of the one shape or the other as they have more tokens than requests
+// or not, and those of a smaller step may be the larger (10 tokens of 4 requests, 16 heads: parts of 64 rows; 64 tokens of 64: 16).  Either
+// shape's units and parts grow with T and with B.
 size_t latent_attention_workspace(int T, int B, int heads, int latent_dim) {
-    return T == 0 || B == 0 ? align_up(kInitBytes, 256) : LatentLayout(T, B, heads, latent_dim).total;
+    if (T == 0 || B == 0)
+        return align_up(kInitBytes, 256);
+    const int t = T < B ? T : B;                  // most tokens of a step of no more tokens than requests
+    const Shape one(t, B, heads);
+    int units = max_units(t, B, one, heads), cap = one.cap;
+    if (T > 1) {                                  // and a step of more has T - 1 requests at most
+        const int b = B < T - 1 ? B : T - 1;
+        const Shape more(T, b, heads);
+        const int n = max_units(T, b, more, heads);
+        units = units > n ? units : n;
+        cap = cap > more.cap ? cap : more.cap;
+    }
+    return LatentLayout(units, cap, latent_dim).total;
 }
 
 cudaError_t launch_latent_attention(const LatentProblem &p, void *ws, int sms, cudaStream_t stream) {

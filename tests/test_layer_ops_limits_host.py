@@ -1,0 +1,27 @@
+"""Norm, rotary positions, latent append and latent attention on the host: sizes and refusals at the ends of what their calls take.  No GPU:
+no pointer is dereferenced."""
+import pytest
+
+from block_scaled_fp4_moe_gb300 import _build, attn
+
+
+@pytest.fixture(scope="module")
+def L():
+    _build.build()
+    return attn.lib()
+
+
+@pytest.mark.parametrize("heads", [1, 15, 16, 17, 64, 65, 96, 128, 129, 256])
+@pytest.mark.parametrize("latent", [256, 512])
+def test_latent_workspace_is_for_every_step_of_up_to_its_sizes(L, heads, latent):
+    """It grows with T and with B, although a step's own units and parts do not."""
+    size = attn.moe_latent_attention_workspace_size
+    tokens = [*range(1, 41), 63, 64, 65, 127, 128, 129, 300, 1000, 5000, 1 << 20]
+    requests = [*range(1, 41), 63, 64, 65, 152, 153, 256, 257, 1000, 8192]
+    tokens = [t for t in tokens if t * heads < 1 << 31]
+    sizes = {(t, b): size(t, b, heads, latent) for t in tokens for b in requests}
+    assert min(sizes.values()) > 0
+    for i, t in enumerate(tokens):
+        for j, b in enumerate(requests):
+            assert i == 0 or sizes[t, b] >= sizes[tokens[i - 1], b], (t, b)
+            assert j == 0 or sizes[t, b] >= sizes[t, requests[j - 1]], (t, b)
