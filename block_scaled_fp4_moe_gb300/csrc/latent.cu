@@ -56,6 +56,7 @@ constexpr int kSoftWarps = 8, kThreads = (kSoftWarps + 3) * 32, kSoft = kSoftWar
 constexpr int kMaxRows = 64;                 // of a CTA's unit
 constexpr int kChunkBytes = kTile * 128;     // 64 dims of a tile
 constexpr int kMaxSlots = 12;                // pairs of chunks in the ring
+constexpr int kMaxSmem = 227 * 1024;         // of a CTA
 constexpr int kRopeSlots = 2;
 constexpr int kSCol = 256;                   // tensor memory: O^T at 64 m, S^T from here
 constexpr float kMostPower = 32.0f;
@@ -103,7 +104,7 @@ struct LatentSmem {
     __host__ __device__ static size_t fixed(int q_rows) { return (size_t)kRopeSlots * kChunkBytes + kChunkBytes + (size_t)q_rows * 128 * kChunks + kTail + 1024; }
     __host__ __device__ static size_t bytes(int q_rows, int slots) { return fixed(q_rows) + (size_t)slots * 2 * kChunkBytes; }
     __host__ static int slots_for(int q_rows) {
-        const int n = (int)((227 * 1024 - fixed(q_rows)) / (2 * kChunkBytes));
+        const int n = (int)((kMaxSmem - fixed(q_rows)) / (2 * kChunkBytes));
         return n < kMaxSlots ? n : kMaxSlots;
     }
     __device__ LatentSmem(uint8_t *base, int q_rows, int slots) {
@@ -1262,8 +1263,8 @@ cudaError_t launch(const LatentProblem &p, void *ws, int sms, cudaStream_t strea
     if (e == cudaSuccess)
         e = encode_tiled(&pair_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.cache.data, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
     const size_t smem = LatentSmem<L>::bytes(g.q_rows, g.slots);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(latent_kernel<L>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess)                                    // a limit of the whole process: the same one from every thread's call
+        e = cudaFuncSetAttribute(latent_kernel<L>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e == cudaSuccess && !g.small)
         e = launch_pdl(latent_plan_kernel, dim3(1), dim3(kPlanThreads), p.B * sizeof(int), stream, g.a);
     if (e == cudaSuccess)

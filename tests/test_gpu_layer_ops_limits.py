@@ -1,9 +1,12 @@
 """Norm, rotary positions, latent append and latent attention at the ends of what their calls take."""
+import ctypes as C
+import threading
+
 import pytest
 import torch
 
 from block_scaled_fp4_moe_gb300 import _build, attn, moe
-from test_gpu_layer_ops import Step
+from test_gpu_layer_ops import Step, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -11,6 +14,41 @@ pytestmark = pytest.mark.gpu
 @pytest.fixture(scope="module", autouse=True)
 def built():
     _build.build()
+
+
+def test_latent_attention_from_two_host_threads():
+    """Each on a stream and a workspace of its own, with head counts whose kernels take different amounts of shared memory.  Through the C
+    ABI, which holds no lock while it launches."""
+    L = attn.lib()
+    steps = [Step([300, 90], [1, 1], 64, 512, 64, seed=71), Step([300, 90], [1, 1], 16, 512, 64, seed=72)]
+    want = [s.run() for s in steps]
+    calls, keep = [], []
+    for s in steps:
+        T, H, out, ws = s.T, s.heads, torch.empty(s.T, s.heads, 512, dtype=torch.bfloat16, device="cuda"), torch.zeros_like(s.ws)
+        offsets, lens, stream = i32(s.offsets), i32(s.kv), torch.cuda.Stream()
+        cache = attn._LatentCache(s.data.data_ptr(), s.data.shape[0], 512, 64)
+        keep.append((out, ws, offsets, lens, stream, cache))
+        args = (s.ql.data_ptr(), s.ql.stride(0), s.ql.stride(1), s.qr.data_ptr(), s.qr.stride(0), s.qr.stride(1), T, H, C.byref(cache), s.table.data_ptr(),
+                s.table.shape[1], offsets.data_ptr(), lens.data_ptr(), 2, s.scale, 1, out.data_ptr(), None, ws.data_ptr(), ws.numel(), stream.cuda_stream)
+        calls.append(lambda args=args: L.moe_latent_attention(*args))
+    torch.cuda.synchronize()
+    statuses = [[], []]
+    start = threading.Barrier(2)
+
+    def go(i):
+        torch.zeros(1, device="cuda")
+        start.wait()
+        for _ in range(4000):
+            statuses[i].append(calls[i]())
+    threads = [threading.Thread(target=go, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert [{v: st.count(v) for v in set(st)} for st in statuses] == [{moe.MOE_OK: 4000}] * 2
+    for k, (out, _) in zip(keep, want):
+        assert torch.equal(k[0], out) and moe.moe_check_device_status(k[1]) == 0
 
 
 @pytest.mark.parametrize("heads,latent", [(16, 512), (96, 256), (5, 512)])
