@@ -400,7 +400,9 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(AppendProb
 cudaError_t launch_kv_tables(const TablesProblem &p, cudaStream_t stream) {
     const size_t smem = (size_t)(3 * p.B + 1) * sizeof(int32_t);
     if (smem > 40 * 1024) {             // 48 KB without asking, of which the kernel's static memory takes its part
-        const cudaError_t e = cudaFuncSetAttribute(kv_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        // a limit of the whole process: the same one from every thread's call
+        const cudaError_t e = cudaFuncSetAttribute(kv_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (3 * kMaxRequests + 1) * (int)sizeof(int32_t));
         if (e != cudaSuccess)
             return e;
     }

@@ -62,3 +62,38 @@ def test_a_workspace_for_many_requests_serves_steps_of_fewer(heads, latent):
         want, want_lse = s.run()
         assert moe.moe_check_device_status(ws) == 0
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+def test_block_tables_from_two_host_threads():
+    """Of 4,000 and of 8,192 requests, whose kernels take different amounts of shared memory; through the C ABI, as above."""
+    L = attn.lib()
+    calls, keep = [], []
+    for B in (4000, 8192):
+        ctx, new, head = i32([17] * B), i32([1] * B), i32([0])
+        free = torch.arange(2 * B, dtype=torch.int32, device="cuda")
+        i = dict(dtype=torch.int32, device="cuda")
+        out = [torch.zeros(B, 2, **i), torch.zeros(B, **i), torch.zeros(B + 1, **i), torch.zeros(B, dtype=torch.int64, device="cuda"), torch.zeros(B, **i),
+               torch.zeros(1, **i)]
+        ws, stream = torch.zeros(512, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()
+        keep.append((ctx, new, head, free, out, ws, stream))
+        args = (ctx.data_ptr(), new.data_ptr(), B, B, 16, free.data_ptr(), 2 * B, head.data_ptr(), out[0].data_ptr(), 2, *[t.data_ptr() for t in out[1:]],
+                ws.data_ptr(), 512, stream.cuda_stream)
+        calls.append(lambda args=args: L.moe_kv_build_tables(*args))
+    torch.cuda.synchronize()
+    statuses = [[], []]
+    start = threading.Barrier(2)
+
+    def go(i):
+        torch.zeros(1, device="cuda")
+        start.wait()
+        for _ in range(4000):
+            statuses[i].append(calls[i]())
+    threads = [threading.Thread(target=go, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert [{v: st.count(v) for v in set(st)} for st in statuses] == [{moe.MOE_OK: 4000}] * 2
+    for ctx, _, _, _, out, ws, _ in keep:
+        assert moe.moe_check_device_status(ws) == 0 and torch.equal(out[1], ctx + 1)
