@@ -1,5 +1,7 @@
 // attn_capi.cu -- the extern "C" boundary of the attention half (moe_attn.h):
 // argument checks and launches.
+#include <mutex>
+
 #include "attn.h"
 
 using namespace moe;
@@ -20,11 +22,29 @@ moe_status_t check_ws(const void *ws, size_t ws_bytes, size_t need) {
     return ws_bytes < need ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
 }
 
+// Tensor maps are made by the driver, which refuses a host thread without a context, as a thread has none before its first CUDA call that
+// needs one.  (A context that is there stays, whoever made it.)
+bool bind_context() {
+    typedef CUresult (*CurrentFn)(CUcontext *);
+    static CurrentFn current = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &p, 12000, cudaEnableDefault, &q) == cudaSuccess && q == cudaDriverEntryPointSuccess)
+            current = reinterpret_cast<CurrentFn>(p);
+    });
+    CUcontext context = nullptr;
+    int dev = 0;
+    return current && current(&context) == CUDA_SUCCESS && (context || (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess));
+}
+
 moe_status_t check_device(int *sms) {
     const moe_status_t st = current_device_sms(sms);
-    if (st == MOE_OK)
-        (void)cudaGetLastError();
-    return st;
+    if (st != MOE_OK)
+        return st;
+    (void)cudaGetLastError();
+    return bind_context() ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status_t check_cache(const moe_kv_cache_t *c) {

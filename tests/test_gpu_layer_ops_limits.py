@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from block_scaled_fp4_moe_gb300 import _build, attn, moe
-from test_gpu_layer_ops import Step, i32
+from test_gpu_layer_ops import Step, gen, i32, normal
 
 pytestmark = pytest.mark.gpu
 
@@ -49,6 +49,53 @@ def test_latent_attention_from_two_host_threads():
     assert [{v: st.count(v) for v in set(st)} for st in statuses] == [{moe.MOE_OK: 4000}] * 2
     for k, (out, _) in zip(keep, want):
         assert torch.equal(k[0], out) and moe.moe_check_device_status(k[1]) == 0
+
+
+@pytest.mark.parametrize("what", ["latent attention", "projection", "projection of few tokens", "attention", "norm", "rotary", "append"])
+def test_a_call_as_the_first_that_a_host_thread_makes(what):
+    """A thread that has no CUDA context yet, as a server's worker that is handed tensors and calls a step."""
+    s = Step([300, 90], [1, 1], 16, 512, 64, seed=73)
+    want, _ = s.run()
+    g = gen(74)
+    x, w = normal(g, 40 if what == "projection" else 2, 512), attn.FP8Weight.from_dense(normal(g, 256, 512))
+    ws, norm = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda"), normal(g, 512)
+    table, pos, slots = attn.RotaryTable.make(64), i32([3, 4]), torch.tensor([0, 1], device="cuda")
+    kv = attn.KVCache.empty(8, 2, 64, 32)
+    for t in (kv.k, kv.v, kv.k_scale, kv.v_scale):
+        t.zero_()
+    heads, block_table, kv_lens = normal(g, 2, 4, 64), i32([[0, 1], [2, 3]]), i32([40, 30])
+    latent = attn.LatentCache(s.data)
+    lens, offsets = i32(s.kv), i32(s.offsets)
+
+    def call():
+        out = torch.zeros_like(want) if what == "latent attention" else torch.zeros(x.shape[0], 256, dtype=torch.bfloat16, device="cuda") if "proj" in what \
+            else torch.zeros_like(heads) if what in ("attention", "rotary") else torch.zeros(8, 32, 576, dtype=torch.bfloat16, device="cuda") if what == "append" \
+            else torch.zeros_like(x)
+        to = attn.LatentCache(out) if what == "append" else None
+        stream = torch.cuda.current_stream()
+        torch.cuda.synchronize()
+        return out, {
+            "latent attention": lambda: attn.moe_latent_attention(s.ql, s.qr, latent, s.table, offsets, lens, s.scale, out, None, ws, stream=stream),
+            "attention": lambda: attn.moe_kv_attention(heads, kv, block_table, offsets, kv_lens, 0.1, out, None, ws, stream=stream),
+            "norm": lambda: attn.moe_rms_norm(x, norm, 1e-6, out, stream=stream),
+            "rotary": lambda: attn.moe_rotary(heads, pos, table, out, stream=stream),
+            "append": lambda: attn.moe_latent_append(want[:, 0], s.qr[:, 0], slots, to, ws, stream=stream),
+        }.get(what, lambda: attn.moe_linear_fp8(x, w, out, ws, stream=stream))
+    want_out, here = call()
+    here()
+    out, there = call()
+    errors = []
+
+    def go():
+        try:
+            there()
+        except Exception as e:                             # noqa: BLE001
+            errors.append(e)
+    t = threading.Thread(target=go)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not errors and torch.equal(out, want_out) and moe.moe_check_device_status(ws) == 0
 
 
 @pytest.mark.parametrize("heads,latent", [(16, 512), (96, 256), (5, 512)])
