@@ -96,6 +96,20 @@ bool real_eps(float eps) { return eps >= 0.0f && eps <= 3.0e38f; }
 
 bool finite(float v) { return v >= -3.0e38f && v <= 3.0e38f; }
 
+// Whether rows of `dim` values of T tokens and `heads` heads, st and sh apart, share no value.
+bool rows_apart(int64_t T, int64_t heads, int64_t dim, int64_t st, int64_t sh) {
+    if ((T > 1 && st < dim) || (heads > 1 && sh < dim))
+        return false;
+    if (T == 1 || heads == 1 || (st - dim) / (heads - 1) >= sh || (sh - dim) / (T - 1) >= st)
+        return true;                             // the usual ones: a token's heads lie before the next token, or a head's tokens before the next head
+    for (int64_t h = 1; h < heads; ++h) {        // h heads on lies between tokens t and t + 1
+        const __int128 at = (__int128)h * sh, t = at / st;
+        if ((t < T && at - t * st < dim) || (t + 1 < T && (t + 1) * st - at < dim))
+            return false;
+    }
+    return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -271,16 +285,15 @@ moe_status_t moe_rotary(const uint16_t *q, int64_t q_stride_t, int64_t q_stride_
         return MOE_OK;
     if (!q || !q_out || !positions || !turns || (k_heads > 0 && (!k || !k_out)))
         return MOE_ERR_INVALID_ARG;
-    // rows of an output lie apart
-    if ((T > 1 && (q_out_stride_t < head_dim || (k_heads > 0 && k_out_stride_t < head_dim))) ||
-        (q_heads > 1 && q_out_stride_h < head_dim) || (k_heads > 1 && k_out_stride_h < head_dim))
-        return MOE_ERR_INVALID_ARG;
     if ((q == q_out && (q_stride_t != q_out_stride_t || q_stride_h != q_out_stride_h)) ||
         (k_heads > 0 && k == k_out && (k_stride_t != k_out_stride_t || k_stride_h != k_out_stride_h)))
         return MOE_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(q_out, 16) || (k_heads > 0 && (!aligned(k, 16) || !aligned(k_out, 16))) || !aligned(positions, 4) ||
         !aligned(turns, 8) || !aligned(q_norm, 16) || (k_heads > 0 && !aligned(k_norm, 16)) || odd)
         return MOE_ERR_MISALIGNED;
+    if (!rows_apart(T, q_heads, head_dim, q_out_stride_t, q_out_stride_h) ||
+        (k_heads > 0 && !rows_apart(T, k_heads, head_dim, k_out_stride_t, k_out_stride_h)))
+        return MOE_ERR_INVALID_ARG;
     int sms = 0;
     const moe_status_t st = check_device(&sms);
     if (st != MOE_OK)

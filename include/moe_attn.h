@@ -180,8 +180,9 @@ moe_status_t moe_rms_norm(const uint16_t *x, int64_t ldx, int T, int H, const ui
  * turns[i] being the pair's frequency in units of 2^-64 turns a position: p turns[i] modulo 2^64 is the exact angle, at any position.
  * With q_norm (k_norm), bf16 [head_dim], a head v is v * rms(v) * norm first, all of its dims; other dims are as they were.
  * fp32, rounded once.  q, q_out bf16, element (t, h, i) at t * stride_t + h * stride_h + i; k the same with k_heads heads (0: none).
- * q_out may be q and k_out k, with the same strides; otherwise outputs overlap no input.  An output's rows lie head_dim or more apart.  A token whose position is negative (as
- * moe_kv_build_tables marks those behind the last) is left out: nothing is written.
+ * q_out may be q and k_out k, with the same strides; otherwise outputs overlap no input.  An output's rows share no value (strides that
+ * would have them do so are refused).  A token whose position is negative (as moe_kv_build_tables marks those behind the last) is left
+ * out: nothing is written.
  * head_dim a multiple of 8 up to 256; pairs and offset multiples of 8, offset + 2 pairs <= head_dim; up to 1024 heads each; T <= 2^20;
  * pointers 16-byte aligned (positions 4, turns 8), strides multiples of 8.
  */

@@ -5,8 +5,9 @@ import threading
 import pytest
 import torch
 
+import layer_ops_reference as ref
 from block_scaled_fp4_moe_gb300 import _build, attn, moe
-from test_gpu_layer_ops import Step, gen, i32, normal
+from test_gpu_layer_ops import Guarded, Step, gen, i32, normal, within
 
 pytestmark = pytest.mark.gpu
 
@@ -144,3 +145,22 @@ def test_block_tables_from_two_host_threads():
     assert [{v: st.count(v) for v in set(st)} for st in statuses] == [{moe.MOE_OK: 4000}] * 2
     for ctx, _, _, _, out, ws, _ in keep:
         assert moe.moe_check_device_status(ws) == 0 and torch.equal(out[1], ctx + 1)
+
+
+@pytest.mark.parametrize("T,heads,st,sh", [(4, 2, 384, 256), (4, 2, 1016, 128), (3, 4, 2048, 512), (2, 3, 128, 256), (5, 3, 136, 1000), (1, 3, 0, 128), (3, 1, 128, 0)])
+def test_rotary_of_outputs_that_lie_between_one_another(T, heads, st, sh):
+    """Any strides by which rows of 128 values share none, and nothing is written between them."""
+    g = gen(T * heads + st)
+    q, pos, table = normal(g, T, heads, 128), torch.arange(T, dtype=torch.int32, device="cuda") * 1000, attn.RotaryTable.make(128)
+    span = (T - 1) * st + (heads - 1) * sh + 128
+    buf = Guarded((span,), torch.bfloat16)
+    out = buf.t.as_strided((T, heads, 128), (st, sh, 1))
+    attn.moe_rotary(q, pos, table, out)
+    buf.check()
+    want, bound = ref.rotary(q, pos, table.turns)
+    within(out, want, bound)
+    rest = torch.ones(span, dtype=torch.bool, device="cuda")
+    for t in range(T):
+        for h in range(heads):
+            rest[t * st + h * sh: t * st + h * sh + 128] = False
+    assert (buf.t[rest].view(torch.uint8) == 0xA5).all()

@@ -3,6 +3,7 @@ no pointer is dereferenced."""
 import pytest
 
 from block_scaled_fp4_moe_gb300 import _build, attn
+from test_layer_ops_host import FAKE, INVALID, rotary
 
 
 @pytest.fixture(scope="module")
@@ -25,3 +26,15 @@ def test_latent_workspace_is_for_every_step_of_up_to_its_sizes(L, heads, latent)
         for j, b in enumerate(requests):
             assert i == 0 or sizes[t, b] >= sizes[tokens[i - 1], b], (t, b)
             assert j == 0 or sizes[t, b] >= sizes[t, requests[j - 1]], (t, b)
+
+
+SHARED = [(128, 128), (128, 256), (128, 504), (1024, 1024), (1 << 60, 1 << 60)]             # strides of tokens and heads, for 2 heads of 128 and more
+SHARED_BY_8 = SHARED + [(256, 128), (1016, 128), (384, 256), (640, 384)]
+
+
+def test_rotary_refuses_outputs_whose_rows_share_values(L):
+    """4 tokens: a row of one of them that is, or reaches into, another's of another head."""
+    for st, sh in SHARED_BY_8:
+        assert rotary(L, qot=st, qoh=sh) == INVALID, (st, sh)
+    for st, sh in SHARED:
+        assert rotary(L, kot=st, koh=sh) == INVALID, (st, sh)
