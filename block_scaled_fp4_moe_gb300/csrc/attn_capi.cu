@@ -255,6 +255,8 @@ moe_status_t moe_rms_norm(const uint16_t *x, int64_t ldx, int T, int H, const ui
     if (!aligned(x, 16) || !aligned(post_weight, 16) || !aligned(gate, 16) || !aligned(residual, 16) || !aligned(residual_out, 16) ||
         !aligned(weight, 16) || !aligned(y, 16) || ldx % 8 || ld_gate % 8)
         return MOE_ERR_MISALIGNED;
+    if (y == x && T > 1 && ldx != H)             // rows of y would lie on other rows of x, which may not have been read
+        return MOE_ERR_INVALID_ARG;
     int sms = 0;
     const moe_status_t st = check_device(&sms);
     if (st != MOE_OK)

@@ -165,7 +165,7 @@ moe_status_t moe_linear_fp8(const uint16_t *x, int64_t ldx, int T, const uint8_t
  * with rms(v) = 1 / sqrt(mean of v^2 + eps).  All in fp32, h for y not rounded first.  x bf16, rows ldx elements apart;
  * post_weight, weight bf16 [H]; gate bf16, rows ld_gate elements apart, or 0 for one row for all tokens; residual and residual_out [T, H]
  * bf16, or fp32 if residual_f32; y bf16 [T, H].  residual, residual_out, gate and post_weight may be NULL; y and weight may
- * be NULL together, if residual_out is given.  residual_out may be residual, y may be x (rows of H).  A row with a value that is not
+ * be NULL together, if residual_out is given.  residual_out may be residual, y may be x where ldx is H (refused otherwise).  A row with a value that is not
  * finite, or whose squares overflow, is as the formulas give it in fp32; no other row is touched by it.
  * H a multiple of 8 up to 32768, T <= 2^20; pointers 16-byte aligned, ldx and ld_gate multiples of 8.
  */

@@ -164,3 +164,21 @@ def test_rotary_of_outputs_that_lie_between_one_another(T, heads, st, sh):
         for h in range(heads):
             rest[t * st + h * sh: t * st + h * sh + 128] = False
     assert (buf.t[rest].view(torch.uint8) == 0xA5).all()
+
+
+def test_norm_over_its_input():
+    """One row, whatever its distance to the next; several where they lie H apart; otherwise a refusal, and nothing is written."""
+    g = gen(76)
+    x, w = normal(g, 5, 272), normal(g, 256)
+    want = torch.empty(5, 256, dtype=torch.bfloat16, device="cuda")
+    attn.moe_rms_norm(x[:, :256], w, 1e-6, want)
+    one = x[2:3].clone()
+    attn.moe_rms_norm(one[:, :256], w, 1e-6, one[:, :256])
+    assert torch.equal(one[0, :256], want[2]) and torch.equal(one[0, 256:], x[2, 256:])
+    near = x[:, :256].contiguous()
+    attn.moe_rms_norm(near, w, 1e-6, near)
+    assert torch.equal(near, want)
+    wide = x.clone()
+    with pytest.raises(moe.MoEError):
+        attn.moe_rms_norm(wide[:, :256], w, 1e-6, wide.view(-1)[:5 * 256].view(5, 256))
+    assert torch.equal(wide, x)

@@ -3,7 +3,7 @@ no pointer is dereferenced."""
 import pytest
 
 from block_scaled_fp4_moe_gb300 import _build, attn
-from test_layer_ops_host import FAKE, INVALID, rotary
+from test_layer_ops_host import ALIGN, INVALID, norm, rotary
 
 
 @pytest.fixture(scope="module")
@@ -38,3 +38,9 @@ def test_rotary_refuses_outputs_whose_rows_share_values(L):
         assert rotary(L, qot=st, qoh=sh) == INVALID, (st, sh)
     for st, sh in SHARED:
         assert rotary(L, kot=st, koh=sh) == INVALID, (st, sh)
+
+
+def test_norm_refuses_y_over_rows_of_x_that_lie_further_apart(L):
+    for kw in (dict(ldx=520), dict(ldx=1024), dict(ldx=520, T=2), dict(ldx=1 << 40, res=0, res_out=0)):
+        assert norm(L, **kw) == INVALID, kw
+    assert norm(L, ldx=516) == ALIGN
