@@ -166,7 +166,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) latent_append_kernel(const 
     if (t >= p.T)
         return;
     const int64_t slot = p.slots[t];
-    if (slot < 0)
+    const int pos = p.turns ? p.positions[t] : 0;
+    if (slot < 0 || pos < 0)                     // positions as in rotary_kernel
         return;
     if (slot >= (int64_t)p.cache.num_blocks * p.cache.block_size) {
         if (lane == 0)
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) latent_append_kernel(const 
     uint16_t a = key[ka], b = key[kb];
     uint16_t *row = p.cache.data + slot * (L + kRopeDims);
     if (p.turns) {
-        const float2 cs = turn_of(p.positions[t], __ldg(p.turns + lane), p.amplitude);
+        const float2 cs = turn_of(pos, __ldg(p.turns + lane), p.amplitude);
         const float x = __uint_as_float((uint32_t)a << 16), y = __uint_as_float((uint32_t)b << 16);
         asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(a) : "f"(x * cs.x - y * cs.y));
         asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(b) : "f"(y * cs.x + x * cs.y));

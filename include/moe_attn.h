@@ -205,8 +205,8 @@ typedef struct {
 /*
  * b7: writes T tokens' latent vectors c (bf16, rows ldc elements apart) and rotary keys k (bf16 [64], rows ldk apart) to the slots
  * slot_map [T] (block * block_size + offset; a negative one is skipped) of the cache.  With norm (bf16 [latent_dim])
- * c * rms(c) * norm is written; with turns (32 of them) k is rotated to positions [T] as b6 does; without, k as it is.  Both NULL or
- * neither of positions and turns.  A slot past the cache is skipped and recorded (MOE_ERR_DEVICE_ASSERT).  Where two tokens
+ * c * rms(c) * norm is written; with turns (32 of them) k is rotated to positions [T] as b6 does, and a token whose position is negative is
+ * left out as there, its latent vector too; without, k as it is.  Both NULL or neither of positions and turns.  A slot past the cache is skipped and recorded (MOE_ERR_DEVICE_ASSERT).  Where two tokens
  * have one slot, either's values may be there afterwards.  T <= 2^24; c, k, norm 16-byte aligned, ldc and ldk multiples of 8.
  * ws: 512 bytes or more.
  */

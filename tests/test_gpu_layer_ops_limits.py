@@ -17,6 +17,31 @@ def built():
     _build.build()
 
 
+@pytest.mark.parametrize("latent", [256, 512])
+@pytest.mark.parametrize("inter", [False, True])
+def test_latent_append_leaves_out_tokens_before_the_first_position(latent, inter):
+    """As moe_rotary does: nothing is written, although their slots are in the cache."""
+    g = gen(70 + latent)
+    pos = [5, -1, 0, -(2 ** 31), 2 ** 31 - 1, -7, 1 << 20]
+    T = len(pos)
+    both = normal(g, T, latent + 64)
+    data = Guarded((2, 16, latent + 64), torch.bfloat16)
+    before, ws = data.t.clone(), torch.zeros(512, dtype=torch.uint8, device="cuda")
+    slots = torch.randperm(32, generator=g, device="cuda")[:T].clone()
+    table = attn.RotaryTable.make(64)
+    attn.moe_latent_append(both[:, :latent], both[:, latent:], slots, attn.LatentCache(data.t), ws, positions=i32(pos), table=table, interleaved=inter)
+    assert moe.moe_check_device_status(ws) == 0
+    data.check()
+    live = i32(pos) >= 0
+    rows, kept = data.t.view(32, -1), before.view(32, -1)
+    want, bound = ref.rotary(both[live][:, None, latent:], i32(pos)[live], table.turns, 1.0, inter)
+    within(rows[slots[live]][:, latent:], want[:, 0], bound[:, 0], "key")
+    assert torch.equal(rows[slots[live]][:, :latent], both[live][:, :latent])
+    rest = torch.ones(32, dtype=torch.bool, device="cuda")
+    rest[slots[live]] = False
+    assert torch.equal(rows[rest].view(torch.int16), kept[rest].view(torch.int16))
+
+
 def test_latent_attention_from_two_host_threads():
     """Each on a stream and a workspace of its own, with head counts whose kernels take different amounts of shared memory.  Through the C
     ABI, which holds no lock while it launches."""
