@@ -197,11 +197,14 @@ class RotaryTable:
 
     @staticmethod
     def make(dims: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0, original_len: int = 0, fast: float = 32.0,
-             slow: float = 1.0, amplitude: float | None = None, device="cuda") -> "RotaryTable":
+             slow: float = 1.0, amplitude: float | None = None, device="cuda", ramp: str = "turns") -> "RotaryTable":
         """A table for ``dims`` rotated dims: pair i turns by base^(-2 i / dims) radians a position.  For contexts ``factor`` times
         as long as a model was trained on, ``scaling`` is "linear" (all frequencies divided by it), "base" (the base enlarged so that the
         slowest pair's is), or "parts" (pairs that turn ``fast`` times or more in ``original_len`` positions as they are, those that
-        turn ``slow`` times or fewer divided, linearly in the turns between; the amplitude is 0.1 ln(factor) + 1 unless one is given)."""
+        turn ``slow`` times or fewer divided; the amplitude is 0.1 ln(factor) + 1 unless one is given).  Between those a frequency
+        is the average of both, its share of the one a straight line in ``ramp``: "turns", how often the pair turns, or "pairs", its
+        index, from the last whole one at or before which a pair would turn ``fast`` times to the first at or after which ``slow`` times.  The
+        two are up to four times apart in the middle: take the one that the weights were trained with."""
         if dims <= 0 or dims % 2 or not base > 0 or not (factor > 0 and math.isfinite(factor)):
             raise ValueError(f"dims {dims}, base {base}, factor {factor}: expected an even number and positive ones")
         if scaling not in (None, "linear", "base", "parts"):
@@ -210,6 +213,13 @@ class RotaryTable:
             raise ValueError("factor: expected with a scaling only")
         if scaling == "parts" and not (original_len > 0 and fast > slow >= 0):
             raise ValueError("scaling by parts: expected original_len > 0 and fast > slow >= 0")
+        if ramp not in ("turns", "pairs"):
+            raise ValueError(f"ramp: expected turns or pairs, got {ramp!r}")
+        if ramp == "pairs":
+            if scaling != "parts" or not (slow > 0 and base > 1):
+                raise ValueError("ramp over pairs: expected scaling by parts, slow > 0 and a base above 1")
+            first, last = (dims * math.log(original_len / (2 * math.pi * n)) / (2 * math.log(base)) for n in (fast, slow))
+            first, last = max(math.floor(first), 0), min(math.ceil(last), dims - 1)
         if scaling == "base":
             if dims < 4:
                 raise ValueError("scaling of the base: expected two pairs or more")
@@ -220,7 +230,8 @@ class RotaryTable:
             if scaling == "linear":
                 f /= factor
             elif scaling == "parts":
-                keep = min(max((original_len * f / (2 * math.pi) - slow) / (fast - slow), 0.0), 1.0)
+                keep = (original_len * f / (2 * math.pi) - slow) / (fast - slow) if ramp == "turns" else (last - i) / max(last - first, 1e-3)
+                keep = min(max(keep, 0.0), 1.0)
                 f = f * keep + f / factor * (1 - keep)
             whole = round(f / (2 * math.pi) * 2.0 ** 64) % (1 << 64)
             turns.append(whole - (1 << 64) if whole >> 63 else whole)
