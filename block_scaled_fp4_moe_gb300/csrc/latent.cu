@@ -35,13 +35,13 @@
 // (one warp for both was often at the scores' when weights were ready: 64 requests of 16,384 tokens, 64 heads, 292 us for 261).  With 64 rows the
 // queries take 72 KB and leave the ring 8 pairs, two tiles; with 16 rows 11.
 //
-// Measured: 64 requests of up to 49,152 tokens, 64 heads, 384 us (6.04 TB/s, 89 % of a copy's rate; a tile takes 1.75 us, 1.66 at that rate).  The
+// Measured: 64 requests of up to 49,152 tokens, 64 heads, 387 us (6.0 TB/s, 88 % of a copy's rate; a tile takes 1.76 us, 1.66 at that rate).  The
 // way of a tile from its copies to the last pair given back takes 3.7 us, two are under way.  152 requests of 8,192, 16 heads, 222 us (6.5 TB/s).
 // Where bytes are shared by more rows, shared memory is next: an MMA of the scores reads 2 KB of the cache and 32 bytes a row in
 // 32 cycles, one of the values 4 KB and 32 bytes a row in 48 (both measured back to back; 24 and 39 with 16 rows): with 64 rows and the tile's arrival
 // 2,500 cycles a tile, 1.2 us.  48 ragged requests of 96 heads, two CTAs to a unit, run at 1.4 us a tile, prompt chunks with 256 dims at
-// 0.72 of 0.69.  One request of 1,000 tokens takes 13.7 us: start and plan 1.5, walk and queries 2, four tiles 5, results 1, the join's start and
-// work 3.5.  Tried: the next tiles asked into L2 by tensor prefetches (no change, 3 % slower with 16 rows).
+// 0.74 of 0.69.  One request of 1,000 tokens takes 14.0 us, steps that wait for one another: start and plan, walk and queries, tiles (16 of
+// them over seven CTAs, three at most; the first CTA's range is the unit's fixed cost), results, the join's start and work.  Tried: the next tiles asked into L2 by tensor prefetches (no change, 3 % slower with 16 rows).
 #define MOE_PLAN_TILE 64
 #define MOE_PLAN_UNIT_COST 3
 #define MOE_PLAN_MIN_COST 3

@@ -9,9 +9,11 @@
 // sum is a few shuffles over the head's lanes (a power of two of them).  A warp has a token and a few sets of heads, whose loads are all
 // in flight before it makes the token's cosines and sines (in shared memory; a lane keeps its eight): no warp waits for another.
 //
-// Bound by memory, 4 bytes a value, and in part by its way there: 4,000 tokens of 48 heads of 128 in 18.0 us (5.5 TB/s), 22 with norms (a warp's
-// sums and the norm's weights).  Before: a CTA a token, with a lane for eight dims and shuffles between halves 37 us; without shuffles 22; CTAs
-// that go from token to token, loads a step ahead, 21.5.  The append: 7,900 tokens of 576 values in 3.9 us (4.7 TB/s; launch and one chain of loads).
+// Bound by memory, 4 bytes a value, and in part by its way there: 4,000 tokens of 48 heads of 128, halves, in 20.0 us (4.9 TB/s), 25.5 with norms
+// (a warp's sums and the norm's weights); neighbours 26 with norms, and 24.4 where half of each head is rotated.  (Three sets of tensors in turn; one set,
+// which L2 holds in part, takes 16.1, and 22.8 with norms.)  Forms before, on tensors that L2 held in part, when this one took 18.0: a CTA a token, with a
+// lane for eight dims and shuffles between halves 37 us; without shuffles 22; CTAs that go from token to token, loads a step ahead, 21.5.
+// The append: 7,900 tokens of 576 values in 4.0 us (4.6 TB/s; launch and one chain of loads).
 #include <type_traits>
 
 #include "attn.h"
@@ -225,10 +227,10 @@ __global__ void __launch_bounds__(kAppendWarps * 32) latent_append_kernel(const 
 cudaError_t launch_rotary(const RotaryProblem &p, int sms, cudaStream_t stream) {
     const int items = p.pairs / 8 + (p.D / 8 - p.pairs / 4 + 1) / 2, lanes = items <= 4 ? 4 : items <= 8 ? 8 : 16;
     const int heads = p.q.heads + p.k.heads, set = 32 / lanes;
-    // Sets of a warp: one while that many warps fit on the GPU at once (64 tokens of 72 heads of 128, 2.6 us; with four, 3.5); else four or three,
-    // as fewer lanes go without a head (4,000 tokens of 48 heads 18.0 and 18.7 us, with two 19.5; 8,192 of 18 heads of 256 43.7 and 32.9).
+    // Sets of a warp: one while that many warps fit on the GPU at once (64 tokens of 72 heads of 128 in a graph, 2.4 us; with four, 2.7); else four or
+    // three, as fewer lanes go without a head (4,000 tokens of 48 heads 20.0 and 21.2 us, with two 22.1; 8,192 of 18 heads of 256 32.4 and 31.0).
     auto waste = [&](int sets) { return (sets * set - heads % (sets * set)) % (sets * set); };
-    const bool norm = p.q.norm || p.k.norm;                // (it takes more registers: 22.1 us with three, 23.7 with four)
+    const bool norm = p.q.norm || p.k.norm;                // (it takes more registers: 25.5 us with three, 27.1 with four)
     const int sets = (int64_t)p.T * heads * lanes <= (int64_t)sms * 512 ? 1 : waste(3) < waste(4) + norm ? 3 : 4;
     const int64_t jobs = (int64_t)p.T * ((heads + sets * set - 1) / (sets * set));
     const dim3 grid((unsigned)((jobs + kRotaryWarps - 1) / kRotaryWarps));

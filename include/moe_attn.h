@@ -215,7 +215,7 @@ moe_status_t moe_latent_append(const uint16_t *c, int64_t ldc, const uint16_t *k
                                const uint16_t *norm, float eps, const moe_latent_cache_t *cache, void *ws, size_t ws_bytes,
                                cudaStream_t stream);
 
-/* Bytes of workspace of moe_latent_attention for up to T new tokens of up to B requests; 0 for sizes that it does not take. */
+/* Bytes of workspace of moe_latent_attention for any step of up to T new tokens of up to B requests; 0 for sizes that it does not take. */
 size_t moe_latent_attention_workspace_size(int T, int B, int heads, int latent_dim);
 
 /*
@@ -229,10 +229,11 @@ size_t moe_latent_attention_workspace_size(int T, int B, int heads, int latent_d
  * what they see (causal or not), rows that see nothing, rows past q_offsets[B], table entries that are not read and device-side errors are as in
  * moe_kv_attention.  What a row does not see has no influence, NaN included; a row that sees a token with a value that is not finite is
  * not finite in those dims at least.  Products are exact, sums and softmax statistics fp32; the weights are
- * rounded to bf16, relative to themselves.  Scores may be of any size that fp32 holds; a row whose largest score leaves that range is NaN.  Latent
+ * rounded to bf16, relative to themselves, and divided by the sum of the rounded ones (lse is of the others).  Scores may be of any size that fp32 holds; a row whose largest score leaves that range is NaN.  Latent
  * values may be of magnitudes up to 2^70.  The same arguments give the same bits on the same device.
  * heads <= 256, B <= 8192, T <= 2^20, T * heads < 2^31; q and out 16-byte aligned, strides multiples of 8; out overlaps no input.  Two
- * launches, or three with many requests.
+ * launches; three where T and B allow more than 152 units of rows (64 rows; where T <= B a token's heads, up to 128), with more than 256 requests,
+ * or with tables of more than 2^29 tokens a request.
  */
 moe_status_t moe_latent_attention(const uint16_t *q_latent, int64_t ql_stride_t, int64_t ql_stride_h, const uint16_t *q_rope,
                                   int64_t qr_stride_t, int64_t qr_stride_h, int T, int heads, const moe_latent_cache_t *cache,
