@@ -318,8 +318,8 @@ def moe_rotary(q, positions, table: RotaryTable, q_out, k=None, k_out=None, inte
 
 def moe_latent_append(c, k, slot_map, cache: LatentCache, ws, positions=None, table: RotaryTable | None = None, interleaved=False,
                       norm=None, eps=1e-6, stream=None):
-    """c bf16 [T, latent_dim] and k bf16 [T, 64], rows may lie further apart; k is rotated where positions and a table are given,
-    c normed where norm is."""
+    """c bf16 [T, latent_dim] and k bf16 [T, 64], rows may lie further apart; k is rotated where positions and a table are given (tokens
+    whose position is negative are left out then), c normed where norm is."""
     turns, amplitude = (None, 1.0) if table is None else (table.turns, table.amplitude)
     st = _native().latent_append(c, k, slot_map, cache.data, ws, positions, turns, amplitude, interleaved, norm, eps, _stream(stream))
     if st:
